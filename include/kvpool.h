@@ -428,6 +428,152 @@ int kvpool_import_layer(kvpool_t* pool, int layer, const void* kq, const void* v
 int kvpool_import_layer_blocks(kvpool_t* pool, int layer, const void* kq, const void* vcodes, const void* vnorm,
                                const void* kscales, const uint8_t* widths, int len, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged private caches. An agent's own tokens (everything behind the shared
+ * context) kept at bf16 in pages of page_tokens tokens, so that agents of very
+ * different lengths share one buffer, fork without copying what they share,
+ * and take chunks of new tokens (a tool's answer, another agent's turn) as
+ * well as single ones. The pages are the caller's memory, as a tail is; the
+ * pager below (host only) says which pages a sequence owns. The recent tokens
+ * stay at native precision, as a tail does (CoMixKV article, incremental
+ * quantisation); the pages of the method describe no paging, this is the
+ * library's own.
+ *
+ * Every call takes its sequences from device arrays, so that a captured graph
+ * replays with the tables and lengths of its time. Page numbers are checked on
+ * the device: a table entry outside [0, pages) is never dereferenced (its
+ * tokens read as zeros, writes to it are dropped) and is recorded in *status.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void* K;          /* bf16 [layers][pages][kv_heads][page_tokens][head_dim], device, 16-byte aligned */
+    void* V;
+    int layers, pages, kv_heads;
+    int page_tokens;  /* 16, 32, 64 or 128 */
+    int head_dim;     /* 64 or 128 */
+    int32_t* status;  /* device word that the kernels OR error bits into (zeroed by the caller), or NULL:
+                         1 a page number out of range, 2 a bounded wait expired; see kvpool_pages_status */
+} kvpool_pages_t;
+
+/* The sequences of one call. Sequence s holds kv_len[s] tokens, this call's
+ * new ones included; its token j is slot j % page_tokens of page
+ * page_table[s * table_stride + j / page_tokens]. The rows [q_start[s],
+ * q_start[s + 1]) of the call's inputs are its new tokens: n of them, the i-th
+ * at position kv_len[s] - n + i. Entries of the table behind a sequence's last
+ * token are not read. Rows from q_start[seqs] on (padding) belong to nobody:
+ * nothing is written for them. */
+typedef struct {
+    int seqs;                  /* >= 1 */
+    int table_stride;          /* table entries per sequence, >= 1 */
+    const int32_t* page_table; /* device [seqs][table_stride] */
+    const int32_t* kv_len;     /* device [seqs] */
+    const int32_t* q_start;    /* device [seqs + 1], q_start[0] = 0, ascending, at most `tokens` */
+    int tokens;                /* rows of the inputs and outputs, >= 1 */
+    int max_q, max_kv;         /* the most new / held tokens of a sequence, as far as the host knows (0:
+                                  tokens / table_stride * page_tokens). They choose kernels and grids,
+                                  never results: a sequence above them is slower, not wrong */
+} kvpool_seqs_t;
+
+/* What a score goes through before the softmax, and which keys a row sees. A
+ * row at position p of sequence s, query head h, key j: x = softmax_scale *
+ * <q, k_j>; cap > 0: x = cap * tanh(x / cap); slopes: x -= slopes[h] * |p - j|.
+ * The row sees j when 0 <= j < kv_len[s], j >= first[row] (document mask: the
+ * first token of the row's document) and (p - window < j <= p, or j <
+ * prefix[s]: a prefix every row of the sequence sees, whole). Keys it does not
+ * see may hold anything, infinities and NaN included. Zeroed: the causal mask
+ * alone. */
+typedef struct {
+    float cap;             /* >= 0; 0: none */
+    int window;            /* >= 0; 0: none; else the last `window` keys, the row's own among them */
+    const float* slopes;   /* device float [q_heads], or NULL */
+    const int32_t* first;  /* device int32 [tokens], or NULL */
+    const int32_t* prefix; /* device int32 [seqs], or NULL */
+} kvpool_score_t;
+
+/* Write the new tokens' K and V of one layer into their slots. K, V: bf16
+ * [tokens][kv_heads][head_dim], device, 16-byte aligned, k_stride / v_stride
+ * elements from one token to the next (a multiple of 8, at least kv_heads *
+ * head_dim: rows of a fused projection may be passed as they are). A page
+ * that two sequences share is written by neither (kvpool_pager_extend gives
+ * the writer a page of its own first). */
+int kvpool_pages_append(const kvpool_pages_t* pages, int layer, const kvpool_seqs_t* seqs, const void* K,
+                        long long k_stride, const void* V, long long v_stride, void* stream);
+
+/* Copy n whole pages, K and V of every layer: page dst[i] becomes page src[i]
+ * (forks, compaction). src, dst: HOST arrays [n], read before the call
+ * returns. No page may be a destination twice, or a destination and a source
+ * (KVPOOL_ERR_INVALID_ARG, nothing is launched); a source may repeat. n = 0 is
+ * a no-op. */
+int kvpool_pages_copy(const kvpool_pages_t* pages, const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* Attention of the new tokens over their sequences' pages (the new tokens' own
+ * K and V already appended), in one softmax per row: single tokens, chunks and
+ * whole prompts in one batch. Q: bf16 [tokens][q_heads][head_dim], device,
+ * 16-byte aligned, q_stride elements from one token to the next (a multiple of
+ * 8, at least q_heads * head_dim); query head h reads KV head h / (q_heads /
+ * kv_heads). score: NULL for the causal mask alone. out: bf16
+ * [tokens][q_heads][head_dim], 16-byte aligned; lse: float [tokens][q_heads],
+ * log sum exp of the row's scores (natural units), or NULL. A row that sees no
+ * key gets out 0 and lse -inf. softmax_scale: 0 means 1/sqrt(head_dim).
+ * Needs no workspace and allocates nothing. */
+int kvpool_pages_attend(const kvpool_pages_t* pages, int layer, const kvpool_seqs_t* seqs, const void* Q,
+                        long long q_stride, int q_heads, const kvpool_score_t* score, void* out, float* lse,
+                        float softmax_scale, void* stream);
+
+/* Synchronise `stream`, then return and clear *pages->status: KVPOOL_OK,
+ * KVPOOL_ERR_INVALID_ARG (a page number was out of range) or
+ * KVPOOL_ERR_TIMEOUT. KVPOOL_ERR_INVALID_ARG too when status is NULL. */
+int kvpool_pages_status(const kvpool_pages_t* pages, void* stream);
+
+/* The pager: which pages each sequence owns. Host only, no device work: its
+ * calls say which pages the caller has to copy (kvpool_pages_copy, on the
+ * stream of the appends, before anything else is asked of the pager or
+ * launched on those pages). Pages are counted: forks share them, and a page
+ * returns to the free ones when its last owner lets go. Always the lowest free
+ * page is taken. Calls of one pager from several threads are the caller's to
+ * serialise. */
+typedef struct kvpool_pager kvpool_pager_t;
+
+/* A pager of `pages` pages of page_tokens tokens (16, 32, 64 or 128). */
+int kvpool_pager_create(kvpool_pager_t** out, int pages, int page_tokens);
+void kvpool_pager_destroy(kvpool_pager_t* pager);
+
+/* A new empty sequence: its number (>= 0; numbers of freed sequences come
+ * back), or a negative error code. */
+int kvpool_pager_new(kvpool_pager_t* pager);
+
+/* Make room for n more tokens at the end of seq. When the last page is partly
+ * filled and shared, the sequence gets a page of its own in its place:
+ * copy[0] (the shared page) has to be copied to copy[1], and 1 is returned; 0
+ * when nothing has to be copied. KVPOOL_ERR_OOM when the free pages do not
+ * suffice (nothing changes). */
+int kvpool_pager_extend(kvpool_pager_t* pager, int seq, int n, int32_t copy[2]);
+
+/* Cut seq to its first len tokens (rejected draft tokens); pages behind them
+ * are let go. */
+int kvpool_pager_truncate(kvpool_pager_t* pager, int seq, int len);
+
+/* A new sequence that holds the same tokens as seq, in the same pages: its
+ * number, or a negative error code. */
+int kvpool_pager_fork(kvpool_pager_t* pager, int seq);
+
+/* End seq: its pages are let go and its number may come back. */
+int kvpool_pager_free(kvpool_pager_t* pager, int seq);
+
+/* Move owned pages from the highest numbers into the lowest free ones, at
+ * most max_pairs of them, until the owned pages are the lowest numbers: page
+ * src[i] has to be copied to dst[i] (host arrays [max_pairs], as for
+ * kvpool_pages_copy); every sequence's table changes with them. Returns the
+ * number of pairs. */
+int kvpool_pager_compact(kvpool_pager_t* pager, int32_t* src, int32_t* dst, int max_pairs);
+
+/* Tokens seq holds; pages seq owns, the first `max` of them written to table
+ * (NULL with max 0: only counted); free pages; owners of a page (0: free).
+ * Negative error codes for what is not there. */
+int kvpool_pager_len(const kvpool_pager_t* pager, int seq);
+int kvpool_pager_table(const kvpool_pager_t* pager, int seq, int32_t* table, int max);
+int kvpool_pager_free_pages(const kvpool_pager_t* pager);
+int kvpool_pager_owners(const kvpool_pager_t* pager, int page);
+
 /* Copy the library's float32 Lloyd-Max table for `bits` (2, 3 or 4) to host
  * arrays: 2^bits centroids (ascending) and 2^bits - 1 midpoints. The library
  * derives it on the host, once, in double precision. */

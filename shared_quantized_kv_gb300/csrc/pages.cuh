@@ -1,0 +1,206 @@
+// What the kernels over paged private caches share: the arguments of a call,
+// which sequence a row belongs to, which keys it sees, and what its scores go
+// through.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <limits.h>
+#include <math_constants.h>
+
+#include "kvpool_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace kvp {
+
+// Bits of kvpool_pages_t.status.
+enum : int { kPgBadPage = 1, kPgTimeout = 2 };
+
+// The pages of one layer and the sequences of one call.
+struct PagedSeqs {
+    int pages, Hk, pshift;  // page_tokens = 1 << pshift
+    int seqs, tstride, tokens;
+    const int32_t* table;
+    const int32_t* kv_len;
+    const int32_t* q_start;
+    int* status;
+};
+
+struct PagedAttend {
+    PagedSeqs s;
+    const uint16_t* K;  // bf16 [pages][Hk][page_tokens][D] of the layer
+    const uint16_t* V;
+    const uint16_t* Q;  // bf16, q_stride elements per token
+    long long q_stride;
+    int Hq, G;
+    float scale_log2;      // softmax scale * log2(e)
+    float cap2, cap_in;    // cap * log2(e); 2 * log2(e) * softmax scale / cap
+    const float* slopes;
+    int window;
+    const int32_t* first;
+    const int32_t* prefix;
+    uint16_t* out;         // bf16 [tokens][Hq][D]
+    float* lse;            // [tokens][Hq] or null
+    // instead of out and lse, the rows' states for a merge with the shared
+    // pool: unnormalised accumulators f32 [tokens][Hq][D] and (m, l), m in log2
+    // units, in slices of st_tokens tokens (the last one shorter), each
+    // [Hk][slice tokens * G][2]
+    float* st_acc;
+    float* st_ml;
+    int st_tokens;
+};
+
+// Does any score modifier apply (else the causal mask alone, which the plain
+// instances of the kernels handle).
+inline bool paged_scored(const PagedAttend& a) {
+    return a.cap2 > 0.0f || a.slopes || a.window > 0 || a.first || a.prefix;
+}
+
+cudaError_t launch_pages_append(const PagedSeqs& s, int head_dim, uint16_t* Kp, uint16_t* Vp, const void* K,
+                                long long k_stride, const void* V, long long v_stride, cudaStream_t st);
+// kinds of attention: max_q, max_kv as in kvpool_seqs_t (never 0 here)
+cudaError_t launch_pages_rows(const PagedAttend& a, int head_dim, int max_q, int max_kv, int sm_count,
+                              cudaStream_t st);
+
+namespace pages {
+
+__device__ __forceinline__ float bf2f(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
+
+__device__ __forceinline__ void flag(int* status, int bit) {
+    if (status) atomicOr(status, bit);
+}
+
+// First row of sequence i: entry i of q_start, held inside [0, tokens].
+__device__ __forceinline__ int row_begin(const PagedSeqs& s, int i) { return min(max(__ldg(s.q_start + i), 0), s.tokens); }
+
+// Tokens that sequence i holds, at most what its table has room for.
+__device__ __forceinline__ int held_tokens(const PagedSeqs& s, int i) {
+    return (int)min((long long)max(__ldg(s.kv_len + i), 0), (long long)s.tstride << s.pshift);
+}
+
+// The rows of all sequences cut into blocks of RB rows (a row: a new token and
+// one of the G query heads of a KV head; a block holds rows of one sequence).
+// Block z: its sequence, its number there, the sequence's first token row q0
+// and new tokens n. False past the last block. Whole warps call it; 32
+// sequences at a time, their loads independent of one another.
+struct RowBlock {
+    int seq, blk, q0, n;
+};
+__device__ __forceinline__ bool find_block(const PagedSeqs& s, int G, int RB, int z, RowBlock& b) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;  // blocks of the sequences before these 32
+    for (int base = 0; base < s.seqs; base += 32) {
+        const int i = base + lane;
+        int q0 = 0, n = 0;
+        if (i < s.seqs) {
+            q0 = row_begin(s, i);
+            n = max(row_begin(s, i + 1) - q0, 0);
+        }
+        const int nb = (int)(((long long)n * G + RB - 1) / RB);
+        int sum = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + sum > z);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            b.seq = base + l;
+            b.q0 = __shfl_sync(0xffffffffu, q0, l);
+            b.n = __shfl_sync(0xffffffffu, n, l);
+            b.blk = z - before - __shfl_sync(0xffffffffu, sum - nb, l);
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return false;
+}
+
+// The keys a row sees: [a1, b1) and [a2, b2) (overlapping or empty as may be).
+struct Seen {
+    int a1, b1, a2, b2;
+    __device__ __forceinline__ bool has(int j) const { return (j >= a1 && j < b1) || (j >= a2 && j < b2); }
+    // every key of [u0, u1)
+    __device__ __forceinline__ bool all(int u0, int u1) const {
+        return (a1 <= u0 && b1 >= u1) || (a2 <= u0 && b2 >= u1);
+    }
+    __device__ __forceinline__ int lo() const { return min(b1 > a1 ? a1 : INT_MAX, b2 > a2 ? a2 : INT_MAX); }
+    __device__ __forceinline__ int hi() const { return max(b1 > a1 ? b1 : 0, b2 > a2 ? b2 : 0); }
+};
+// Row `tok` (of the call) at position pos of sequence seq, which holds T tokens.
+template <bool SCORED>
+__device__ __forceinline__ Seen row_seen(const PagedAttend& a, int seq, int tok, int pos, int T) {
+    Seen r;
+    r.a1 = 0;
+    r.b1 = min(pos + 1, T);
+    r.a2 = r.b2 = 0;
+    if constexpr (SCORED) {
+        const int first = a.first ? max(__ldg(a.first + tok), 0) : 0;
+        r.a1 = a.window > 0 ? (int)max((long long)pos - a.window + 1, (long long)first) : first;
+        if (a.prefix) {
+            r.a2 = first;
+            r.b2 = min(__ldg(a.prefix + seq), T);
+        }
+    }
+    return r;
+}
+
+// <q, k> -> the score in log2 units. tanh(y) = 1 - 2 / (e^(2y) + 1): off by a
+// few units of 2^-24 whatever y, which the cap turns into cap * 2^-22 of a
+// score; the reciprocal of an overflowed e^(2y) is 0, as it should be.
+template <bool SCORED>
+__device__ __forceinline__ float score(const PagedAttend& a, float s, float slope2, int pos, int j) {
+    if constexpr (!SCORED) return s * a.scale_log2;
+    float x = s * a.scale_log2;
+    if (a.cap2 > 0.0f) x = a.cap2 * (1.0f - __fdividef(2.0f, ptx::ex2(s * a.cap_in) + 1.0f));
+    return fmaf(-slope2, (float)abs(pos - j), x);
+}
+
+// One row over the keys it sees among [t0, t1) whose 16-token unit number is u0
+// modulo us, with nothing that it does not see touching the result: the slow
+// path of rows whose sums came out infinite or NaN, which a matrix product
+// gives for 0 * NaN where a masked key's V is not finite. One warp; lane holds
+// D / 32 consecutive channels of acc.
+template <int D, bool SCORED>
+__device__ __noinline__ void careful_row(const PagedAttend& a, int seq, int tok, int head, int pos, const Seen& see,
+                                         int t0, int t1, int u0, int us, float& m, float& l, float (&acc)[D / 32]) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const PagedSeqs& s = a.s;
+    const int g = head / a.G;
+    const float slope2 = SCORED && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.0f;
+    float q[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[e] = bf2f(a.Q[(long long)tok * a.q_stride + (long long)head * D + lane * E + e]);
+    m = -CUDART_INF_F;
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int j = t0; j < t1; ++j) {
+        if ((j >> 4) % us != u0 || !see.has(j)) continue;
+        const int page = __ldg(s.table + (long long)seq * s.tstride + (j >> s.pshift));
+        const bool ok = page >= 0 && page < s.pages;
+        const long long at =
+            ((((long long)(ok ? page : 0) * s.Hk + g) << s.pshift) + (j & ((1 << s.pshift) - 1))) * D + lane * E;
+        float dot = 0.0f, v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            dot = fmaf(q[e], ok ? bf2f(a.K[at + e]) : 0.0f, dot);
+            v[e] = ok ? bf2f(a.V[at + e]) : 0.0f;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        const float x = score<SCORED>(a, dot, slope2, pos, j);
+        const float mn = fmaxf(m, x), ref = mn == -CUDART_INF_F ? 0.0f : mn;
+        const float c = l == 0.0f ? 0.0f : ptx::ex2(m - ref), w = ptx::ex2(x - ref);
+        l = l == 0.0f ? w : fmaf(l, c, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e] * c);
+        m = mn;
+    }
+    if (m == -CUDART_INF_F && l != 0.0f) m = 0.0f;  // NaN scores alone: keep them
+    if (l == 0.0f) m = -CUDART_INF_F;
+}
+
+}  // namespace pages
+}  // namespace kvp

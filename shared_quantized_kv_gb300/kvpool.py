@@ -32,6 +32,23 @@ class Tail(ctypes.Structure):
                 ("T_max", ctypes.c_int)]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("layers", ctypes.c_int), ("pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("page_tokens", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("status", ctypes.c_void_p)]
+
+
+class Seqs(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int), ("table_stride", ctypes.c_int), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("tokens", ctypes.c_int),
+                ("max_q", ctypes.c_int), ("max_kv", ctypes.c_int)]
+
+
+class Score(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("window", ctypes.c_int), ("slopes", ctypes.c_void_p),
+                ("first", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
 class LayerView(ctypes.Structure):
     _fields_ = [("kq", ctypes.c_void_p), ("vcodes", ctypes.c_void_p), ("vnorm", ctypes.c_void_p),
                 ("kscale", ctypes.c_void_p), ("ctx", ctypes.c_int), ("ctx_padded", ctypes.c_int),
@@ -97,6 +114,27 @@ _SIGS = {
                                              ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float,
                                              ctypes.c_void_p]),
+    "kvpool_pages_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_longlong, ctypes.c_void_p, ctypes.c_longlong,
+                                           ctypes.c_void_p]),
+    "kvpool_pages_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_void_p]),
+    "kvpool_pages_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p]),
+    "kvpool_pages_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "kvpool_pager_create": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int, ctypes.c_int]),
+    "kvpool_pager_destroy": (None, [ctypes.c_void_p]),
+    "kvpool_pager_new": (ctypes.c_int, [ctypes.c_void_p]),
+    "kvpool_pager_extend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "kvpool_pager_truncate": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int]),
+    "kvpool_pager_fork": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int]),
+    "kvpool_pager_free": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int]),
+    "kvpool_pager_compact": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int]),
+    "kvpool_pager_len": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int]),
+    "kvpool_pager_table": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int]),
+    "kvpool_pager_free_pages": (ctypes.c_int, [ctypes.c_void_p]),
+    "kvpool_pager_owners": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int]),
     "kvpool_strerror": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -208,6 +246,202 @@ def allocate_bits(sens, cost, budget):
     _check(_lib().kvpool_allocate_bits(L, s.ctypes.data, c.ctypes.data, int(budget), out.ctypes.data),
            "kvpool_allocate_bits")
     return [int(b) for b in out]
+
+
+# ------------------------------------------------------- paged private caches
+
+class Pager:
+    """Which pages each sequence owns (a ``kvpool_pager_t``; host only)."""
+
+    def __init__(self, pages, page_tokens):
+        h = ctypes.c_void_p()
+        _check(_lib().kvpool_pager_create(ctypes.byref(h), pages, page_tokens), "kvpool_pager_create")
+        self._h, self.pages, self.page_tokens = h, pages, page_tokens
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _lib().kvpool_pager_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @staticmethod
+    def _count(n, what):
+        """n of a call that returns a count or a negative error code."""
+        _check(min(0, n), what)
+        return n
+
+    def new(self) -> int:
+        """A new empty sequence's number."""
+        return self._count(_lib().kvpool_pager_new(self._h), "kvpool_pager_new")
+
+    def extend(self, seq, n):
+        """Room for n more tokens: None, or the (shared page, own page) pair
+        that has to be copied before they are written."""
+        pair = (ctypes.c_int32 * 2)()
+        due = self._count(_lib().kvpool_pager_extend(self._h, seq, n, pair), "kvpool_pager_extend")
+        return (pair[0], pair[1]) if due else None
+
+    def truncate(self, seq, length):
+        """Cut a sequence to its first `length` tokens."""
+        _check(_lib().kvpool_pager_truncate(self._h, seq, length), "kvpool_pager_truncate")
+
+    def fork(self, seq) -> int:
+        """A new sequence that shares all pages of seq."""
+        return self._count(_lib().kvpool_pager_fork(self._h, seq), "kvpool_pager_fork")
+
+    def free(self, seq):
+        """End a sequence."""
+        _check(_lib().kvpool_pager_free(self._h, seq), "kvpool_pager_free")
+
+    def compact(self):
+        """Owned pages become the lowest numbers: lists (src, dst) of the page copies due."""
+        src, dst = (ctypes.c_int32 * self.pages)(), (ctypes.c_int32 * self.pages)()
+        n = self._count(_lib().kvpool_pager_compact(self._h, src, dst, self.pages), "kvpool_pager_compact")
+        return list(src[:n]), list(dst[:n])
+
+    def length(self, seq) -> int:
+        return self._count(_lib().kvpool_pager_len(self._h, seq), "kvpool_pager_len")
+
+    def table(self, seq):
+        """The sequence's pages in order (list of int)."""
+        n = self._count(_lib().kvpool_pager_table(self._h, seq, None, 0), "kvpool_pager_table")
+        buf = (ctypes.c_int32 * max(n, 1))()
+        self._count(_lib().kvpool_pager_table(self._h, seq, buf, n), "kvpool_pager_table")
+        return list(buf[:n])
+
+    def free_pages(self) -> int:
+        return self._count(_lib().kvpool_pager_free_pages(self._h), "kvpool_pager_free_pages")
+
+    def owners(self, page) -> int:
+        """Sequences that own the page (0: free)."""
+        return self._count(_lib().kvpool_pager_owners(self._h, page), "kvpool_pager_owners")
+
+
+def _one_device(*named):
+    """The tensors given, in order, are on the current CUDA device."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and (t.device.type != "cuda" or t.device.index != dev):
+            raise ValueError(f"{name} must be on the current CUDA device ({dev}), not {t.device}")
+
+
+def _pages(K_pages, V_pages, status=None):
+    import torch
+
+    if K_pages.dim() != 5 or V_pages.shape != K_pages.shape:
+        raise ValueError("K_pages and V_pages must be [layers, pages, kv_heads, page_tokens, head_dim]")
+    L, n, hk, P, d = K_pages.shape
+    kp, vp = _dev_ptr(K_pages, torch.bfloat16, "K_pages"), _dev_ptr(V_pages, torch.bfloat16, "V_pages")
+    _one_device(("K_pages", K_pages), ("V_pages", V_pages), ("status", status))
+    return Pages(kp.value, vp.value, L, n, hk, P, d, None if status is None else
+                 _dev_ptr(status, torch.int32, "status").value)
+
+
+def _seqs(table, kv_len, q_start, tokens, max_q, max_kv):
+    import torch
+
+    if table.dim() != 2 or kv_len.shape != (table.shape[0],) or q_start.shape != (table.shape[0] + 1,):
+        raise ValueError("table [seqs, pages], kv_len [seqs] and q_start [seqs + 1] do not fit together")
+    _one_device(("table", table), ("kv_len", kv_len), ("q_start", q_start))
+    return Seqs(table.shape[0], table.shape[1], _dev_ptr(table, torch.int32, "table").value,
+                _dev_ptr(kv_len, torch.int32, "kv_len").value, _dev_ptr(q_start, torch.int32, "q_start").value, tokens,
+                int(max_q or 0), int(max_kv or 0))
+
+
+def _token_rows(t, name, heads, d):
+    """Pointer and token stride of a bf16 [tokens, heads, d] tensor whose heads lie together."""
+    import torch
+
+    if t.dim() != 3 or t.shape[1:] != (heads, d) or t.dtype != torch.bfloat16 or not t.is_cuda or \
+            t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be a bf16 CUDA tensor [tokens, {heads}, {d}] whose heads lie together")
+    _one_device((name, t))
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def pages_append(K_pages, V_pages, layer, K, V, table, kv_len, q_start, status=None, stream=None):
+    """Write new tokens into their pages (kvpool_pages_append). K_pages,
+    V_pages: bf16 [layers, pages, kv_heads, page_tokens, d]; K, V: bf16
+    [tokens, kv_heads, d], rows of a fused projection as they are; table int32
+    [seqs, pages of a sequence], kv_len int32 [seqs] (the new tokens included),
+    q_start int32 [seqs + 1]: sequence s's new tokens are rows q_start[s] ...
+    q_start[s + 1] - 1. status: None or an int32 [1] word that records page
+    numbers out of range. All on the current device."""
+    pg = _pages(K_pages, V_pages, status)
+    if V.shape != K.shape:
+        raise ValueError("K and V must have the same shape")
+    kp, ks = _token_rows(K, "K", pg.kv_heads, pg.head_dim)
+    vp, vs = _token_rows(V, "V", pg.kv_heads, pg.head_dim)
+    sq = _seqs(table, kv_len, q_start, K.shape[0], 0, 0)
+    _check(_lib().kvpool_pages_append(ctypes.byref(pg), layer, ctypes.byref(sq), kp, ks, vp, vs, _stream_ptr(stream)),
+           "kvpool_pages_append")
+
+
+def pages_copy(K_pages, V_pages, src, dst, stream=None):
+    """Page dst[i] of every layer becomes page src[i] (kvpool_pages_copy);
+    src, dst: lists of int. No page twice a destination, or both."""
+    n = len(src)
+    if len(dst) != n:
+        raise ValueError("src and dst must have the same length")
+    arr = ctypes.c_int32 * max(n, 1)
+    pg = _pages(K_pages, V_pages)
+    _check(_lib().kvpool_pages_copy(ctypes.byref(pg), arr(*src), arr(*dst), n, _stream_ptr(stream)),
+           "kvpool_pages_copy")
+
+
+def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=None, cap=0.0, slopes=None,
+                 window=0, first=None, prefix=None, out=None, lse=None, return_lse=False, softmax_scale=0.0, status=None,
+                 stream=None):
+    """Attention of the new tokens over their sequences' pages
+    (kvpool_pages_attend): Q bf16 [tokens, q_heads, d]; pages, table, kv_len,
+    q_start as for pages_append. max_q, max_kv: the most new and held tokens of
+    a sequence where the caller knows them (they choose kernels, not results).
+    Scores: cap (x = cap tanh(x / cap)), slopes float32 [q_heads] (minus slope
+    times distance), window (the last keys up to the row's own), first int32
+    [tokens] (document mask), prefix int32 [seqs] (keys every row sees).
+    Returns out bf16 [tokens, q_heads, d], or (out, lse float32 [tokens,
+    q_heads]) with return_lse or an lse to write to. A row that sees no key
+    gets 0 and -inf; rows behind the last sequence are left as they are."""
+    import torch
+
+    pg = _pages(K_pages, V_pages, status)
+    if Q.dim() != 3:
+        raise ValueError("Q must be [tokens, q_heads, head_dim]")
+    n, hq, d = Q.shape
+    qp, qs = _token_rows(Q, "Q", hq, pg.head_dim)
+    sq = _seqs(table, kv_len, q_start, n, max_q, max_kv)
+    for name, t, shape in (("slopes", slopes, (hq,)), ("first", first, (n,)), ("prefix", prefix, (sq.seqs,)),
+                           ("out", out, (n, hq, d)), ("lse", lse, (n, hq))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}")
+    _one_device(("slopes", slopes), ("first", first), ("prefix", prefix), ("out", out), ("lse", lse))
+    sc = None
+    if cap or window or slopes is not None or first is not None or prefix is not None:
+        ptr = lambda t, dt, name: None if t is None else _dev_ptr(t, dt, name).value
+        sc = ctypes.byref(Score(cap, window, ptr(slopes, torch.float32, "slopes"), ptr(first, torch.int32, "first"),
+                                ptr(prefix, torch.int32, "prefix")))
+    if out is None or (return_lse and lse is None):
+        # on the stream that writes them, so that the allocator knows it
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=Q.device)
+            if return_lse and lse is None:
+                lse = torch.empty((n, hq), dtype=torch.float32, device=Q.device)
+    _check(_lib().kvpool_pages_attend(ctypes.byref(pg), layer, ctypes.byref(sq), qp, qs, hq, sc,
+                                      _dev_ptr(out, torch.bfloat16, "out"), _dev_ptr(lse, torch.float32, "lse"),
+                                      softmax_scale, _stream_ptr(stream)), "kvpool_pages_attend")
+    return out if lse is None else (out, lse)
 
 
 class KVPool:
