@@ -211,6 +211,11 @@ cudaError_t launch_sensitivity(const void* Q, int agents, int q_heads, int kv_he
 // Mean squared error of the library's Lloyd-Max quantiser for N(0,1).
 double lm_distortion(int bits);
 
+// TMA map of `rows` rows of D bf16 values (pages of one layer); boxes of 64
+// values x box_rows rows land with the 128-byte swizzle. False without a
+// driver that encodes it.
+bool make_page_map(CUtensorMap* map, const void* base, int D, long long rows, int box_rows);
+
 // Largest V norm of a layer (for layers loaded with kvpool_import_layer).
 cudaError_t launch_norm_max(const Shape& s, const LayerBufs& L, cudaStream_t st);
 

@@ -295,7 +295,9 @@ int kvpool_pages_attend(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t
     const long long room = (long long)seqs->table_stride * pg->page_tokens;
     const int max_kv = (int)std::min<long long>(seqs->max_kv > 0 ? std::min<long long>(seqs->max_kv, room) : room, 1LL << 30);
     const int max_q = seqs->max_q > 0 ? std::min(seqs->max_q, seqs->tokens) : seqs->tokens;
-    return map_cuda(kvp::launch_pages_rows(a, pg->head_dim, max_q, max_kv, sms, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((long long)max_q * group > 16) return map_cuda(kvp::launch_pages_chunk(a, pg->head_dim, max_kv, sms, st));
+    return map_cuda(kvp::launch_pages_rows(a, pg->head_dim, max_q, max_kv, sms, st));
 }
 
 int kvpool_pages_status(const kvpool_pages_t* pg, void* stream) {

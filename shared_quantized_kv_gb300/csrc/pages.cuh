@@ -57,9 +57,11 @@ inline bool paged_scored(const PagedAttend& a) {
 
 cudaError_t launch_pages_append(const PagedSeqs& s, int head_dim, uint16_t* Kp, uint16_t* Vp, const void* K,
                                 long long k_stride, const void* V, long long v_stride, cudaStream_t st);
-// kinds of attention: max_q, max_kv as in kvpool_seqs_t (never 0 here)
+// The two kinds of attention (pages_rows.cu: few rows per sequence;
+// pages_chunk.cu: many); max_q, max_kv as in kvpool_seqs_t, but never 0.
 cudaError_t launch_pages_rows(const PagedAttend& a, int head_dim, int max_q, int max_kv, int sm_count,
                               cudaStream_t st);
+cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_kv, int sm_count, cudaStream_t st);
 
 namespace pages {
 
@@ -156,14 +158,15 @@ __device__ __forceinline__ float score(const PagedAttend& a, float s, float slop
     return fmaf(-slope2, (float)abs(pos - j), x);
 }
 
-// One row over the keys it sees among [t0, t1) whose 16-token unit number is u0
-// modulo us, with nothing that it does not see touching the result: the slow
+// One row over the keys j it sees among [t0, t1) with (j >> sh) % us == u0,
+// with nothing that it does not see touching the result: the slow
 // path of rows whose sums came out infinite or NaN, which a matrix product
 // gives for 0 * NaN where a masked key's V is not finite. One warp; lane holds
 // D / 32 consecutive channels of acc.
 template <int D, bool SCORED>
 __device__ __noinline__ void careful_row(const PagedAttend& a, int seq, int tok, int head, int pos, const Seen& see,
-                                         int t0, int t1, int u0, int us, float& m, float& l, float (&acc)[D / 32]) {
+                                         int t0, int t1, int sh, int u0, int us, float& m, float& l,
+                                         float (&acc)[D / 32]) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const PagedSeqs& s = a.s;
@@ -177,7 +180,7 @@ __device__ __noinline__ void careful_row(const PagedAttend& a, int seq, int tok,
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
     for (int j = t0; j < t1; ++j) {
-        if ((j >> 4) % us != u0 || !see.has(j)) continue;
+        if ((j >> sh) % us != u0 || !see.has(j)) continue;
         const int page = __ldg(s.table + (long long)seq * s.tstride + (j >> s.pshift));
         const bool ok = page >= 0 && page < s.pages;
         const long long at =

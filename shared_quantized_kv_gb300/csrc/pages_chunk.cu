@@ -1,0 +1,610 @@
+// Attention of many query rows per sequence over its pages: chunks of new
+// tokens, whole prompts (sm_103a, tcgen05).
+//
+// Mathematics as in pages_rows.cu: one pass over the keys, a running reference
+// maximum that moves when the maximum passes it by more than 2^8, p = 2^(x - m)
+// rounded to bf16 for the product with V (2^-9 of each weight on average less,
+// against the output's own rounding to bf16), l = sum p in float32.
+//
+// Bound: the tensor cores, 4 D FLOP per (row, key). A CTA has up to 256 rows
+// (new tokens x heads of a group) of one sequence and KV head, as two tiles of
+// 128, and walks the keys in tiles of 128. Two slots of tensor memory, each
+// with S (128 columns; P, its bf16 weights, overwrites it) and O (D columns),
+// are worked on in turn: while the tensor cores do P V and the next Q K^T of
+// one slot, the four softmax warps of the other turn its S into P. With more
+// than 128 rows the slots are the two row tiles, and each K and V tile serves
+// both; with fewer, both slots have the same rows and take every second key
+// tile, and their states are merged at the end.
+//   warp 0        loader: pages by TMA, one box of 64 channels per page, K and
+//                 V tiles through one ring in the order they are needed
+//   warp 1        issuer of the MMAs (one lane)
+//   warps 4-11    softmax, a thread per row of its slot
+// S_{i+1} of a slot may overwrite P_i because the MMAs of a thread run in the
+// order they are issued. V comes as [key][channel], which the MMA takes as an
+// MN-major operand. The keys may be split over the CTAs of a cluster, whose
+// states meet in distributed shared memory: no workspace, no second launch.
+// Every wait is bounded; one that expires is recorded in the status word, and
+// the CTA runs to its end without waiting again.
+#include <algorithm>
+
+#include "pages.cuh"
+
+namespace kvp {
+namespace {
+
+using pages::Seen;
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;              // keys per tile, rows per slot
+constexpr int kRows = 2 * kTile;        // rows per CTA
+constexpr float kLazyMax = 8.0f;        // log2 units the reference may trail the maximum
+constexpr int kMaxSplit = 8;
+constexpr uint64_t kWaitNs = 200ull * 1000 * 1000;
+constexpr uint32_t kCols = 512;         // tensor memory: S0, S1, O0, O1
+constexpr uint32_t kBarQ = 1;           // named barrier: issuer and softmax warps (Q staged)
+// registers: 3 warpgroups launched with 168 each; 88 + 2 x 208 = 3 x 168
+constexpr int kRegsFew = 88, kRegsMany = 208;
+
+template <int D>
+struct Lay {
+    static constexpr int stage = kTile * D * 2;  // a K or V tile
+    static constexpr int nst = D == 128 ? 5 : 10;
+    static constexpr int ring = 2 * stage;       // after the two Q tiles
+    static constexpr int bars = ring + nst * stage;
+    static constexpr int nbars = 2 * nst + 2 + 2 + 2 + 1;
+    static constexpr int info = bars + nbars * 8;  // rng[2][2], tensor memory address
+    static constexpr int total = info + 32 + 1024;  // + alignment of the base
+    static constexpr int rs = D + 4;             // floats of a merge row: O, m, l
+    static_assert(kRows * rs * 4 <= bars, "merge rows fit in the tiles");
+    static_assert(total <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float asf(uint32_t u) { return __uint_as_float(u); }
+__device__ __forceinline__ uint32_t asu(float f) { return __float_as_uint(f); }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < CUDART_INF_F; }
+
+// ring entries of tile i's K and V, of n tiles: K0 K1 V0 K2 V1 K3 ...
+__device__ __forceinline__ int k_entry(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int v_entry(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool& bad) {
+    bool ok = bad || ptx::mbar_wait(bar, parity, kWaitNs);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) bad = true;
+    return ok;
+}
+
+// bits k of [32 c, 32 c + 32) with a <= 32 c + k < b
+__device__ __forceinline__ uint32_t span_bits(int a, int b, int c) {
+    const int x = min(max(a - 32 * c, 0), 32), y = min(max(b - 32 * c, 0), 32);
+    if (y <= x) return 0u;
+    const uint32_t upto = y == 32 ? 0xffffffffu : (1u << y) - 1u;
+    return upto & ~(x == 32 ? 0xffffffffu : (1u << x) - 1u);
+}
+
+template <int D, bool SCORED>
+__global__ void __launch_bounds__(kThreads, 1)
+pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const PagedAttend p) {
+    using L = Lay<D>;
+    constexpr uint32_t kColS = 0, kColO = 256;  // slot w: 128 w columns on
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const PagedSeqs& s = p.s;
+    const int S = (int)ptx::cluster_size(), rank = (int)ptx::cluster_rank();
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+    // blocks of a sequence from its last (the one that sees most) to its first
+    const int job = blockIdx.x / S, g = job % s.Hk;
+    pages::RowBlock b;
+    if (!pages::find_block(s, p.G, kRows, job / s.Hk, b)) return;  // the whole cluster's
+    const int T = pages::held_tokens(s, b.seq);
+    const int nblk = (b.n * p.G + kRows - 1) / kRows;
+    const int r_begin = (nblk - 1 - b.blk) * kRows;
+    const int nr = min(kRows, b.n * p.G - r_begin);
+    const bool two = nr > kTile;  // two row tiles, or one in both slots
+
+    const uint32_t b_full = ptx::smem_u32(sm + L::bars), b_empty = b_full + 8 * L::nst;
+    const uint32_t b_s = b_empty + 8 * L::nst, b_p = b_s + 16, b_o = b_p + 16, b_fin = b_o + 16;
+    int* rng = reinterpret_cast<int*>(sm + L::info);  // [slot] {first key seen, end of the keys seen}
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(rng + 4);
+    if (tid == 0) {
+        for (int i = 0; i < L::nst; ++i) {
+            ptx::mbar_init(b_full + 8 * i, 1);
+            ptx::mbar_init(b_empty + 8 * i, 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            ptx::mbar_init(b_s + 8 * w, 1);
+            ptx::mbar_init(b_p + 8 * w, 4);
+            ptx::mbar_init(b_o + 8 * w, 1);
+            rng[2 * w] = INT_MAX;
+            rng[2 * w + 1] = 0;
+        }
+        ptx::mbar_init(b_fin, 1);
+        ptx::mbar_init_fence();
+    }
+    if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tslot), kCols);
+    __syncthreads();
+
+    // softmax threads: their row and what it sees
+    const int w = (warp - 4) / 4;          // slot
+    const int lr = tid & 127;              // row of the slot
+    const int row = two ? w * kTile + lr : lr;
+    const bool live = warp >= 4 && row < nr;
+    Seen see = {0, INT_MAX, 0, 0};  // rows past the block: Q is 0, nothing to mask, dropped at the end
+    int tok = 0, head = 0, pos = 0;
+    if (live) {
+        const int i = (r_begin + row) / p.G;
+        tok = b.q0 + i;
+        head = g * p.G + (r_begin + row) - i * p.G;
+        pos = T - b.n + i;
+        see = pages::row_seen<SCORED>(p, b.seq, tok, pos, T);
+    }
+    if (warp >= 4) {
+        const int lo = __reduce_min_sync(0xffffffffu, live ? see.lo() : INT_MAX);
+        const int hi = __reduce_max_sync(0xffffffffu, live ? see.hi() : 0);
+        if (lane == 0 && hi > 0) {
+            atomicMin(&rng[2 * w], lo);
+            atomicMax(&rng[2 * w + 1], hi);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tslot;
+
+    // this CTA's key tiles [ta, ta + n): the cluster's share of the tiles that
+    // any row sees; slot w takes the first nt[w] of them (two row tiles), or
+    // every second one
+    const int hi = max(rng[1], rng[3]);
+    const int t_lo = hi > 0 ? min(rng[0], rng[2]) / kTile : 0, t_hi = (hi + kTile - 1) / kTile;
+    const int per = (t_hi - t_lo + S - 1) / S;
+    const int ta = t_lo + rank * per;
+    const int n = max(0, min(t_hi, ta + per) - ta);
+    auto tiles_of = [&](int slot) {
+        if (!two) return (n - slot + 1) / 2;
+        return max(0, min(n, (rng[2 * slot + 1] + kTile - 1) / kTile - ta));
+    };
+    bool bad = false;
+
+    if (warp < 4) {
+        ptx::regs_dec<kRegsFew>();
+        if (warp == 0) {
+            // ------------------------------------------------------- loader
+            const int P = 1 << s.pshift, np = kTile >> s.pshift;  // pages per tile
+            const int32_t* table = s.table + (long long)b.seq * s.tstride;
+            const int none = s.pages * (s.Hk << s.pshift);  // a row behind the last: reads as zeros
+            // first token row of this lane's page of tile i, -1 for none
+            auto page_row = [&](int i) {
+                const int t = (ta + i) * kTile + lane * P;
+                if (i >= n || lane >= np || t >= T) return -1;
+                const int page = __ldg(table + (t >> s.pshift));
+                if (page < 0 || page >= s.pages) {
+                    pages::flag(s.status, kPgBadPage);
+                    return none;
+                }
+                return (page * s.Hk + g) << s.pshift;
+            };
+            auto load = [&](int e, int r, const CUtensorMap* map) {
+                const int st = e % L::nst;
+                const uint32_t bar = b_full + 8 * st;
+                const int cnt = __popc(__ballot_sync(0xffffffffu, r >= 0));
+                if (e >= L::nst) warp_wait(b_empty + 8 * st, ((e / L::nst) - 1) & 1, bad);
+                if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)(cnt * P * D * 2));
+                __syncwarp();
+                if (r >= 0) {
+                    const uint32_t dst = ptx::smem_u32(sm + L::ring + st * L::stage) + lane * P * 128;
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        ptx::tma_load_2d(dst + c * (kTile * 128), map, c * 64, r, bar);
+                }
+                __syncwarp();
+            };
+            int r0 = page_row(0), r1 = page_row(1);
+            if (n > 0) load(0, r0, &kmap);
+            for (int i = 0; i < n; ++i) {
+                const int r2 = page_row(i + 2);
+                if (i + 1 < n) load(k_entry(i + 1), r1, &kmap);
+                load(v_entry(i, n), r0, &vmap);
+                r0 = r1;
+                r1 = r2;
+            }
+            // every requested tile has landed before the CTA may go on
+            for (int e = max(0, 2 * n - L::nst); e < 2 * n; ++e)
+                ptx::mbar_wait(b_full + 8 * (e % L::nst), (e / L::nst) & 1, kWaitNs);
+        } else if (warp == 1) {
+            // ------------------------------------------------------- issuer
+            ptx::bar_sync(kBarQ, 32 + 256);  // Q is in shared memory
+            if (lane == 0 && n > 0) {
+                const uint32_t idS = ptx::idesc_bf16(kTile, kTile, 0, 0);
+                const uint32_t idO = ptx::idesc_bf16(kTile, D, 0, 1);
+                const uint32_t base = ptx::smem_u32(sm), ring = base + L::ring;
+                const int nt[2] = {tiles_of(0), tiles_of(1)};
+                auto full = [&](int e) {
+                    if (!bad && !ptx::mbar_wait(b_full + 8 * (e % L::nst), (e / L::nst) & 1, kWaitNs)) bad = true;
+                };
+                auto release = [&](int e) { ptx::mma_commit(b_empty + 8 * (e % L::nst)); };
+                auto qk = [&](int slot, int i) {
+                    const int e = k_entry(i);
+                    full(e);
+                    ptx::tc_fence_after();
+                    const uint32_t aq = base + (two ? slot : 0) * L::stage, ak = ring + (e % L::nst) * L::stage;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t o = (ks / 4) * (kTile * 128) + (ks % 4) * 32;
+                        ptx::mma_f16(tmem + kColS + 128 * slot, ptx::sdesc(aq + o, 16, 1024), ptx::sdesc(ak + o, 16, 1024),
+                                     idS, ks > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_commit(b_s + 8 * slot);
+                };
+                auto pv = [&](int slot, int i, int it) {  // it: the slot's how-manieth tile
+                    const int e = v_entry(i, n);
+                    full(e);
+                    if (!bad && !ptx::mbar_wait(b_p + 8 * slot, it & 1, kWaitNs)) bad = true;
+                    ptx::tc_fence_after();
+                    const uint32_t av = ring + (e % L::nst) * L::stage;
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        ptx::mma_f16_ta(tmem + kColO + 128 * slot, tmem + kColS + 128 * slot + ks * 8,
+                                        ptx::sdesc(av + ks * 2048, kTile * 128, 1024), idO, (it > 0 || ks > 0) ? 1u : 0u);
+                    ptx::mma_commit(b_o + 8 * slot);
+                };
+                if (two) {
+                    for (int k = 0; k < 2; ++k)
+                        if (nt[k] > 0) qk(k, 0);
+                    release(k_entry(0));
+                    for (int i = 0; i < n; ++i) {
+                        for (int k = 0; k < 2; ++k) {
+                            if (nt[k] > i) pv(k, i, i);
+                            if (nt[k] > i + 1) qk(k, i + 1);
+                        }
+                        release(v_entry(i, n));
+                        if (i + 1 < n) release(k_entry(i + 1));
+                    }
+                } else {
+                    for (int i = 0; i < min(n, 2); ++i) {
+                        qk(i, i);
+                        release(k_entry(i));
+                    }
+                    for (int i = 0; i < n; ++i) {
+                        pv(i & 1, i, i >> 1);
+                        release(v_entry(i, n));
+                        if (i + 2 < n) {
+                            qk(i & 1, i + 2);
+                            release(k_entry(i + 2));
+                        }
+                    }
+                }
+                ptx::mma_commit(b_fin);
+                // waited for even after a timeout: no MMA still runs when the CTA goes on
+                ptx::mbar_wait(b_fin, 0, kWaitNs);
+            }
+            __syncwarp();
+        }
+        if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
+        __syncwarp();
+    }
+
+    float m = -CUDART_INF_F, l = 0.0f;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    if (warp >= 4) {
+        ptx::regs_inc<kRegsMany>();
+        // ------------------------------------------------------------ softmax
+        if (two || w == 0) {
+            const uint4* src =
+                reinterpret_cast<const uint4*>(p.Q + (long long)tok * p.q_stride + (long long)head * D);
+            unsigned char* dst = sm + w * L::stage + lr * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(dst + (c / 8) * (kTile * 128) + (((c % 8) ^ (lr & 7)) << 4)) = v;
+            }
+            ptx::fence_proxy_async();  // the MMAs read Q through the async proxy
+        }
+        ptx::bar_sync(kBarQ, 32 + 256);
+        const int mine = tiles_of(w);
+        const bool some = __any_sync(0xffffffffu, live);
+        const float slope2 = SCORED && live && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.0f;
+        const uint32_t tS = tmem + kColS + 128 * w + lane_off, tO = tmem + kColO + 128 * w + lane_off;
+        for (int it = 0; it < mine; ++it) {
+            const int i = two ? it : 2 * it + w;  // tile of this CTA
+            const int t0 = (ta + i) * kTile;
+            warp_wait(b_s + 8 * w, it & 1, bad);
+            ptx::tc_fence_after();
+            // keys behind the sequence's end: whatever their V holds becomes 0 (a
+            // weight of 0 times NaN would be NaN). Once per tile: by slot 0, whose
+            // P the issuer waits for first, or by the slot that has the tile. (After
+            // S: what the ring's stage held before this V has then been used, so the
+            // parity waited for is this load's and not that of the one before the last.)
+            if (t0 + kTile > T && (!two || w == 0 || tiles_of(0) <= i)) {
+                const int e = v_entry(i, n);
+                warp_wait(b_full + 8 * (e % L::nst), (e / L::nst) & 1, bad);
+                if (t0 + lr >= T) {
+                    unsigned char* v = sm + L::ring + (e % L::nst) * L::stage + lr * 128;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint4*>(v + (c / 8) * (kTile * 128) + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                ptx::fence_proxy_async();
+            }
+            if (!some) {  // no row of this warp: only the barrier's count
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_p + 8 * w);
+                continue;
+            }
+            uint32_t u[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, u[c]);
+            ptx::tmem_wait_ld();
+            if constexpr (SCORED) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        u[c][k] = asu(pages::score<true>(p, asf(u[c][k]), slope2, pos, t0 + 32 * c + k));
+            }
+            if (!__all_sync(0xffffffffu, see.all(t0, t0 + kTile))) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t bits = span_bits(see.a1 - t0, see.b1 - t0, c);
+                    if constexpr (SCORED) bits |= span_bits(see.a2 - t0, see.b2 - t0, c);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(bits >> k & 1u)) u[c][k] = asu(-CUDART_INF_F);
+                }
+            }
+            float mm[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                auto f = [&](int k) { return asf(u[c][k]); };
+                float x[11];
+#pragma unroll
+                for (int k = 0; k < 10; ++k) x[k] = ptx::max3(f(3 * k), f(3 * k + 1), f(3 * k + 2));
+                x[10] = fmaxf(f(30), f(31));
+                mm[c] = ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
+                                  ptx::max3(x[7], x[8], x[9]), x[10]);
+            }
+            const float top = ptx::max3(fmaxf(mm[0], mm[1]), mm[2], mm[3]);
+            // plain scores are scaled in the exponent's fused step (the scale is positive)
+            const float mt = SCORED ? top : top * p.scale_log2;
+            const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
+            if (__any_sync(0xffffffffu, move)) {
+                if (it > 0) {
+                    // O in the old reference: the slot's previous P V has to be done
+                    warp_wait(b_o + 8 * w, (it - 1) & 1, bad);
+                    ptx::tc_fence_after();
+                    const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
+                    l *= al;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(tO + c, o);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = asu(asf(o[k]) * al);
+                        ptx::tmem_st32x(tO + c, o);
+                    }
+                }
+                if (move) m = mt;
+            }
+            const float ref = m == -CUDART_INF_F ? 0.0f : m;
+            const float2 sc = SCORED ? make_float2(1.f, 1.f) : make_float2(p.scale_log2, p.scale_log2);
+            const float2 nm = make_float2(-ref, -ref);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pw[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float2 d = __ffma2_rn(make_float2(asf(u[c][2 * k]), asf(u[c][2 * k + 1])), sc, nm);
+                    const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
+                    sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+                    pw[k] = pack_bf2(e.x, e.y);
+                }
+                ptx::tmem_st16(tS + 16 * c, pw);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(b_p + 8 * w);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        }
+        if (mine > 0) {
+            warp_wait(b_o + 8 * w, (mine - 1) & 1, bad);
+            ptx::tc_fence_after();
+        }
+        if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
+        __syncwarp();
+    }
+
+    // careful_row of this warp's row `of` (a lane), over the slot's tiles
+    auto careful = [&](int of, float& cm, float& cl, float (&acc)[D / 32]) {
+        Seen se;
+        se.a1 = __shfl_sync(0xffffffffu, see.a1, of);
+        se.b1 = __shfl_sync(0xffffffffu, see.b1, of);
+        se.a2 = __shfl_sync(0xffffffffu, see.a2, of);
+        se.b2 = __shfl_sync(0xffffffffu, see.b2, of);
+        pages::careful_row<D, SCORED>(p, b.seq, __shfl_sync(0xffffffffu, tok, of), __shfl_sync(0xffffffffu, head, of),
+                                      __shfl_sync(0xffffffffu, pos, of), se, ta * kTile, (ta + n) * kTile, 7,
+                                      two ? 0 : (ta + w) & 1, two ? 1 : 2, cm, cl, acc);
+    };
+    const float inv_ln = 0.6931471805599453f;
+
+    if (two && S == 1) {
+        // ------------------------------------- a row's thread writes its output
+        if (warp >= 4) {
+            uint16_t* dst = p.out + ((long long)tok * p.Hq + head) * D;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            bool odd = live && l != 0.0f && !finite(l);
+            uint32_t o[D / 32][32];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) ptx::tmem_ld32(tmem + kColO + 128 * w + lane_off + 32 * c, o[c]);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    o[c][k] = l == 0.0f ? 0u : asu(asf(o[c][k]) * inv);
+                    odd = odd || (live && !finite(asf(o[c][k])));
+                }
+            if (live && !odd) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        *reinterpret_cast<uint4*>(dst + c * 32 + k) =
+                            make_uint4(pack_bf2(asf(o[c][k]), asf(o[c][k + 1])), pack_bf2(asf(o[c][k + 2]), asf(o[c][k + 3])),
+                                       pack_bf2(asf(o[c][k + 4]), asf(o[c][k + 5])),
+                                       pack_bf2(asf(o[c][k + 6]), asf(o[c][k + 7])));
+                if (p.lse) p.lse[(long long)tok * p.Hq + head] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * inv_ln;
+            }
+            for (unsigned odds = __ballot_sync(0xffffffffu, odd); odds; odds &= odds - 1) {
+                const int of = __ffs(odds) - 1;
+                float cm, cl, acc[D / 32];
+                careful(of, cm, cl, acc);
+                const long long at = (long long)__shfl_sync(0xffffffffu, tok, of) * p.Hq +
+                                     __shfl_sync(0xffffffffu, head, of);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e)
+                    p.out[at * D + lane * (D / 32) + e] =
+                        cl == 0.0f ? (uint16_t)0 : __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] / cl));
+                if (lane == 0 && p.lse) p.lse[at] = cl == 0.0f ? -CUDART_INF_F : (cm + log2f(cl)) * inv_ln;
+            }
+        }
+    } else {
+        // --------------------- states into shared memory, merged over the cluster
+        ptx::tc_fence_before();
+        __syncthreads();  // no MMA reads the tiles any more, every load has landed
+        ptx::tc_fence_after();
+        float* rows = reinterpret_cast<float*>(sm);
+        if (warp >= 4) {
+            float* dst = rows + (w * kTile + lr) * L::rs;
+            bool odd = live && l != 0.0f && !finite(l);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                ptx::tmem_ld32(tmem + kColO + 128 * w + lane_off + 32 * c, o);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 v = make_float4(asf(o[k]), asf(o[k + 1]), asf(o[k + 2]), asf(o[k + 3]));
+                    odd = odd || (live && l != 0.0f && !(finite(v.x) && finite(v.y) && finite(v.z) && finite(v.w)));
+                    *reinterpret_cast<float4*>(dst + c * 32 + k) = v;
+                }
+            }
+            dst[D] = l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m);
+            dst[D + 1] = l;
+            __syncwarp();
+            for (unsigned odds = __ballot_sync(0xffffffffu, odd); odds; odds &= odds - 1) {
+                const int of = __ffs(odds) - 1;
+                float cm, cl, acc[D / 32];
+                careful(of, cm, cl, acc);
+                float* to = rows + (w * kTile + (warp & 3) * 32 + of) * L::rs;
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) to[lane * (D / 32) + e] = acc[e];
+                if (lane == 0) to[D] = cm, to[D + 1] = cl;
+                __syncwarp();
+            }
+        }
+        __syncthreads();
+        if (S > 1) {
+            ptx::cluster_arrive();
+            ptx::cluster_wait();
+        }
+        constexpr int C4 = D / 4;
+        const int parts = two ? 1 : 2;  // states of a row in each CTA
+        for (int x = rank * kThreads + tid; x < nr * C4; x += S * kThreads) {
+            const int r = x / C4, c4 = x % C4;
+            float M = -CUDART_INF_F;
+            for (int k = 0; k < S; ++k)
+                for (int q = 0; q < parts; ++q)
+                    M = fmaxf(M, ptx::ld_dsmem(ptx::dsmem_addr(rows + (r + q * kTile) * L::rs + D, k)));
+            float Lt = 0.0f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < S; ++k)
+                for (int q = 0; q < parts; ++q) {
+                    const float* at = rows + (r + q * kTile) * L::rs;
+                    const float2 ml = ptx::ld_dsmem2(ptx::dsmem_addr(at + D, k));
+                    const float4 v = ptx::ld_dsmem4(ptx::dsmem_addr(at + c4 * 4, k));
+                    if (ml.y == 0.0f) continue;  // a state of nothing, whatever its O holds
+                    const float f = ptx::ex2(ml.x - M);
+                    Lt = fmaf(f, ml.y, Lt);
+                    a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+                }
+            const int i = (r_begin + r) / p.G;
+            const long long at = (long long)(b.q0 + i) * p.Hq + g * p.G + (r_begin + r) - i * p.G;
+            const float inv = Lt == 0.0f ? 0.0f : 1.0f / Lt;
+            *reinterpret_cast<uint2*>(p.out + at * D + c4 * 4) =
+                Lt == 0.0f ? make_uint2(0u, 0u) : make_uint2(pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv));
+            if (c4 == 0 && p.lse) p.lse[at] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * inv_ln;
+        }
+        if (S > 1) {  // no CTA goes away while another reads its rows
+            ptx::cluster_arrive();
+            ptx::cluster_wait();
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kCols);
+    }
+}
+
+template <int D, bool SCORED>
+cudaError_t opt_in() {
+    auto kern = pages_chunk_kernel<D, SCORED>;
+    static const cudaError_t opt =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::total);
+    return opt;
+}
+
+template <int D, bool SCORED>
+cudaError_t launch(const PagedAttend& a, int max_kv, int sm_count, cudaStream_t st) {
+    cudaError_t e = opt_in<D, SCORED>();
+    if (e != cudaSuccess) return e;
+    const long long rows = (long long)a.s.tokens * a.G;
+    const long long blocks = rows / kRows + a.s.seqs;  // at least as many as there are
+    const long long jobs = std::max<long long>(1, (rows + kRows - 1) / kRows + (a.s.seqs - 1) / 2) * a.s.Hk;  // about
+    const int ntiles = std::max(1, (max_kv + kTile - 1) / kTile);
+    int split = 1;
+    long long best = -1;
+    for (int S = 1; S <= kMaxSplit && S * 2 <= std::max(ntiles, 2); S *= 2) {
+        // key tiles one SM works through: waves x tiles per CTA, and about two
+        // tiles' time for a CTA's start and end (one more for a merge)
+        const long long cost = (jobs * S + sm_count - 1) / sm_count * ((ntiles + S - 1) / S + (S > 1 ? 3 : 2));
+        if (best < 0 || cost < best) best = cost, split = S;
+    }
+    if (split * blocks * a.s.Hk > INT_MAX) return cudaErrorInvalidValue;
+    CUtensorMap kmap, vmap;
+    const long long trows = (long long)a.s.pages * a.s.Hk << a.s.pshift;
+    if (!make_page_map(&kmap, a.K, D, trows, 1 << a.s.pshift) || !make_page_map(&vmap, a.V, D, trows, 1 << a.s.pshift))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(split * blocks * a.s.Hk), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Lay<D>::total;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pages_chunk_kernel<D, SCORED>, kmap, vmap, a);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_kv, int sm_count, cudaStream_t st) {
+    const bool scored = paged_scored(a);
+    if (head_dim == 64) return scored ? launch<64, true>(a, max_kv, sm_count, st) : launch<64, false>(a, max_kv, sm_count, st);
+    return scored ? launch<128, true>(a, max_kv, sm_count, st) : launch<128, false>(a, max_kv, sm_count, st);
+}
+
+}  // namespace kvp

@@ -306,7 +306,7 @@ pages_rows_kernel(const PagedAttend p) {
                 const int i = (r_begin + r) / p.G, hd = g * p.G + (r_begin + r) - i * p.G;
                 const Seen se = pages::row_seen<SCORED>(p, b.seq, b.q0 + i, T - b.n + i, T);
                 float mm, ll, acc[D / 32];
-                pages::careful_row<D, SCORED>(p, b.seq, b.q0 + i, hd, T - b.n + i, se, ua * kUnit, ub * kUnit,
+                pages::careful_row<D, SCORED>(p, b.seq, b.q0 + i, hd, T - b.n + i, se, ua * kUnit, ub * kUnit, 4,
                                               (ua + warp) % kWarps, kWarps, mm, ll, acc);
                 float* dst = rows + r * RS;
                 __syncwarp();
