@@ -17,7 +17,7 @@
 // tile, and their states are merged at the end.
 //   warp 0        loader: pages by TMA, one box of 64 channels per page, K and
 //                 V tiles through one ring in the order they are needed
-//   warp 1        issuer of the MMAs (one lane)
+//   warps 1, 2    issuers of the MMAs, one per slot (one lane each)
 //   warps 4-11    softmax, a thread per row of its slot
 // S_{i+1} of a slot may overwrite P_i because the MMAs of a thread run in the
 // order they are issued. V comes as [key][channel], which the MMA takes as an
@@ -25,6 +25,15 @@
 // states meet in distributed shared memory: no workspace, no second launch.
 // Every wait is bounded; one that expires is recorded in the status word, and
 // the CTA runs to its end without waiting again.
+//
+// Measured on 2,432 new tokens over 16K keys, 32 query heads on 8 KV heads of
+// 128 (two full waves of CTAs): 406 us, 1488 TFLOP/s. What got it there: one
+// issuer per slot, taking turns (a single one's waits and commits left the
+// tensor cores idle: 466 us; two without turns fell into step: 592 us);
+// operands of the MMAs in uniform registers (509 us before); P formed under
+// the reference as it is, the maxima checked beside it, and handed over in
+// halves; no register spills (the roles' registers shifted between the
+// warpgroups). The MMAs alone, with no softmax, take 338 us.
 #include <algorithm>
 
 #include "pages.cuh"
@@ -39,9 +48,13 @@ constexpr int kTile = 128;              // keys per tile, rows per slot
 constexpr int kRows = 2 * kTile;        // rows per CTA
 constexpr float kLazyMax = 8.0f;        // log2 units the reference may trail the maximum
 constexpr int kMaxSplit = 8;
-constexpr uint64_t kWaitNs = 200ull * 1000 * 1000;
+constexpr uint32_t kTryNs = 1000, kTries = 1u << 20;
 constexpr uint32_t kCols = 512;         // tensor memory: S0, S1, O0, O1
-constexpr uint32_t kBarQ = 1;           // named barrier: issuer and softmax warps (Q staged)
+// named barriers: Q is staged (issuers and softmax warps); every role is done; the merge rows are written;
+// a slot's turn at the tensor cores
+constexpr uint32_t kBarQ = 1, kBarDone = 2, kBarRows = 3, kBarTurn = 4;
+constexpr int kSoftmax = 256;           // softmax threads
+constexpr float kLn2 = 0.6931471805599453f;
 // registers: 3 warpgroups launched with 168 each; 88 + 2 x 208 = 3 x 168
 constexpr int kRegsFew = 88, kRegsMany = 208;
 
@@ -51,8 +64,9 @@ struct Lay {
     static constexpr int nst = D == 128 ? 5 : 10;
     static constexpr int ring = 2 * stage;       // after the two Q tiles
     static constexpr int bars = ring + nst * stage;
-    static constexpr int nbars = 2 * nst + 2 + 2 + 2 + 1;
-    static constexpr int info = bars + nbars * 8;  // rng[2][2], tensor memory address
+    // barriers: full, empty per ring stage; per slot S, P (of each half), O, all done
+    static constexpr int bar_s = bars + 2 * nst * 8, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_fin = bar_o + 16;
+    static constexpr int info = bar_fin + 16;  // rng[2][2], tensor memory address
     static constexpr int total = info + 32 + 1024;  // + alignment of the base
     static constexpr int rs = D + 4;             // floats of a merge row: O, m, l
     static_assert(kRows * rs * 4 <= bars, "merge rows fit in the tiles");
@@ -71,11 +85,22 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < CUDART_INF_F
 __device__ __forceinline__ int k_entry(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_entry(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
 
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool& bad) {
-    bool ok = bad || ptx::mbar_wait(bar, parity, kWaitNs);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) bad = true;
-    return ok;
+// Wait for phase `parity` of the barrier by a whole warp; after kTries tries
+// (each suspends the warp for a while; about a second in all) `bad` is set, and
+// no wait after that waits. One short loop: what is around a wait is on the
+// main loop's critical path.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, bool& bad) {
+    if (!bad) {
+        uint32_t ok;
+        asm volatile(
+            "{\n.reg .pred p, q;\n.reg .u32 n;\nmov.u32 n, 0;\n"
+            "TRY:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n@p bra DONE;\n"
+            "add.u32 n, n, 1;\nsetp.lt.u32 q, n, %4;\n@q bra TRY;\n"
+            "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(kTryNs), "n"(kTries) : "memory");
+        bad = !ok;
+    }
+    __syncwarp();
 }
 
 // bits k of [32 c, 32 c + 32) with a <= 32 c + k < b
@@ -107,24 +132,27 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int r_begin = (nblk - 1 - b.blk) * kRows;
     const int nr = min(kRows, b.n * p.G - r_begin);
     const bool two = nr > kTile;  // two row tiles, or one in both slots
+    const bool direct = two && S == 1;  // a row's only state is its thread's
 
     const uint32_t b_full = ptx::smem_u32(sm + L::bars), b_empty = b_full + 8 * L::nst;
-    const uint32_t b_s = b_empty + 8 * L::nst, b_p = b_s + 16, b_o = b_p + 16, b_fin = b_o + 16;
+    const uint32_t b_s = ptx::smem_u32(sm + L::bar_s), b_p = ptx::smem_u32(sm + L::bar_p);
+    const uint32_t b_o = ptx::smem_u32(sm + L::bar_o), b_fin = ptx::smem_u32(sm + L::bar_fin);
     int* rng = reinterpret_cast<int*>(sm + L::info);  // [slot] {first key seen, end of the keys seen}
     uint32_t* tslot = reinterpret_cast<uint32_t*>(rng + 4);
     if (tid == 0) {
         for (int i = 0; i < L::nst; ++i) {
             ptx::mbar_init(b_full + 8 * i, 1);
-            ptx::mbar_init(b_empty + 8 * i, 1);
+            ptx::mbar_init(b_empty + 8 * i, two ? 2 : 1);  // the slots that use a tile
         }
         for (int w = 0; w < 2; ++w) {
             ptx::mbar_init(b_s + 8 * w, 1);
-            ptx::mbar_init(b_p + 8 * w, 4);
+            ptx::mbar_init(b_p + 16 * w, 4);  // P of the tile's first half, of its second
+            ptx::mbar_init(b_p + 16 * w + 8, 4);
             ptx::mbar_init(b_o + 8 * w, 1);
+            ptx::mbar_init(b_fin + 8 * w, 1);
             rng[2 * w] = INT_MAX;
             rng[2 * w + 1] = 0;
         }
-        ptx::mbar_init(b_fin, 1);
         ptx::mbar_init_fence();
     }
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tslot), kCols);
@@ -170,6 +198,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         return max(0, min(n, (rng[2 * slot + 1] + kTile - 1) / kTile - ta));
     };
     bool bad = false;
+    float* rows = reinterpret_cast<float*>(sm);  // merge rows, once the tiles are done with
 
     if (warp < 4) {
         ptx::regs_dec<kRegsFew>();
@@ -215,84 +244,140 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
             // every requested tile has landed before the CTA may go on
             for (int e = max(0, 2 * n - L::nst); e < 2 * n; ++e)
-                ptx::mbar_wait(b_full + 8 * (e % L::nst), (e / L::nst) & 1, kWaitNs);
-        } else if (warp == 1) {
-            // ------------------------------------------------------- issuer
-            ptx::bar_sync(kBarQ, 32 + 256);  // Q is in shared memory
-            if (lane == 0 && n > 0) {
-                const uint32_t idS = ptx::idesc_bf16(kTile, kTile, 0, 0);
-                const uint32_t idO = ptx::idesc_bf16(kTile, D, 0, 1);
-                const uint32_t base = ptx::smem_u32(sm), ring = base + L::ring;
-                const int nt[2] = {tiles_of(0), tiles_of(1)};
-                auto full = [&](int e) {
-                    if (!bad && !ptx::mbar_wait(b_full + 8 * (e % L::nst), (e / L::nst) & 1, kWaitNs)) bad = true;
-                };
-                auto release = [&](int e) { ptx::mma_commit(b_empty + 8 * (e % L::nst)); };
-                auto qk = [&](int slot, int i) {
-                    const int e = k_entry(i);
-                    full(e);
-                    ptx::tc_fence_after();
-                    const uint32_t aq = base + (two ? slot : 0) * L::stage, ak = ring + (e % L::nst) * L::stage;
+            {
+                bool late = false;
+                warp_wait(b_full + 8 * (e % L::nst), (e / L::nst) & 1, late);
+            }
+        } else if (warp <= 2) {
+            // ------------------------------------------------------ issuers
+            // One warp per slot: what one of them waits for costs the other's MMAs
+            // nothing (a single issuer's waits and commits, about 1000 cycles per tile,
+            // left the tensor cores idle). The whole warp runs this with uniform
+            // values; lane 0 issues.
+            ptx::bar_sync(kBarQ, 64 + kSoftmax);  // Q is in shared memory
+            const uint32_t lead = lane == 0;
+            const int slot = __shfl_sync(0xffffffffu, warp - 1, 0);
+            const int nn = __shfl_sync(0xffffffffu, n, 0), nt = __shfl_sync(0xffffffffu, tiles_of(slot), 0);
+            const bool pairs = __shfl_sync(0xffffffffu, (int)two, 0) != 0;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t base = __shfl_sync(0xffffffffu, ptx::smem_u32(sm), 0), ring = base + L::ring;
+            const uint32_t tS = tm + kColS + 128 * slot, tO = tm + kColO + 128 * slot;
+            const uint32_t idS = ptx::idesc_bf16(kTile, kTile, 0, 0);
+            const uint32_t idO = ptx::idesc_bf16(kTile, D, 0, 1);
+            const uint32_t u_full = base + L::bars, u_empty = u_full + 8 * L::nst;
+            const uint32_t u_s = base + L::bar_s + 8 * slot, u_p = base + L::bar_p + 16 * slot;
+            const uint32_t u_o = base + L::bar_o + 8 * slot, u_fin = base + L::bar_fin + 8 * slot;
+            const uint64_t dq = ptx::sdesc(base + (pairs ? slot : 0) * L::stage, 16, 1024);
+            auto full = [&](int e) { warp_wait(u_full + 8 * (e % L::nst), (e / L::nst) & 1, bad); };
+            auto release = [&](int e) { ptx::mma_commit_lead(lead, u_empty + 8 * (e % L::nst)); };
+            auto qk = [&](int e) {
+                const uint64_t dk = ptx::sdesc(ring + (e % L::nst) * L::stage, 16, 1024);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t o = (ks / 4) * (kTile * 128) + (ks % 4) * 32;
-                        ptx::mma_f16(tmem + kColS + 128 * slot, ptx::sdesc(aq + o, 16, 1024), ptx::sdesc(ak + o, 16, 1024),
-                                     idS, ks > 0 ? 1u : 0u);
-                    }
-                    ptx::mma_commit(b_s + 8 * slot);
-                };
-                auto pv = [&](int slot, int i, int it) {  // it: the slot's how-manieth tile
-                    const int e = v_entry(i, n);
-                    full(e);
-                    if (!bad && !ptx::mbar_wait(b_p + 8 * slot, it & 1, kWaitNs)) bad = true;
-                    ptx::tc_fence_after();
-                    const uint32_t av = ring + (e % L::nst) * L::stage;
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t o = ((ks / 4) * (kTile * 128) + (ks % 4) * 32) >> 4;  // descriptor units
+                    ptx::mma_f16_lead(lead, tS, dq + o, dk + o, idS, ks > 0 ? 1u : 0u);
+                }
+                ptx::mma_commit_lead(lead, u_s);
+            };
+            auto pv = [&](int e, int it) {
+                const uint64_t dv = ptx::sdesc(ring + (e % L::nst) * L::stage, kTile * 128, 1024);
 #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        ptx::mma_f16_ta(tmem + kColO + 128 * slot, tmem + kColS + 128 * slot + ks * 8,
-                                        ptx::sdesc(av + ks * 2048, kTile * 128, 1024), idO, (it > 0 || ks > 0) ? 1u : 0u);
-                    ptx::mma_commit(b_o + 8 * slot);
-                };
-                if (two) {
-                    for (int k = 0; k < 2; ++k)
-                        if (nt[k] > 0) qk(k, 0);
-                    release(k_entry(0));
-                    for (int i = 0; i < n; ++i) {
-                        for (int k = 0; k < 2; ++k) {
-                            if (nt[k] > i) pv(k, i, i);
-                            if (nt[k] > i + 1) qk(k, i + 1);
-                        }
-                        release(v_entry(i, n));
-                        if (i + 1 < n) release(k_entry(i + 1));
+                for (int h = 0; h < 2; ++h) {
+                    if (h) {
+                        warp_wait(u_p + 8, it & 1, bad);
+                        ptx::tc_fence_after();
                     }
-                } else {
-                    for (int i = 0; i < min(n, 2); ++i) {
-                        qk(i, i);
-                        release(k_entry(i));
-                    }
-                    for (int i = 0; i < n; ++i) {
-                        pv(i & 1, i, i >> 1);
-                        release(v_entry(i, n));
-                        if (i + 2 < n) {
-                            qk(i & 1, i + 2);
-                            release(k_entry(i + 2));
-                        }
+#pragma unroll
+                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks)  // P of half h: 32 columns from column 64 h on
+                        ptx::mma_f16_ta_lead(lead, tO, tS + 32 * h + ks * 8, dv + ks * (2048 >> 4), idO,
+                                             (it > 0 || ks > 0) ? 1u : 0u);
+                    ptx::mma_commit_lead(lead, u_o);
+                }
+            };
+            // The slots take turns: P V and the next Q K^T of one, then of the other, so
+            // that one's softmax runs beside the other's MMAs. (Left to themselves both
+            // run their MMAs and then their softmax at the same time, which took 1.3
+            // times as long.) What a turn needs is waited for before it, what can be
+            // done after it is.
+            // it: turns so far; own: the slot has a tile in this turn, more: and one after it
+            auto turn = [&](int it, bool own, int ev, bool more, int ek) {
+                if (own) {
+                    full(ev);
+                    warp_wait(u_p, it & 1, bad);
+                }
+                if (more) full(ek);
+                ptx::tc_fence_after();
+                if (slot || it > 0) ptx::bar_sync(kBarTurn + slot, 64);
+                if (own) pv(ev, it);
+                if (more) qk(ek);
+                ptx::bar_arrive(kBarTurn + 1 - slot, 64);
+                if (own) release(ev);
+                if (more) release(ek);
+            };
+            // a tile that the other slot alone works on: its K or V is not needed here
+            auto pass = [&](int e) {
+                full(e);
+                if (lead) ptx::mbar_arrive(u_empty + 8 * (e % L::nst));
+            };
+            if (pairs) {
+                if (nn > 0) {
+                    full(k_entry(0));
+                    ptx::tc_fence_after();
+                    if (nt > 0) {
+                        qk(k_entry(0));
+                        release(k_entry(0));
+                    } else {
+                        pass(k_entry(0));
                     }
                 }
-                ptx::mma_commit(b_fin);
+                for (int i = 0; i < nn; ++i) {
+                    const int ev = v_entry(i, nn), ek = k_entry(i + 1);
+                    turn(i, nt > i, ev, nt > i + 1, ek);
+                    if (nt <= i) pass(ev);
+                    if (nt <= i + 1 && i + 1 < nn) pass(ek);
+                }
+                if (nn > 0 && !slot) ptx::bar_sync(kBarTurn, 64);
+            } else {
+                // the other slot's tiles are waited for as well: a wait by parity needs
+                // the stage's load before the last to be known done
+                for (int i = 0; i < min(nn, 2); ++i) {
+                    full(k_entry(i));
+                    if (i != slot) continue;
+                    ptx::tc_fence_after();
+                    qk(k_entry(i));
+                    release(k_entry(i));
+                }
+                for (int i = 0; i < nn; i += 2) {
+                    if (slot) {
+                        full(v_entry(i, nn));
+                        if (i + 2 < nn) full(k_entry(i + 2));
+                    }
+                    turn(i >> 1, i + slot < nn, v_entry(i + slot, nn), i + 2 + slot < nn, k_entry(i + 2 + slot));
+                    if (!slot) {
+                        if (i + 1 < nn) full(v_entry(i + 1, nn));
+                        if (i + 3 < nn) full(k_entry(i + 3));
+                    }
+                }
+                if (nn > 0 && !slot) ptx::bar_sync(kBarTurn, 64);
+            }
+            if (nt > 0) {
+                ptx::mma_commit_lead(lead, u_fin);
                 // waited for even after a timeout: no MMA still runs when the CTA goes on
-                ptx::mbar_wait(b_fin, 0, kWaitNs);
+                bool late = false;
+                warp_wait(u_fin, 0, late);
+                bad = bad || late;
             }
             __syncwarp();
         }
         if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
-        __syncwarp();
-    }
-
-    float m = -CUDART_INF_F, l = 0.0f;
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    if (warp >= 4) {
+        if (!direct) {
+            ptx::bar_sync(kBarDone, kThreads);
+            ptx::bar_sync(kBarRows, kThreads);
+        }
+    } else {
         ptx::regs_inc<kRegsMany>();
+        float m = -CUDART_INF_F, l = 0.0f;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         // ------------------------------------------------------------ softmax
         if (two || w == 0) {
             const uint4* src =
@@ -305,7 +390,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
             ptx::fence_proxy_async();  // the MMAs read Q through the async proxy
         }
-        ptx::bar_sync(kBarQ, 32 + 256);
+        ptx::bar_sync(kBarQ, 64 + kSoftmax);
         const int mine = tiles_of(w);
         const bool some = __any_sync(0xffffffffu, live);
         const float slope2 = SCORED && live && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.0f;
@@ -316,11 +401,10 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             warp_wait(b_s + 8 * w, it & 1, bad);
             ptx::tc_fence_after();
             // keys behind the sequence's end: whatever their V holds becomes 0 (a
-            // weight of 0 times NaN would be NaN). Once per tile: by slot 0, whose
-            // P the issuer waits for first, or by the slot that has the tile. (After
-            // S: what the ring's stage held before this V has then been used, so the
-            // parity waited for is this load's and not that of the one before the last.)
-            if (t0 + kTile > T && (!two || w == 0 || tiles_of(0) <= i)) {
+            // weight of 0 times NaN would be NaN); each slot for itself. (After S: what
+            // the ring's stage held before this V has then been used, so the parity
+            // waited for is this load's and not that of the one before the last.)
+            if (t0 + kTile > T) {
                 const int e = v_entry(i, n);
                 warp_wait(b_full + 8 * (e % L::nst), (e / L::nst) & 1, bad);
                 if (t0 + lr >= T) {
@@ -331,137 +415,148 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 ptx::fence_proxy_async();
             }
-            if (!some) {  // no row of this warp: only the barrier's count
+            if (!some) {  // no row of this warp: only the barriers' counts
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(b_p + 8 * w);
+                if (lane < 2) ptx::mbar_arrive(b_p + 16 * w + 8 * lane);
                 continue;
             }
-            uint32_t u[4][32];
+            // The tile's keys in two halves, so that P V of the first runs while P of
+            // the second is formed. P under the reference as it is, its row maxima on
+            // the way; only where a maximum passes the reference (the first half
+            // tile, and rarely after it) is the reference moved and P formed again:
+            // the maxima cost no time of their own on the chain from S to P.
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                const int k0 = t0 + 64 * h;  // first key of the half
+                const uint32_t tSh = tS + 64 * h;
+                const bool whole = __all_sync(0xffffffffu, see.all(k0, k0 + 64));
+                uint32_t pw[2][16];
+                float2 sum[2];
+#pragma unroll 1
+                for (;;) {
+                    const float ref = m == -CUDART_INF_F ? 0.0f : m;
+                    const float2 sc = SCORED ? make_float2(1.f, 1.f) : make_float2(p.scale_log2, p.scale_log2);
+                    const float2 nm = make_float2(-ref, -ref);
+                    float mm[2];
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
+                    auto form = [&](int c, uint32_t (&u)[32]) {
+                        if constexpr (SCORED) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, u[c]);
-            ptx::tmem_wait_ld();
-            if constexpr (SCORED) {
+                            for (int k = 0; k < 32; ++k)
+                                u[k] = asu(pages::score<true>(p, asf(u[k]), slope2, pos, k0 + 32 * c + k));
+                        }
+                        if (!whole) {
+                            uint32_t bits = span_bits(see.a1 - k0, see.b1 - k0, c);
+                            if constexpr (SCORED) bits |= span_bits(see.a2 - k0, see.b2 - k0, c);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                            for (int k = 0; k < 32; ++k)
+                                if (!(bits >> k & 1u)) u[k] = asu(-CUDART_INF_F);
+                        }
+                        auto f = [&](int k) { return asf(u[k]); };
+                        float x[11];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        u[c][k] = asu(pages::score<true>(p, asf(u[c][k]), slope2, pos, t0 + 32 * c + k));
-            }
-            if (!__all_sync(0xffffffffu, see.all(t0, t0 + kTile))) {
+                        for (int k = 0; k < 10; ++k) x[k] = ptx::max3(f(3 * k), f(3 * k + 1), f(3 * k + 2));
+                        x[10] = fmaxf(f(30), f(31));
+                        mm[c] = ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
+                                          ptx::max3(x[7], x[8], x[9]), x[10]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t bits = span_bits(see.a1 - t0, see.b1 - t0, c);
-                    if constexpr (SCORED) bits |= span_bits(see.a2 - t0, see.b2 - t0, c);
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 d = __ffma2_rn(make_float2(f(2 * k), f(2 * k + 1)), sc, nm);
+                            const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
+                            sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+                            pw[c][k] = pack_bf2(e.x, e.y);
+                        }
+                    };
+                    uint32_t u0[32], u1[32];  // the second chunk is on its way while the first is worked on
+                    ptx::tmem_ld32(tSh, u0);
+                    ptx::tmem_wait_ld(u0);
+                    ptx::tmem_ld32(tSh + 32, u1);
+                    form(0, u0);
+                    ptx::tmem_wait_ld(u1);
+                    form(1, u1);
+                    const float top = fmaxf(mm[0], mm[1]);
+                    // plain scores are scaled in the exponent's fused step (the scale is positive)
+                    const float mt = SCORED ? top : top * p.scale_log2;
+                    const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
+                    if (!__any_sync(0xffffffffu, move)) break;
+                    const int before = 2 * it + h;  // half tiles of the slot before this one
+                    if (before > 0) {
+                        // O in the old reference: the P V of the half before has to be done
+                        // (the one before that is: S of this tile came after it)
+                        warp_wait(b_o + 8 * w, (before - 1) & 1, bad);
+                        ptx::tc_fence_after();
+                        const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
+                        l *= al;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            ptx::tmem_ld32(tO + c, u0);
+                            ptx::tmem_wait_ld(u0);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!(bits >> k & 1u)) u[c][k] = asu(-CUDART_INF_F);
-                }
-            }
-            float mm[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                auto f = [&](int k) { return asf(u[c][k]); };
-                float x[11];
-#pragma unroll
-                for (int k = 0; k < 10; ++k) x[k] = ptx::max3(f(3 * k), f(3 * k + 1), f(3 * k + 2));
-                x[10] = fmaxf(f(30), f(31));
-                mm[c] = ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
-                                  ptx::max3(x[7], x[8], x[9]), x[10]);
-            }
-            const float top = ptx::max3(fmaxf(mm[0], mm[1]), mm[2], mm[3]);
-            // plain scores are scaled in the exponent's fused step (the scale is positive)
-            const float mt = SCORED ? top : top * p.scale_log2;
-            const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
-            if (__any_sync(0xffffffffu, move)) {
-                if (it > 0) {
-                    // O in the old reference: the slot's previous P V has to be done
-                    warp_wait(b_o + 8 * w, (it - 1) & 1, bad);
-                    ptx::tc_fence_after();
-                    const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
-                    l *= al;
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        ptx::tmem_ld32(tO + c, o);
-                        ptx::tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = asu(asf(o[k]) * al);
-                        ptx::tmem_st32x(tO + c, o);
+                            for (int k = 0; k < 32; ++k) u0[k] = asu(asf(u0[k]) * al);
+                            ptx::tmem_st32x(tO + c, u0);
+                        }
+                        ptx::tmem_wait_st();
                     }
+                    if (move) m = mt;
                 }
-                if (move) m = mt;
-            }
-            const float ref = m == -CUDART_INF_F ? 0.0f : m;
-            const float2 sc = SCORED ? make_float2(1.f, 1.f) : make_float2(p.scale_log2, p.scale_log2);
-            const float2 nm = make_float2(-ref, -ref);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                // P over the half's own columns of S
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pw[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float2 d = __ffma2_rn(make_float2(asf(u[c][2 * k]), asf(u[c][2 * k + 1])), sc, nm);
-                    const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
-                    sum[k & 1] = __fadd2_rn(sum[k & 1], e);
-                    pw[k] = pack_bf2(e.x, e.y);
-                }
-                ptx::tmem_st16(tS + 16 * c, pw);
+                for (int c = 0; c < 2; ++c) ptx::tmem_st16(tSh + 16 * c, pw[c]);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_p + 16 * w + 8 * h);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(b_p + 8 * w);
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
         if (mine > 0) {
-            warp_wait(b_o + 8 * w, (mine - 1) & 1, bad);
+            // the last half tile's P V; the one before it is done (S of the last tile
+            // came after the P V of the tile before)
+            warp_wait(b_o + 8 * w, 0, bad);
+            warp_wait(b_o + 8 * w, 1, bad);
             ptx::tc_fence_after();
         }
         if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
         __syncwarp();
-    }
 
-    // careful_row of this warp's row `of` (a lane), over the slot's tiles
-    auto careful = [&](int of, float& cm, float& cl, float (&acc)[D / 32]) {
-        Seen se;
-        se.a1 = __shfl_sync(0xffffffffu, see.a1, of);
-        se.b1 = __shfl_sync(0xffffffffu, see.b1, of);
-        se.a2 = __shfl_sync(0xffffffffu, see.a2, of);
-        se.b2 = __shfl_sync(0xffffffffu, see.b2, of);
-        pages::careful_row<D, SCORED>(p, b.seq, __shfl_sync(0xffffffffu, tok, of), __shfl_sync(0xffffffffu, head, of),
-                                      __shfl_sync(0xffffffffu, pos, of), se, ta * kTile, (ta + n) * kTile, 7,
-                                      two ? 0 : (ta + w) & 1, two ? 1 : 2, cm, cl, acc);
-    };
-    const float inv_ln = 0.6931471805599453f;
-
-    if (two && S == 1) {
-        // ------------------------------------- a row's thread writes its output
-        if (warp >= 4) {
+        // careful_row of this warp's row `of` (a lane), over the slot's tiles
+        auto careful = [&](int of, float& cm, float& cl, float (&acc)[D / 32]) {
+            Seen se;
+            se.a1 = __shfl_sync(0xffffffffu, see.a1, of);
+            se.b1 = __shfl_sync(0xffffffffu, see.b1, of);
+            se.a2 = __shfl_sync(0xffffffffu, see.a2, of);
+            se.b2 = __shfl_sync(0xffffffffu, see.b2, of);
+            pages::careful_row<D, SCORED>(p, b.seq, __shfl_sync(0xffffffffu, tok, of),
+                                          __shfl_sync(0xffffffffu, head, of), __shfl_sync(0xffffffffu, pos, of), se,
+                                          ta * kTile, (ta + n) * kTile, 7, two ? 0 : (ta + w) & 1, two ? 1 : 2, cm, cl,
+                                          acc);
+        };
+        bool odd = live && l != 0.0f && !finite(l);  // sums that a masked key may have spoilt
+        if (direct) {
+            // a row's thread writes its output
             uint16_t* dst = p.out + ((long long)tok * p.Hq + head) * D;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            bool odd = live && l != 0.0f && !finite(l);
-            uint32_t o[D / 32][32];
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) ptx::tmem_ld32(tmem + kColO + 128 * w + lane_off + 32 * c, o[c]);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c)
+            uint32_t o[32];
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                ptx::tmem_ld32(tO + c, o);
+                ptx::tmem_wait_ld(o);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    o[c][k] = l == 0.0f ? 0u : asu(asf(o[c][k]) * inv);
-                    odd = odd || (live && !finite(asf(o[c][k])));
+                    odd = odd || (live && l != 0.0f && !finite(asf(o[k])));
+                    o[k] = l == 0.0f ? 0u : asu(asf(o[k]) * inv);
                 }
-            if (live && !odd) {
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
+                if (live) {  // (odd rows are written again)
 #pragma unroll
                     for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4*>(dst + c * 32 + k) =
-                            make_uint4(pack_bf2(asf(o[c][k]), asf(o[c][k + 1])), pack_bf2(asf(o[c][k + 2]), asf(o[c][k + 3])),
-                                       pack_bf2(asf(o[c][k + 4]), asf(o[c][k + 5])),
-                                       pack_bf2(asf(o[c][k + 6]), asf(o[c][k + 7])));
-                if (p.lse) p.lse[(long long)tok * p.Hq + head] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * inv_ln;
+                        *reinterpret_cast<uint4*>(dst + c + k) =
+                            make_uint4(pack_bf2(asf(o[k]), asf(o[k + 1])), pack_bf2(asf(o[k + 2]), asf(o[k + 3])),
+                                       pack_bf2(asf(o[k + 4]), asf(o[k + 5])), pack_bf2(asf(o[k + 6]), asf(o[k + 7])));
+                }
             }
+            if (live && p.lse)
+                p.lse[(long long)tok * p.Hq + head] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+            __syncwarp();
             for (unsigned odds = __ballot_sync(0xffffffffu, odd); odds; odds &= odds - 1) {
                 const int of = __ffs(odds) - 1;
                 float cm, cl, acc[D / 32];
@@ -472,23 +567,18 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 for (int e = 0; e < D / 32; ++e)
                     p.out[at * D + lane * (D / 32) + e] =
                         cl == 0.0f ? (uint16_t)0 : __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] / cl));
-                if (lane == 0 && p.lse) p.lse[at] = cl == 0.0f ? -CUDART_INF_F : (cm + log2f(cl)) * inv_ln;
+                if (lane == 0 && p.lse) p.lse[at] = cl == 0.0f ? -CUDART_INF_F : (cm + log2f(cl)) * kLn2;
             }
-        }
-    } else {
-        // --------------------- states into shared memory, merged over the cluster
-        ptx::tc_fence_before();
-        __syncthreads();  // no MMA reads the tiles any more, every load has landed
-        ptx::tc_fence_after();
-        float* rows = reinterpret_cast<float*>(sm);
-        if (warp >= 4) {
+        } else {
+            // states into shared memory, once no MMA reads the tiles any more and
+            // every load has landed
+            ptx::bar_sync(kBarDone, kThreads);
             float* dst = rows + (w * kTile + lr) * L::rs;
-            bool odd = live && l != 0.0f && !finite(l);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
-                ptx::tmem_ld32(tmem + kColO + 128 * w + lane_off + 32 * c, o);
-                ptx::tmem_wait_ld();
+                ptx::tmem_ld32(tO + 32 * c, o);
+                ptx::tmem_wait_ld(o);
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     const float4 v = make_float4(asf(o[k]), asf(o[k + 1]), asf(o[k + 2]), asf(o[k + 3]));
@@ -509,8 +599,12 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (lane == 0) to[D] = cm, to[D + 1] = cl;
                 __syncwarp();
             }
+            ptx::bar_sync(kBarRows, kThreads);
         }
-        __syncthreads();
+    }
+
+    if (!direct) {
+        // the rows' states, merged over the slots and the cluster
         if (S > 1) {
             ptx::cluster_arrive();
             ptx::cluster_wait();
@@ -540,7 +634,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const float inv = Lt == 0.0f ? 0.0f : 1.0f / Lt;
             *reinterpret_cast<uint2*>(p.out + at * D + c4 * 4) =
                 Lt == 0.0f ? make_uint2(0u, 0u) : make_uint2(pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv));
-            if (c4 == 0 && p.lse) p.lse[at] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * inv_ln;
+            if (c4 == 0 && p.lse) p.lse[at] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * kLn2;
         }
         if (S > 1) {  // no CTA goes away while another reads its rows
             ptx::cluster_arrive();
