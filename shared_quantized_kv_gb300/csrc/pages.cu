@@ -41,8 +41,7 @@ pages_append_kernel(const PagedSeqs s, uint4* __restrict__ Kp, uint4* __restrict
     // blocks of one row each are numbered over the sequences' rows alone; rows
     // that belong to nobody lie behind them, so the block's row is the token
     // (q_start ascending from 0, as documented)
-    const int T = pages::held_tokens(s, b.seq);
-    const int pos = T - b.n + b.blk;
+    const int pos = b.T - b.n + b.blk;
     if (pos < 0 || b.q0 + b.blk != tok) return;
     const int page = __ldg(s.table + (long long)b.seq * s.tstride + (pos >> s.pshift));
     if (page < 0 || page >= s.pages) {
@@ -278,6 +277,7 @@ int kvpool_pages_attend(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t
     a.q_stride = q_stride;
     a.Hq = q_heads;
     a.G = group;
+    a.g_magic = (uint32_t)(((1ull << 32) + group - 1) / group);
     const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf((float)pg->head_dim);
     a.scale_log2 = scale * 1.4426950408889634f;
     if (score) {
@@ -296,7 +296,7 @@ int kvpool_pages_attend(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t
     const int max_kv = (int)std::min<long long>(seqs->max_kv > 0 ? std::min<long long>(seqs->max_kv, room) : room, 1LL << 30);
     const int max_q = seqs->max_q > 0 ? std::min(seqs->max_q, seqs->tokens) : seqs->tokens;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((long long)max_q * group > 16) return map_cuda(kvp::launch_pages_chunk(a, pg->head_dim, max_kv, sms, st));
+    if ((long long)max_q * group > 16) return map_cuda(kvp::launch_pages_chunk(a, pg->head_dim, max_q, max_kv, st));
     return map_cuda(kvp::launch_pages_rows(a, pg->head_dim, max_q, max_kv, sms, st));
 }
 

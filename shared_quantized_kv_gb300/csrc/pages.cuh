@@ -32,6 +32,7 @@ struct PagedAttend {
     const uint16_t* Q;  // bf16, q_stride elements per token
     long long q_stride;
     int Hq, G;
+    uint32_t g_magic;      // 2^32 / G, rounded up (see div_group)
     float scale_log2;      // softmax scale * log2(e)
     float cap2, cap_in;    // cap * log2(e); 2 * log2(e) * softmax scale / cap
     const float* slopes;
@@ -61,7 +62,7 @@ cudaError_t launch_pages_append(const PagedSeqs& s, int head_dim, uint16_t* Kp, 
 // pages_chunk.cu: many); max_q, max_kv as in kvpool_seqs_t, but never 0.
 cudaError_t launch_pages_rows(const PagedAttend& a, int head_dim, int max_q, int max_kv, int sm_count,
                               cudaStream_t st);
-cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_kv, int sm_count, cudaStream_t st);
+cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_q, int max_kv, cudaStream_t st);
 
 namespace pages {
 
@@ -81,21 +82,22 @@ __device__ __forceinline__ int held_tokens(const PagedSeqs& s, int i) {
 
 // The rows of all sequences cut into blocks of RB rows (a row: a new token and
 // one of the G query heads of a KV head; a block holds rows of one sequence).
-// Block z: its sequence, its number there, the sequence's first token row q0
-// and new tokens n. False past the last block. Whole warps call it; 32
-// sequences at a time, their loads independent of one another.
+// Block z: its sequence, its number there, the sequence's first token row q0,
+// new tokens n and held tokens T. False past the last block. Whole warps call
+// it; 32 sequences at a time, their loads independent of one another.
 struct RowBlock {
-    int seq, blk, q0, n;
+    int seq, blk, q0, n, T;
 };
 __device__ __forceinline__ bool find_block(const PagedSeqs& s, int G, int RB, int z, RowBlock& b) {
     const int lane = threadIdx.x & 31;
     int before = 0;  // blocks of the sequences before these 32
     for (int base = 0; base < s.seqs; base += 32) {
         const int i = base + lane;
-        int q0 = 0, n = 0;
+        int q0 = 0, n = 0, T = 0;
         if (i < s.seqs) {
             q0 = row_begin(s, i);
             n = max(row_begin(s, i + 1) - q0, 0);
+            T = held_tokens(s, i);
         }
         const int nb = (int)(((long long)n * G + RB - 1) / RB);
         int sum = nb;
@@ -110,12 +112,18 @@ __device__ __forceinline__ bool find_block(const PagedSeqs& s, int G, int RB, in
             b.seq = base + l;
             b.q0 = __shfl_sync(0xffffffffu, q0, l);
             b.n = __shfl_sync(0xffffffffu, n, l);
+            b.T = __shfl_sync(0xffffffffu, T, l);
             b.blk = z - before - __shfl_sync(0xffffffffu, sum - nb, l);
             return true;
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
     }
     return false;
+}
+
+// x / G for x G < 2^32: the product's excess over x / G is below x G / 2^32 of a G-th.
+__device__ __forceinline__ int div_group(const PagedAttend& a, int x) {
+    return a.G == 1 ? x : (int)__umulhi((uint32_t)x, a.g_magic);
 }
 
 // The keys a row sees: [a1, b1) and [a2, b2) (overlapping or empty as may be).

@@ -46,13 +46,14 @@ using pages::Seen;
 constexpr int kThreads = 384;
 constexpr int kTile = 128;              // keys per tile, rows per slot
 constexpr int kRows = 2 * kTile;        // rows per CTA
+constexpr int kFewTiles = 8;            // key tiles that a cluster does not split
+constexpr int kMaxParts = 16;           // states of a row: 8 CTAs, 2 slots
 constexpr float kLazyMax = 8.0f;        // log2 units the reference may trail the maximum
-constexpr int kMaxSplit = 8;
 constexpr uint32_t kTryNs = 1000, kTries = 1u << 20;
 constexpr uint32_t kCols = 512;         // tensor memory: S0, S1, O0, O1
 // named barriers: Q is staged (issuers and softmax warps); every role is done; the merge rows are written;
-// a slot's turn at the tensor cores
-constexpr uint32_t kBarQ = 1, kBarDone = 2, kBarRows = 3, kBarTurn = 4;
+// a slot's turn at the tensor cores; both slots' stores of 32 rows are done
+constexpr uint32_t kBarQ = 1, kBarDone = 2, kBarRows = 3, kBarTurn = 4, kBarOdd = 6;
 constexpr int kSoftmax = 256;           // softmax threads
 constexpr float kLn2 = 0.6931471805599453f;
 // registers: 3 warpgroups launched with 168 each; 88 + 2 x 208 = 3 x 168
@@ -69,7 +70,7 @@ struct Lay {
     static constexpr int info = bar_fin + 16;  // rng[2][2], tensor memory address
     static constexpr int total = info + 32 + 1024;  // + alignment of the base
     static constexpr int rs = D + 4;             // floats of a merge row: O, m, l
-    static_assert(kRows * rs * 4 <= bars, "merge rows fit in the tiles");
+    static_assert(kRows * (rs + kMaxParts) * 4 <= bars, "merge rows and weights fit in the tiles");
     static_assert(total <= 227 * 1024, "shared memory");
 };
 
@@ -121,28 +122,34 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     unsigned char* sm = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const PagedSeqs& s = p.s;
-    const int S = (int)ptx::cluster_size(), rank = (int)ptx::cluster_rank();
+    const int CS = (int)ptx::cluster_size(), rank = (int)ptx::cluster_rank();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+    int* rng = reinterpret_cast<int*>(sm + L::info);  // [slot] {first key seen, end of the keys seen}
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(rng + 4);
+    if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tslot), kCols);  // beside the search
     // blocks of a sequence from its last (the one that sees most) to its first
-    const int job = blockIdx.x / S, g = job % s.Hk;
+    const int job = blockIdx.x / CS, g = job % s.Hk;
     pages::RowBlock b;
-    if (!pages::find_block(s, p.G, kRows, job / s.Hk, b)) return;  // the whole cluster's
-    const int T = pages::held_tokens(s, b.seq);
+    if (!pages::find_block(s, p.G, kRows, job / s.Hk, b)) {  // the whole cluster's
+        __syncthreads();
+        if (warp == 1) ptx::tmem_dealloc(*tslot, kCols);
+        return;
+    }
+    const int T = b.T;
     const int nblk = (b.n * p.G + kRows - 1) / kRows;
     const int r_begin = (nblk - 1 - b.blk) * kRows;
     const int nr = min(kRows, b.n * p.G - r_begin);
     const bool two = nr > kTile;  // two row tiles, or one in both slots
-    const bool direct = two && S == 1;  // a row's only state is its thread's
+    // row r of the block: token row b.q0 + i_begin + div_group(j_begin + r), and the head of the group
+    const int i_begin = r_begin / p.G, j_begin = r_begin - i_begin * p.G;
 
     const uint32_t b_full = ptx::smem_u32(sm + L::bars), b_empty = b_full + 8 * L::nst;
     const uint32_t b_s = ptx::smem_u32(sm + L::bar_s), b_p = ptx::smem_u32(sm + L::bar_p);
     const uint32_t b_o = ptx::smem_u32(sm + L::bar_o), b_fin = ptx::smem_u32(sm + L::bar_fin);
-    int* rng = reinterpret_cast<int*>(sm + L::info);  // [slot] {first key seen, end of the keys seen}
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(rng + 4);
     if (tid == 0) {
         for (int i = 0; i < L::nst; ++i) {
             ptx::mbar_init(b_full + 8 * i, 1);
-            ptx::mbar_init(b_empty + 8 * i, two ? 2 : 1);  // the slots that use a tile
+            ptx::mbar_init(b_empty + 8 * i, 2);  // both slots
         }
         for (int w = 0; w < 2; ++w) {
             ptx::mbar_init(b_s + 8 * w, 1);
@@ -155,8 +162,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         ptx::mbar_init_fence();
     }
-    if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tslot), kCols);
-    __syncthreads();
+    if constexpr (SCORED) __syncthreads();
 
     // softmax threads: their row and what it sees
     const int w = (warp - 4) / 4;          // slot
@@ -166,18 +172,20 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     Seen see = {0, INT_MAX, 0, 0};  // rows past the block: Q is 0, nothing to mask, dropped at the end
     int tok = 0, head = 0, pos = 0;
     if (live) {
-        const int i = (r_begin + row) / p.G;
-        tok = b.q0 + i;
-        head = g * p.G + (r_begin + row) - i * p.G;
-        pos = T - b.n + i;
+        const int i = pages::div_group(p, j_begin + row);
+        tok = b.q0 + i_begin + i;
+        head = g * p.G + j_begin + row - i * p.G;
+        pos = T - b.n + i_begin + i;
         see = pages::row_seen<SCORED>(p, b.seq, tok, pos, T);
     }
-    if (warp >= 4) {
-        const int lo = __reduce_min_sync(0xffffffffu, live ? see.lo() : INT_MAX);
-        const int hi = __reduce_max_sync(0xffffffffu, live ? see.hi() : 0);
-        if (lane == 0 && hi > 0) {
-            atomicMin(&rng[2 * w], lo);
-            atomicMax(&rng[2 * w + 1], hi);
+    if constexpr (SCORED) {
+        if (warp >= 4) {
+            const int lo = __reduce_min_sync(0xffffffffu, live ? see.lo() : INT_MAX);
+            const int hi = __reduce_max_sync(0xffffffffu, live ? see.hi() : 0);
+            if (lane == 0 && hi > 0) {
+                atomicMin(&rng[2 * w], lo);
+                atomicMax(&rng[2 * w + 1], hi);
+            }
         }
     }
     ptx::tc_fence_before();
@@ -185,18 +193,34 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     ptx::tc_fence_after();
     const uint32_t tmem = *tslot;
 
+    // end of the keys that a slot's rows see; with the causal mask alone the
+    // last row sees most
+    auto seen_end = [&](int slot) {
+        if constexpr (SCORED) return rng[2 * slot + 1];
+        const int last = two && slot == 0 ? kTile - 1 : nr - 1;
+        return max(0, min(T, T - b.n + i_begin + pages::div_group(p, j_begin + last) + 1));
+    };
     // this CTA's key tiles [ta, ta + n): the cluster's share of the tiles that
     // any row sees; slot w takes the first nt[w] of them (two row tiles), or
-    // every second one
-    const int hi = max(rng[1], rng[3]);
-    const int t_lo = hi > 0 ? min(rng[0], rng[2]) / kTile : 0, t_hi = (hi + kTile - 1) / kTile;
+    // every second one. Few tiles are not split: the cluster's first CTA takes
+    // them all, as a merge costs about what kFewTiles cost.
+    const int hi = max(seen_end(0), seen_end(1));
+    int t_lo = 0;
+    if constexpr (SCORED) t_lo = hi > 0 ? min(rng[0], rng[2]) / kTile : 0;
+    const int t_hi = (hi + kTile - 1) / kTile;
+    const int S = t_hi - t_lo <= kFewTiles ? 1 : CS;
     const int per = (t_hi - t_lo + S - 1) / S;
     const int ta = t_lo + rank * per;
     const int n = max(0, min(t_hi, ta + per) - ta);
     auto tiles_of = [&](int slot) {
         if (!two) return (n - slot + 1) / 2;
-        return max(0, min(n, (rng[2 * slot + 1] + kTile - 1) / kTile - ta));
+        return max(0, min(n, (seen_end(slot) + kTile - 1) / kTile - ta));
     };
+    if (rank >= S) {  // not a split block's: nothing to do, and nobody waits for this CTA
+        if (warp == 1) ptx::tmem_dealloc(tmem, kCols);
+        return;
+    }
+    const bool direct = S == 1;  // the rows' states never leave this CTA
     bool bad = false;
     float* rows = reinterpret_cast<float*>(sm);  // merge rows, once the tiles are done with
 
@@ -338,24 +362,28 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 if (nn > 0 && !slot) ptx::bar_sync(kBarTurn, 64);
             } else {
-                // the other slot's tiles are waited for as well: a wait by parity needs
-                // the stage's load before the last to be known done
+                // the other slot's tiles are let pass in the ring's order: a wait by
+                // parity needs the stage's load before this one to be done, and the
+                // one after it not to be
                 for (int i = 0; i < min(nn, 2); ++i) {
+                    if (i != slot) {
+                        pass(k_entry(i));
+                        continue;
+                    }
                     full(k_entry(i));
-                    if (i != slot) continue;
                     ptx::tc_fence_after();
                     qk(k_entry(i));
                     release(k_entry(i));
                 }
                 for (int i = 0; i < nn; i += 2) {
                     if (slot) {
-                        full(v_entry(i, nn));
-                        if (i + 2 < nn) full(k_entry(i + 2));
+                        pass(v_entry(i, nn));
+                        if (i + 2 < nn) pass(k_entry(i + 2));
                     }
                     turn(i >> 1, i + slot < nn, v_entry(i + slot, nn), i + 2 + slot < nn, k_entry(i + 2 + slot));
                     if (!slot) {
-                        if (i + 1 < nn) full(v_entry(i + 1, nn));
-                        if (i + 3 < nn) full(k_entry(i + 3));
+                        if (i + 1 < nn) pass(v_entry(i + 1, nn));
+                        if (i + 3 < nn) pass(k_entry(i + 3));
                     }
                 }
                 if (nn > 0 && !slot) ptx::bar_sync(kBarTurn, 64);
@@ -370,23 +398,36 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             __syncwarp();
         }
         if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
-        if (!direct) {
-            ptx::bar_sync(kBarDone, kThreads);
-            ptx::bar_sync(kBarRows, kThreads);
-        }
+        if (!direct || !two) ptx::bar_sync(kBarDone, kThreads);
+        if (!direct) ptx::bar_sync(kBarRows, kThreads);
     } else {
         ptx::regs_inc<kRegsMany>();
         float m = -CUDART_INF_F, l = 0.0f;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         // ------------------------------------------------------------ softmax
         if (two || w == 0) {
-            const uint4* src =
-                reinterpret_cast<const uint4*>(p.Q + (long long)tok * p.q_stride + (long long)head * D);
-            unsigned char* dst = sm + w * L::stage + lr * 128;
+            // 16-byte pieces, consecutive lanes on consecutive pieces of a row
+            constexpr int CH = D / 8;
+            unsigned char* dst = sm + w * L::stage;
+            const int first = two ? w * kTile : 0;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(dst + (c / 8) * (kTile * 128) + (((c % 8) ^ (lr & 7)) << 4)) = v;
+            for (int k0 = 0; k0 < CH; k0 += 8) {
+                uint4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int x = (k0 + k) * kTile + (tid & 127), r = x / CH, c = x % CH;
+                    const int i = pages::div_group(p, j_begin + first + r);
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (first + r < nr)
+                        v[k] = __ldg(reinterpret_cast<const uint4*>(
+                                         p.Q + (long long)(b.q0 + i_begin + i) * p.q_stride +
+                                         (long long)(g * p.G + j_begin + first + r - i * p.G) * D) + c);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int x = (k0 + k) * kTile + (tid & 127), r = x / CH, c = x % CH;
+                    *reinterpret_cast<uint4*>(dst + (c / 8) * (kTile * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v[k];
+                }
             }
             ptx::fence_proxy_async();  // the MMAs read Q through the async proxy
         }
@@ -395,6 +436,25 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const bool some = __any_sync(0xffffffffu, live);
         const float slope2 = SCORED && live && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.0f;
         const uint32_t tS = tmem + kColS + 128 * w + lane_off, tO = tmem + kColO + 128 * w + lane_off;
+        if (!SCORED && mine > 0 && some) {
+            // the maximum of the first half tile, where no key is masked, is the
+            // first reference
+            const int t0 = (ta + (two ? 0 : w)) * kTile;
+            if (__all_sync(0xffffffffu, see.all(t0, t0 + 64))) {
+                warp_wait(b_s + 8 * w, 0, bad);
+                ptx::tc_fence_after();
+                float x = -CUDART_INF_F;
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t u[32];
+                    ptx::tmem_ld32(tS + c, u);
+                    ptx::tmem_wait_ld(u);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) x = ptx::max3(x, asf(u[k]), asf(u[k + 1]));
+                }
+                m = x * p.scale_log2;
+            }
+        }
         for (int it = 0; it < mine; ++it) {
             const int i = two ? it : 2 * it + w;  // tile of this CTA
             const int t0 = (ta + i) * kTile;
@@ -510,17 +570,16 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
         }
         if (mine > 0) {
-            // the last half tile's P V; the one before it is done (S of the last tile
-            // came after the P V of the tile before)
-            warp_wait(b_o + 8 * w, 0, bad);
-            warp_wait(b_o + 8 * w, 1, bad);
+            // every MMA of the slot (a barrier of one phase: of b_o's last two phases
+            // either may be the one under way here, which a parity cannot tell)
+            warp_wait(b_fin + 8 * w, 0, bad);
             ptx::tc_fence_after();
         }
         if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
         __syncwarp();
 
-        // careful_row of this warp's row `of` (a lane), over the slot's tiles
-        auto careful = [&](int of, float& cm, float& cl, float (&acc)[D / 32]) {
+        // careful_row of this warp's row `of` (a lane), over the slot's tiles or all of the CTA's
+        auto careful = [&](int of, bool all, float& cm, float& cl, float (&acc)[D / 32]) {
             Seen se;
             se.a1 = __shfl_sync(0xffffffffu, see.a1, of);
             se.b1 = __shfl_sync(0xffffffffu, see.b1, of);
@@ -528,39 +587,16 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             se.b2 = __shfl_sync(0xffffffffu, see.b2, of);
             pages::careful_row<D, SCORED>(p, b.seq, __shfl_sync(0xffffffffu, tok, of),
                                           __shfl_sync(0xffffffffu, head, of), __shfl_sync(0xffffffffu, pos, of), se,
-                                          ta * kTile, (ta + n) * kTile, 7, two ? 0 : (ta + w) & 1, two ? 1 : 2, cm, cl,
-                                          acc);
+                                          ta * kTile, (ta + n) * kTile, 7, two || all ? 0 : (ta + w) & 1,
+                                          two || all ? 1 : 2, cm, cl, acc);
         };
         bool odd = live && l != 0.0f && !finite(l);  // sums that a masked key may have spoilt
-        if (direct) {
-            // a row's thread writes its output
-            uint16_t* dst = p.out + ((long long)tok * p.Hq + head) * D;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            uint32_t o[32];
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                ptx::tmem_ld32(tO + c, o);
-                ptx::tmem_wait_ld(o);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    odd = odd || (live && l != 0.0f && !finite(asf(o[k])));
-                    o[k] = l == 0.0f ? 0u : asu(asf(o[k]) * inv);
-                }
-                if (live) {  // (odd rows are written again)
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4*>(dst + c + k) =
-                            make_uint4(pack_bf2(asf(o[k]), asf(o[k + 1])), pack_bf2(asf(o[k + 2]), asf(o[k + 3])),
-                                       pack_bf2(asf(o[k + 4]), asf(o[k + 5])), pack_bf2(asf(o[k + 6]), asf(o[k + 7])));
-                }
-            }
-            if (live && p.lse)
-                p.lse[(long long)tok * p.Hq + head] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
-            __syncwarp();
-            for (unsigned odds = __ballot_sync(0xffffffffu, odd); odds; odds &= odds - 1) {
+        // rows `odds` of the warp again, over the CTA's tiles, and their output
+        auto again = [&](unsigned odds) {
+            for (; odds; odds &= odds - 1) {
                 const int of = __ffs(odds) - 1;
                 float cm, cl, acc[D / 32];
-                careful(of, cm, cl, acc);
+                careful(of, true, cm, cl, acc);
                 const long long at = (long long)__shfl_sync(0xffffffffu, tok, of) * p.Hq +
                                      __shfl_sync(0xffffffffu, head, of);
 #pragma unroll
@@ -568,6 +604,97 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     p.out[at * D + lane * (D / 32) + e] =
                         cl == 0.0f ? (uint16_t)0 : __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] / cl));
                 if (lane == 0 && p.lse) p.lse[at] = cl == 0.0f ? -CUDART_INF_F : (cm + log2f(cl)) * kLn2;
+            }
+        };
+        auto store8 = [&](uint16_t* dst, const float (&y)[32], int k) {
+            *reinterpret_cast<uint4*>(dst + k) =
+                make_uint4(pack_bf2(y[k], y[k + 1]), pack_bf2(y[k + 2], y[k + 3]), pack_bf2(y[k + 4], y[k + 5]),
+                           pack_bf2(y[k + 6], y[k + 7]));
+        };
+        uint16_t* orow = p.out + ((long long)tok * p.Hq + head) * D;
+        if (direct && two) {
+            // a row's thread writes its output
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                float y[32];
+                ptx::tmem_ld32(tO + c, o);
+                ptx::tmem_wait_ld(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    odd = odd || (live && l != 0.0f && !finite(asf(o[k])));
+                    y[k] = l == 0.0f ? 0.0f : asf(o[k]) * inv;
+                }
+                if (live) {  // (odd rows are written again)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) store8(orow + c, y, k);
+                }
+            }
+            if (live && p.lse)
+                p.lse[(long long)tok * p.Hq + head] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+            __syncwarp();
+            again(__ballot_sync(0xffffffffu, odd));
+        } else if (direct) {
+            // Both slots have the row: each hands half its channels to the other
+            // and writes the rest. A row: the half of slot 0, of slot 1, then
+            // (m, l) of both; l = NaN marks a state with sums that are not finite.
+            ptx::bar_sync(kBarDone, kThreads);  // no MMA reads the tiles any more, every load has landed
+            float* mine_at = rows + lr * L::rs;
+            constexpr int HC = D / 2;
+            uint32_t keep[HC];
+#pragma unroll
+            for (int c = 0; c < HC; c += 32) {
+                uint32_t o[32];
+                ptx::tmem_ld32(tO + (1 - w) * HC + c, o);
+                ptx::tmem_wait_ld(o);
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 v = make_float4(asf(o[k]), asf(o[k + 1]), asf(o[k + 2]), asf(o[k + 3]));
+                    odd = odd || (live && l != 0.0f && !(finite(v.x) && finite(v.y) && finite(v.z) && finite(v.w)));
+                    *reinterpret_cast<float4*>(mine_at + w * HC + c + k) = v;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < HC; c += 32) {
+                uint32_t (&o)[32] = *reinterpret_cast<uint32_t (*)[32]>(keep + c);
+                ptx::tmem_ld32(tO + w * HC + c, o);
+                ptx::tmem_wait_ld(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) odd = odd || (live && l != 0.0f && !finite(asf(o[k])));
+            }
+            *reinterpret_cast<float2*>(mine_at + D + 2 * w) =
+                make_float2(l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m), odd ? CUDART_NAN_F : l);
+            ptx::bar_sync(kBarRows, kSoftmax);
+            const float4 ml = *reinterpret_cast<const float4*>(mine_at + D);
+            const float M = fmaxf(ml.x, ml.z);
+            const float f0 = ml.y == 0.0f ? 0.0f : ptx::ex2(ml.x - M), f1 = ml.w == 0.0f ? 0.0f : ptx::ex2(ml.z - M);
+            const float Lt = fmaf(f0, ml.y, f1 * ml.w);
+            const float inv = Lt == 0.0f ? 0.0f : 1.0f / Lt;
+            const float fm = (w ? f1 : f0) * inv, fo = (w ? f0 : f1) * inv;  // own and other slot's weight
+            const bool none = (w ? ml.w : ml.y) == 0.0f, onone = (w ? ml.y : ml.w) == 0.0f;
+            odd = live && Lt != 0.0f && !finite(Lt);
+#pragma unroll
+            for (int c = 0; c < HC; c += 32) {
+                float y[32];
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(mine_at + (1 - w) * HC + c + k);
+                    const float ov[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[k + e] = (none ? 0.0f : asf(keep[c + k + e]) * fm) + (onone ? 0.0f : ov[e] * fo);
+                }
+                if (live) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) store8(orow + w * HC + c, y, k);
+                }
+            }
+            if (live && p.lse && !w)
+                p.lse[(long long)tok * p.Hq + head] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * kLn2;
+            if (__any_sync(0xffffffffu, odd)) {
+                ptx::bar_sync(kBarOdd + (warp & 3), 64);  // after both halves' stores
+                if (!w) again(__ballot_sync(0xffffffffu, odd));
             }
         } else {
             // states into shared memory, once no MMA reads the tiles any more and
@@ -592,7 +719,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             for (unsigned odds = __ballot_sync(0xffffffffu, odd); odds; odds &= odds - 1) {
                 const int of = __ffs(odds) - 1;
                 float cm, cl, acc[D / 32];
-                careful(of, cm, cl, acc);
+                careful(of, false, cm, cl, acc);
                 float* to = rows + (w * kTile + (warp & 3) * 32 + of) * L::rs;
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) to[lane * (D / 32) + e] = acc[e];
@@ -604,37 +731,68 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     }
 
     if (!direct) {
-        // the rows' states, merged over the slots and the cluster
+        // The rows' states, merged over the slots and the cluster: each CTA takes
+        // a share of the rows. First a thread per row: the states' weights (with
+        // the division by the sum in them); then 4 channels per item, the states'
+        // loads all under way before the first is used.
         if (S > 1) {
             ptx::cluster_arrive();
             ptx::cluster_wait();
         }
-        constexpr int C4 = D / 4;
-        const int parts = two ? 1 : 2;  // states of a row in each CTA
-        for (int x = rank * kThreads + tid; x < nr * C4; x += S * kThreads) {
-            const int r = x / C4, c4 = x % C4;
-            float M = -CUDART_INF_F;
-            for (int k = 0; k < S; ++k)
-                for (int q = 0; q < parts; ++q)
-                    M = fmaxf(M, ptx::ld_dsmem(ptx::dsmem_addr(rows + (r + q * kTile) * L::rs + D, k)));
-            float Lt = 0.0f;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < S; ++k)
-                for (int q = 0; q < parts; ++q) {
-                    const float* at = rows + (r + q * kTile) * L::rs;
-                    const float2 ml = ptx::ld_dsmem2(ptx::dsmem_addr(at + D, k));
-                    const float4 v = ptx::ld_dsmem4(ptx::dsmem_addr(at + c4 * 4, k));
-                    if (ml.y == 0.0f) continue;  // a state of nothing, whatever its O holds
-                    const float f = ptx::ex2(ml.x - M);
-                    Lt = fmaf(f, ml.y, Lt);
-                    a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
-                }
-            const int i = (r_begin + r) / p.G;
-            const long long at = (long long)(b.q0 + i) * p.Hq + g * p.G + (r_begin + r) - i * p.G;
+        const int slots = two ? 1 : 2, parts = slots * S;  // states of a row; k-th: slot k % slots of CTA k / slots
+        const int share = (nr + S - 1) / S, r0 = rank * share, cnt = max(0, min(nr - r0, share));
+        float* weights = rows + kRows * L::rs;  // [share][parts]
+        auto state = [&](int r, int k) {
+            return ptx::dsmem_addr(rows + (r0 + r + (k % slots) * kTile) * L::rs, k / slots);
+        };
+        auto out_row = [&](int r) {
+            const int i = pages::div_group(p, j_begin + r0 + r);
+            return (long long)(b.q0 + i_begin + i) * p.Hq + g * p.G + j_begin + r0 + r - i * p.G;
+        };
+        for (int r = tid; r < cnt; r += kThreads) {
+            float2 ml[kMaxParts];
+#pragma unroll
+            for (int k = 0; k < kMaxParts; ++k)
+                ml[k] = k < parts ? ptx::ld_dsmem2(state(r, k) + D * 4) : make_float2(-CUDART_INF_F, 0.0f);
+            float M = -CUDART_INF_F, Lt = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kMaxParts; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+            for (int k = 0; k < kMaxParts; ++k) {
+                ml[k].x = ml[k].y == 0.0f ? 0.0f : ptx::ex2(ml[k].x - M);  // a state of nothing: 0
+                Lt = fmaf(ml[k].x, ml[k].y, Lt);
+            }
             const float inv = Lt == 0.0f ? 0.0f : 1.0f / Lt;
-            *reinterpret_cast<uint2*>(p.out + at * D + c4 * 4) =
-                Lt == 0.0f ? make_uint2(0u, 0u) : make_uint2(pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv));
-            if (c4 == 0 && p.lse) p.lse[at] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * kLn2;
+#pragma unroll
+            for (int k = 0; k < kMaxParts; ++k)
+                if (k < parts) weights[r * parts + k] = ml[k].y == 0.0f ? -1.0f : ml[k].x * inv;
+            if (p.lse) p.lse[out_row(r)] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * kLn2;
+        }
+        __syncthreads();
+        constexpr int C4 = D / 4;
+#pragma unroll 2
+        for (int x = tid; x < cnt * C4; x += kThreads) {
+            const int r = x / C4, c4 = x % C4;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < parts; k0 += 4) {
+                float4 v[4];
+                float f[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    f[u] = -1.0f;
+                    if (k0 + u < parts) {
+                        v[u] = ptx::ld_dsmem4(state(r, k0 + u) + c4 * 16);
+                        f[u] = weights[r * parts + k0 + u];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (f[u] < 0.0f) continue;  // a state of nothing, whatever its O holds
+                    a.x = fmaf(f[u], v[u].x, a.x), a.y = fmaf(f[u], v[u].y, a.y);
+                    a.z = fmaf(f[u], v[u].z, a.z), a.w = fmaf(f[u], v[u].w, a.w);
+                }
+            }
+            *reinterpret_cast<uint2*>(p.out + out_row(r) * D + c4 * 4) = make_uint2(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w));
         }
         if (S > 1) {  // no CTA goes away while another reads its rows
             ptx::cluster_arrive();
@@ -649,28 +807,60 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     }
 }
 
+// Per instance, once (a static initialiser: thread-safe): the shared memory
+// opted in, and how many clusters of 1, 2, 4 and 8 CTAs the GPU holds at once
+// (a cluster's CTAs share a group of SMs whose number need not be a multiple).
+struct Fit {
+    cudaError_t err;
+    int clusters[4];
+};
 template <int D, bool SCORED>
-cudaError_t opt_in() {
-    auto kern = pages_chunk_kernel<D, SCORED>;
-    static const cudaError_t opt =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::total);
-    return opt;
+const Fit& fit() {
+    static const Fit f = [] {
+        auto kern = pages_chunk_kernel<D, SCORED>;
+        Fit x{cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::total), {}};
+        for (int i = 0; i < 4 && x.err == cudaSuccess; ++i) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1 << i, 1, 1);
+            cfg.blockDim = dim3(kThreads, 1, 1);
+            cfg.dynamicSmemBytes = Lay<D>::total;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1 << i;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            x.err = cudaOccupancyMaxActiveClusters(&x.clusters[i], kern, &cfg);
+        }
+        return x;
+    }();
+    return f;
 }
 
 template <int D, bool SCORED>
-cudaError_t launch(const PagedAttend& a, int max_kv, int sm_count, cudaStream_t st) {
-    cudaError_t e = opt_in<D, SCORED>();
-    if (e != cudaSuccess) return e;
+cudaError_t launch(const PagedAttend& a, int max_q, int max_kv, cudaStream_t st) {
+    const Fit& f = fit<D, SCORED>();
+    if (f.err != cudaSuccess) return f.err;
     const long long rows = (long long)a.s.tokens * a.G;
     const long long blocks = rows / kRows + a.s.seqs;  // at least as many as there are
-    const long long jobs = std::max<long long>(1, (rows + kRows - 1) / kRows + (a.s.seqs - 1) / 2) * a.s.Hk;  // about
+    // about as many as there are, and the key tiles of one (in halves where one
+    // row tile has both slots)
+    const long long per_seq = ((long long)max_q * a.G + kRows - 1) / kRows;
+    const long long jobs = std::min(rows / kRows + (a.s.seqs + 1) / 2, a.s.seqs * per_seq) * a.s.Hk;
+    const bool one = (long long)max_q * a.G <= kTile;
     const int ntiles = std::max(1, (max_kv + kTile - 1) / kTile);
     int split = 1;
     long long best = -1;
-    for (int S = 1; S <= kMaxSplit && S * 2 <= std::max(ntiles, 2); S *= 2) {
-        // key tiles one SM works through: waves x tiles per CTA, and about two
-        // tiles' time for a CTA's start and end (one more for a merge)
-        const long long cost = (jobs * S + sm_count - 1) / sm_count * ((ntiles + S - 1) / S + (S > 1 ? 3 : 2));
+    for (int i = 0; i < 4 && f.clusters[i] > 0; ++i) {
+        const int S = 1 << i;
+        if (S > 1 && ntiles <= kFewTiles) break;
+        // the time of the GPU's slots in key tiles: waves x (tiles of a CTA, and
+        // about five for its start and end, ten with a merge over the cluster:
+        // 2.8, 7 and 14 thousand cycles)
+        const long long tiles = (ntiles + S - 1) / S;
+        const long long cost =
+            (std::max(1LL, jobs) + f.clusters[i] - 1) / f.clusters[i] * ((one ? (tiles + 1) / 2 : tiles) + (S > 1 ? 10 : 5));
         if (best < 0 || cost < best) best = cost, split = S;
     }
     if (split * blocks * a.s.Hk > INT_MAX) return cudaErrorInvalidValue;
@@ -695,10 +885,10 @@ cudaError_t launch(const PagedAttend& a, int max_kv, int sm_count, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_kv, int sm_count, cudaStream_t st) {
+cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_q, int max_kv, cudaStream_t st) {
     const bool scored = paged_scored(a);
-    if (head_dim == 64) return scored ? launch<64, true>(a, max_kv, sm_count, st) : launch<64, false>(a, max_kv, sm_count, st);
-    return scored ? launch<128, true>(a, max_kv, sm_count, st) : launch<128, false>(a, max_kv, sm_count, st);
+    if (head_dim == 64) return scored ? launch<64, true>(a, max_q, max_kv, st) : launch<64, false>(a, max_q, max_kv, st);
+    return scored ? launch<128, true>(a, max_q, max_kv, st) : launch<128, false>(a, max_q, max_kv, st);
 }
 
 }  // namespace kvp

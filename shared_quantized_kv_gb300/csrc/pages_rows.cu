@@ -97,11 +97,12 @@ pages_rows_kernel(const PagedAttend p) {
         b.blk = 0;
         b.q0 = pages::row_begin(s, b.seq);
         b.n = max(pages::row_begin(s, b.seq + 1) - b.q0, 0);
+        b.T = pages::held_tokens(s, b.seq);
         if (b.n == 0) return;  // the whole cluster's
     } else {
         if (!pages::find_block(s, p.G, kRows, blockIdx.x / S, b)) return;
     }
-    const int T = pages::held_tokens(s, b.seq);
+    const int T = b.T;
     const int32_t* table = s.table + (long long)b.seq * s.tstride;
 
     for (;; ++b.blk) {
