@@ -519,6 +519,29 @@ int kvpool_pages_attend(const kvpool_pages_t* pages, int layer, const kvpool_seq
                         long long q_stride, int q_heads, const kvpool_score_t* score, void* out, float* lse,
                         float softmax_scale, void* stream);
 
+/* Attention over a compressed pool layer followed by each sequence's own
+ * pages, in one softmax per row: kvpool_attend with private caches that are
+ * paged, of any length, and take chunks of new tokens. Row r of sequence s at
+ * position p sees every token the pool layer holds and its sequence's tokens
+ * up to p (the causal mask alone: positions count a sequence's own tokens).
+ * Rows from q_start[seqs] on see the pool alone. Q: bf16 [tokens][q_heads]
+ * [head_dim], contiguous; out: float [tokens][q_heads][head_dim]; both device,
+ * 16-byte aligned. The pages have the pool's kv_heads and head_dim;
+ * page_layer and pool_layer name the layer in each. workspace: device memory
+ * of at least kvpool_attend_pages_ws_bytes bytes, 16-byte aligned, scratch;
+ * calls that overlap on the GPU must not share one. The pool's max_rows bounds
+ * one token's rows here, not the call's: more tokens than max_rows / (q_heads
+ * / kv_heads) read the pool again for every such slice. Errors as
+ * kvpool_attend_ws and kvpool_pages_attend. Source: as kvpool_attend (PolyKV
+ * summary, section 2.A; CoMixKV article, recent states). */
+int kvpool_attend_pages(kvpool_t* pool, int pool_layer, const kvpool_pages_t* pages, int page_layer,
+                        const kvpool_seqs_t* seqs, const void* Q, int q_heads, float* out, float softmax_scale,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kvpool_attend_pages needs for `tokens` rows (0 for
+ * invalid arguments). */
+size_t kvpool_attend_pages_ws_bytes(const kvpool_t* pool, int tokens, int q_heads);
+
 /* Synchronise `stream`, then return and clear *pages->status: KVPOOL_OK,
  * KVPOOL_ERR_INVALID_ARG (a page number was out of range) or
  * KVPOOL_ERR_TIMEOUT. KVPOOL_ERR_INVALID_ARG too when status is NULL. */

@@ -27,6 +27,7 @@
 #include <vector>
 
 #include "kvpool_internal.cuh"
+#include "pages.cuh"
 
 // ----------------------------------------------------------- Lloyd-Max table
 namespace kvp {
@@ -639,6 +640,90 @@ int kvpool_attend_ws(kvpool_t* p, int layer, const void* Q, int agents, int q_he
         e = kvp::launch_merge_partials(nslice, pa.part_ml, pa.part_acc, p->kv_heads, p->head_dim, a, st,
                                        p->sm_count);
     if (e == cudaSuccess) p->wrote(stream, -1);
+    return map_cuda(e);
+}
+
+namespace {
+
+// kvpool_attend_pages takes the tokens in slices whose rows fit the pool's
+// row limit; its workspace holds the pages' (m, l) of all rows, then what
+// kvpool_attend_ws needs for a slice.
+struct PagesWs {
+    int slice;  // tokens per slice
+    size_t ml_bytes, bytes;
+};
+PagesWs pages_ws(const kvpool* p, long long tokens, int group) {
+    PagesWs w{(int)std::min<long long>(tokens, p->max_rows / group), 0, 0};
+    if (w.slice < 1) return w;
+    const WsLayout l = ws_layout(p, (long long)w.slice * group, group);
+    if (l.bytes == 0) return w;
+    w.ml_bytes = align256((size_t)p->kv_heads * tokens * group * 2 * sizeof(float));
+    // the last, shorter slice has fewer row groups and so may have more context slices
+    const long long last = tokens % w.slice;
+    const size_t tail = last ? ws_layout(p, last * group, group).bytes : 0;
+    w.bytes = w.ml_bytes + std::max(l.bytes, tail);
+    return w;
+}
+
+}  // namespace
+
+size_t kvpool_attend_pages_ws_bytes(const kvpool_t* p, int tokens, int q_heads) {
+    if (!p || tokens < 1 || q_heads < p->kv_heads || q_heads % p->kv_heads) return 0;
+    return pages_ws(p, tokens, q_heads / p->kv_heads).bytes;
+}
+
+int kvpool_attend_pages(kvpool_t* p, int pool_layer, const kvpool_pages_t* pages, int page_layer,
+                        const kvpool_seqs_t* seqs, const void* Q, int q_heads, float* out, float softmax_scale,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_layer(p, pool_layer);
+    if (rc) return rc;
+    if (!pages || pages->kv_heads != p->kv_heads || pages->head_dim != p->head_dim || !out || !aligned16(out))
+        return KVPOOL_ERR_INVALID_ARG;
+    kvp::PagedAttend pa{};
+    int max_q = 0, max_kv = 0;
+    rc = kvp::paged_attend_args(pages, page_layer, seqs, Q, (long long)q_heads * p->head_dim, q_heads, nullptr,
+                                softmax_scale, pa, max_q, max_kv);
+    if (rc) return rc;
+    const int group = q_heads / p->kv_heads, tokens = seqs->tokens;
+    if (group > p->max_rows) return KVPOOL_ERR_INVALID_ARG;
+    if (!p->compressed[pool_layer]) return KVPOOL_ERR_STATE;
+    const PagesWs w = pages_ws(p, tokens, group);
+    if (w.bytes == 0) return KVPOOL_ERR_UNSUPPORTED;  // more row groups than one wave of CTAs
+    if (!workspace || !aligned16(workspace) || workspace_bytes < w.bytes) return KVPOOL_ERR_INVALID_ARG;
+    // The pages' states of all rows: accumulators into out, (m, l) into the
+    // workspace (0 for rows of no sequence); then slice by slice the pool's
+    // attention, whose merge joins them as it joins tails.
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    float* ml = static_cast<float*>(workspace);
+    pa.st_acc = out;
+    pa.st_ml = ml;
+    pa.st_tokens = w.slice;
+    cudaError_t e = cudaMemsetAsync(ml, 0, w.ml_bytes, st);
+    if (e == cudaSuccess) e = kvp::launch_pages_attend(pa, p->head_dim, max_q, max_kv, p->sm_count, st);
+    const size_t row = (size_t)q_heads * p->head_dim;
+    for (int t0 = 0; t0 < tokens && e == cudaSuccess; t0 += w.slice) {
+        const int n = std::min(w.slice, tokens - t0);
+        kvp::AttendArgs a;
+        rc = attend_args(p, pool_layer, static_cast<const uint16_t*>(Q) + t0 * row, n, q_heads, nullptr, out + t0 * row,
+                         softmax_scale, stream, a);
+        if (rc) return rc;
+        const WsLayout l = ws_layout(p, a.rows, group);
+        unsigned char* at = static_cast<unsigned char*>(workspace) + w.ml_bytes;
+        kvp::AttendArgs part = a;
+        part.part_ml = reinterpret_cast<float*>(at);
+        part.part_acc = reinterpret_cast<float*>(at + l.acc_off);
+        part.ws_ctas = p->sm_count;
+        part.ws_nslice_max = (int)l.nslice_max;
+        int nslice = 0;
+        part.ws_nslice = &nslice;
+        e = kvp::launch_attend_tc(p->shape_of(pool_layer), p->layer(pool_layer), part, p->status, p->sm_count, st);
+        if (e == cudaSuccess && (nslice < 1 || nslice > l.nslice_max)) e = cudaErrorInvalidValue;
+        a.ws_tail_ml = ml + 2 * (size_t)t0 * group * p->kv_heads;
+        if (e == cudaSuccess)
+            e = kvp::launch_merge_partials(nslice, part.part_ml, part.part_acc, p->kv_heads, p->head_dim, a, st,
+                                           p->sm_count);
+        if (e == cudaSuccess) p->wrote(stream, -1);
+    }
     return map_cuda(e);
 }
 

@@ -185,6 +185,58 @@ kvp::PagedSeqs seqs_view(const kvpool_pages_t* pg, const kvpool_seqs_t* s) {
 
 }  // namespace
 
+int kvp::paged_attend_args(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t* seqs, const void* Q,
+                           long long q_stride, int q_heads, const kvpool_score_t* score, float softmax_scale,
+                           PagedAttend& a, int& max_q, int& max_kv) {
+    int rc = check_pages(pg, layer);
+    if (rc) return rc;
+    rc = check_seqs(seqs);
+    if (rc) return rc;
+    if (!Q || !aligned(Q, 16)) return KVPOOL_ERR_INVALID_ARG;
+    if (q_heads < pg->kv_heads || q_heads % pg->kv_heads || q_stride % 8 ||
+        q_stride < (long long)q_heads * pg->head_dim)
+        return KVPOOL_ERR_INVALID_ARG;
+    if (!(softmax_scale >= 0.0f) || isinf(softmax_scale)) return KVPOOL_ERR_INVALID_ARG;
+    if (score && (!(score->cap >= 0.0f) || isinf(score->cap) || score->window < 0 || !aligned(score->slopes, 4) ||
+                  !aligned(score->first, 4) || !aligned(score->prefix, 4)))
+        return KVPOOL_ERR_INVALID_ARG;
+    const int group = q_heads / pg->kv_heads;
+    // rows (tokens x heads of a group) are counted in 31 bits, a group in 16
+    if ((long long)seqs->tokens * group > (1LL << 31) - 1024 || group > 65535) return KVPOOL_ERR_INVALID_ARG;
+    a = PagedAttend{};
+    a.s = seqs_view(pg, seqs);
+    const long long at = layer * layer_elems(pg);
+    a.K = static_cast<const uint16_t*>(pg->K) + at;
+    a.V = static_cast<const uint16_t*>(pg->V) + at;
+    a.Q = static_cast<const uint16_t*>(Q);
+    a.q_stride = q_stride;
+    a.Hq = q_heads;
+    a.G = group;
+    a.g_magic = (uint32_t)(((1ull << 32) + group - 1) / group);
+    const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf((float)pg->head_dim);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    if (score) {
+        if (score->cap > 0.0f) {
+            a.cap2 = score->cap * 1.4426950408889634f;
+            a.cap_in = 2.0f * 1.4426950408889634f * scale / score->cap;
+        }
+        a.slopes = score->slopes;
+        a.window = score->window;
+        a.first = score->first;
+        a.prefix = score->prefix;
+    }
+    const long long room = std::min<long long>((long long)seqs->table_stride * pg->page_tokens, 1LL << 30);
+    max_kv = (int)(seqs->max_kv > 0 ? std::min<long long>(seqs->max_kv, room) : room);
+    max_q = seqs->max_q > 0 ? std::min(seqs->max_q, seqs->tokens) : seqs->tokens;
+    return KVPOOL_OK;
+}
+
+cudaError_t kvp::launch_pages_attend(const PagedAttend& a, int head_dim, int max_q, int max_kv, int sm_count,
+                                     cudaStream_t st) {
+    if ((long long)max_q * a.G > 16) return launch_pages_chunk(a, head_dim, max_q, max_kv, st);
+    return launch_pages_rows(a, head_dim, max_q, max_kv, sm_count, st);
+}
+
 extern "C" {
 
 int kvpool_pages_append(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t* seqs, const void* K,
@@ -250,54 +302,17 @@ int kvpool_pages_copy(const kvpool_pages_t* pg, const int32_t* src, const int32_
 int kvpool_pages_attend(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t* seqs, const void* Q,
                         long long q_stride, int q_heads, const kvpool_score_t* score, void* out, float* lse,
                         float softmax_scale, void* stream) {
-    int rc = check_pages(pg, layer);
+    kvp::PagedAttend a{};
+    int max_q = 0, max_kv = 0, sms = 0;
+    int rc = kvp::paged_attend_args(pg, layer, seqs, Q, q_stride, q_heads, score, softmax_scale, a, max_q, max_kv);
     if (rc) return rc;
-    rc = check_seqs(seqs);
-    if (rc) return rc;
-    if (!Q || !out || !aligned(Q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return KVPOOL_ERR_INVALID_ARG;
-    if (q_heads < pg->kv_heads || q_heads % pg->kv_heads || q_stride % 8 ||
-        q_stride < (long long)q_heads * pg->head_dim)
-        return KVPOOL_ERR_INVALID_ARG;
-    if (!(softmax_scale >= 0.0f) || isinf(softmax_scale)) return KVPOOL_ERR_INVALID_ARG;
-    if (score && (!(score->cap >= 0.0f) || isinf(score->cap) || score->window < 0 || !aligned(score->slopes, 4) ||
-                  !aligned(score->first, 4) || !aligned(score->prefix, 4)))
-        return KVPOOL_ERR_INVALID_ARG;
-    const int group = q_heads / pg->kv_heads;
-    // rows (tokens x heads of a group) are counted in 31 bits
-    if ((long long)seqs->tokens * group > (1LL << 31) - 1024) return KVPOOL_ERR_INVALID_ARG;
-    int sms = 0;
+    if (!out || !aligned(out, 16) || !aligned(lse, 4)) return KVPOOL_ERR_INVALID_ARG;
     rc = check_device(sms);
     if (rc) return rc;
-    kvp::PagedAttend a{};
-    a.s = seqs_view(pg, seqs);
-    const long long at = layer * layer_elems(pg);
-    a.K = static_cast<const uint16_t*>(pg->K) + at;
-    a.V = static_cast<const uint16_t*>(pg->V) + at;
-    a.Q = static_cast<const uint16_t*>(Q);
-    a.q_stride = q_stride;
-    a.Hq = q_heads;
-    a.G = group;
-    a.g_magic = (uint32_t)(((1ull << 32) + group - 1) / group);
-    const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf((float)pg->head_dim);
-    a.scale_log2 = scale * 1.4426950408889634f;
-    if (score) {
-        if (score->cap > 0.0f) {
-            a.cap2 = score->cap * 1.4426950408889634f;
-            a.cap_in = 2.0f * 1.4426950408889634f * scale / score->cap;
-        }
-        a.slopes = score->slopes;
-        a.window = score->window;
-        a.first = score->first;
-        a.prefix = score->prefix;
-    }
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    const long long room = (long long)seqs->table_stride * pg->page_tokens;
-    const int max_kv = (int)std::min<long long>(seqs->max_kv > 0 ? std::min<long long>(seqs->max_kv, room) : room, 1LL << 30);
-    const int max_q = seqs->max_q > 0 ? std::min(seqs->max_q, seqs->tokens) : seqs->tokens;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((long long)max_q * group > 16) return map_cuda(kvp::launch_pages_chunk(a, pg->head_dim, max_q, max_kv, st));
-    return map_cuda(kvp::launch_pages_rows(a, pg->head_dim, max_q, max_kv, sms, st));
+    return map_cuda(
+        kvp::launch_pages_attend(a, pg->head_dim, max_q, max_kv, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int kvpool_pages_status(const kvpool_pages_t* pg, void* stream) {

@@ -62,6 +62,14 @@ cudaError_t launch_pages_append(const PagedSeqs& s, int head_dim, uint16_t* Kp, 
 // pages_chunk.cu: many); max_q, max_kv as in kvpool_seqs_t, but never 0.
 cudaError_t launch_pages_rows(const PagedAttend& a, int head_dim, int max_q, int max_kv, int sm_count,
                               cudaStream_t st);
+// What both entry points that attend over pages check and hand on: `a` without
+// its outputs; hints of 0 replaced.
+int paged_attend_args(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t* seqs, const void* Q,
+                      long long q_stride, int q_heads, const kvpool_score_t* score, float softmax_scale, PagedAttend& a,
+                      int& max_q, int& max_kv);
+// Chooses the kernel; sm_count of the current (sm_103) device.
+cudaError_t launch_pages_attend(const PagedAttend& a, int head_dim, int max_q, int max_kv, int sm_count,
+                                cudaStream_t st);
 cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_q, int max_kv, cudaStream_t st);
 
 namespace pages {
@@ -153,6 +161,14 @@ __device__ __forceinline__ Seen row_seen(const PagedAttend& a, int seq, int tok,
         }
     }
     return r;
+}
+
+// Where the state (m, l) of token row t and query head hd goes.
+__device__ __forceinline__ float2* state_ml(const PagedAttend& a, int t, int hd) {
+    const int sl = t / a.st_tokens, tl = t - sl * a.st_tokens, g = hd / a.G;
+    const int in = min(a.st_tokens, a.s.tokens - sl * a.st_tokens);  // tokens of the slice
+    return reinterpret_cast<float2*>(a.st_ml) + (long long)sl * a.st_tokens * a.G * a.s.Hk +
+           ((long long)g * in + tl) * a.G + (hd - g * a.G);
 }
 
 // <q, k> -> the score in log2 units. tanh(y) = 1 - 2 / (e^(2y) + 1): off by a

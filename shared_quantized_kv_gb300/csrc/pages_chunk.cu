@@ -49,7 +49,7 @@ constexpr int kRows = 2 * kTile;        // rows per CTA
 constexpr int kFewTiles = 8;            // key tiles that a cluster does not split
 constexpr int kMaxParts = 16;           // states of a row: 8 CTAs, 2 slots
 constexpr float kLazyMax = 8.0f;        // log2 units the reference may trail the maximum
-constexpr uint32_t kTryNs = 1000, kTries = 1u << 20;
+constexpr uint32_t kTryNs = 1000, kTries = 1u << 18;
 constexpr uint32_t kCols = 512;         // tensor memory: S0, S1, O0, O1
 // named barriers: Q is staged (issuers and softmax warps); every role is done; the merge rows are written;
 // a slot's turn at the tensor cores; both slots' stores of 32 rows are done
@@ -87,7 +87,7 @@ __device__ __forceinline__ int k_entry(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_entry(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
 
 // Wait for phase `parity` of the barrier by a whole warp; after kTries tries
-// (each suspends the warp for a while; about a second in all) `bad` is set, and
+// (each suspends the warp for a while; about a quarter of a second in all) `bad` is set, and
 // no wait after that waits. One short loop: what is around a wait is on the
 // main loop's critical path.
 __device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, bool& bad) {
@@ -112,7 +112,10 @@ __device__ __forceinline__ uint32_t span_bits(int a, int b, int c) {
     return upto & ~(x == 32 ? 0xffffffffu : (1u << x) - 1u);
 }
 
-template <int D, bool SCORED>
+// STATE: the rows' states for a merge instead of the output; the weights then
+// go through the product with V as bf16 hi and lo (16 bits; lo in the half of
+// S's columns that hi leaves), as the merged output is float32.
+template <int D, bool SCORED, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1)
 pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const PagedAttend p) {
@@ -312,9 +315,12 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         ptx::tc_fence_after();
                     }
 #pragma unroll
-                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks)  // P of half h: 32 columns from column 64 h on
+                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks) {  // P of half h: 32 columns from column 64 h on
                         ptx::mma_f16_ta_lead(lead, tO, tS + 32 * h + ks * 8, dv + ks * (2048 >> 4), idO,
                                              (it > 0 || ks > 0) ? 1u : 0u);
+                        if constexpr (STATE)
+                            ptx::mma_f16_ta_lead(lead, tO, tS + 32 * h + ks * 8 + 32, dv + ks * (2048 >> 4), idO, 1u);
+                    }
                     ptx::mma_commit_lead(lead, u_o);
                 }
             };
@@ -490,7 +496,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const int k0 = t0 + 64 * h;  // first key of the half
                 const uint32_t tSh = tS + 64 * h;
                 const bool whole = __all_sync(0xffffffffu, see.all(k0, k0 + 64));
-                uint32_t pw[2][16];
+                uint32_t pw[2][16], pl[STATE ? 2 : 1][16];  // (pl: STATE)
                 float2 sum[2];
 #pragma unroll 1
                 for (;;) {
@@ -525,6 +531,8 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                             const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
                             sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                             pw[c][k] = pack_bf2(e.x, e.y);
+                            if constexpr (STATE)
+                                pl[c][k] = pack_bf2(e.x - asf(pw[c][k] << 16), e.y - asf(pw[c][k] & 0xFFFF0000u));
                         }
                     };
                     uint32_t u0[32], u1[32];  // the second chunk is on its way while the first is worked on
@@ -561,7 +569,10 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 // P over the half's own columns of S
 #pragma unroll
-                for (int c = 0; c < 2; ++c) ptx::tmem_st16(tSh + 16 * c, pw[c]);
+                for (int c = 0; c < 2; ++c) {
+                    ptx::tmem_st16(tSh + 16 * c, pw[c]);
+                    if constexpr (STATE) ptx::tmem_st16(tSh + 32 + 16 * c, pl[c]);
+                }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -591,30 +602,47 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                                           two || all ? 1 : 2, cm, cl, acc);
         };
         bool odd = live && l != 0.0f && !finite(l);  // sums that a masked key may have spoilt
+        // a row's last numbers: m and l, or their logarithm
+        auto finish = [&](int t, int hd, float rm, float rl) {
+            if constexpr (STATE)
+                *pages::state_ml(p, t, hd) = make_float2(rm, rl);
+            else if (p.lse)
+                p.lse[(long long)t * p.Hq + hd] = rl == 0.0f ? -CUDART_INF_F : (rm + log2f(rl)) * kLn2;
+        };
         // rows `odds` of the warp again, over the CTA's tiles, and their output
         auto again = [&](unsigned odds) {
             for (; odds; odds &= odds - 1) {
                 const int of = __ffs(odds) - 1;
                 float cm, cl, acc[D / 32];
                 careful(of, true, cm, cl, acc);
-                const long long at = (long long)__shfl_sync(0xffffffffu, tok, of) * p.Hq +
-                                     __shfl_sync(0xffffffffu, head, of);
+                const int ct = __shfl_sync(0xffffffffu, tok, of), ch = __shfl_sync(0xffffffffu, head, of);
+                const long long at = ((long long)ct * p.Hq + ch) * D + lane * (D / 32);
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e)
-                    p.out[at * D + lane * (D / 32) + e] =
-                        cl == 0.0f ? (uint16_t)0 : __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] / cl));
-                if (lane == 0 && p.lse) p.lse[at] = cl == 0.0f ? -CUDART_INF_F : (cm + log2f(cl)) * kLn2;
+                for (int e = 0; e < D / 32; ++e) {
+                    if constexpr (STATE) p.st_acc[at + e] = acc[e];
+                    else p.out[at + e] = cl == 0.0f ? (uint16_t)0 : __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] / cl));
+                }
+                if (lane == 0) finish(ct, ch, cm, cl);
             }
         };
-        auto store8 = [&](uint16_t* dst, const float (&y)[32], int k) {
-            *reinterpret_cast<uint4*>(dst + k) =
-                make_uint4(pack_bf2(y[k], y[k + 1]), pack_bf2(y[k + 2], y[k + 3]), pack_bf2(y[k + 4], y[k + 5]),
-                           pack_bf2(y[k + 6], y[k + 7]));
+        // 32 channels from c on of this thread's row
+        auto store32 = [&](int c, const float (&y)[32]) {
+            const long long at = ((long long)tok * p.Hq + head) * D + c;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+                if constexpr (STATE) {
+                    *reinterpret_cast<float4*>(p.st_acc + at + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                    *reinterpret_cast<float4*>(p.st_acc + at + k + 4) = make_float4(y[k + 4], y[k + 5], y[k + 6], y[k + 7]);
+                } else {
+                    *reinterpret_cast<uint4*>(p.out + at + k) =
+                        make_uint4(pack_bf2(y[k], y[k + 1]), pack_bf2(y[k + 2], y[k + 3]), pack_bf2(y[k + 4], y[k + 5]),
+                                   pack_bf2(y[k + 6], y[k + 7]));
+                }
+            }
         };
-        uint16_t* orow = p.out + ((long long)tok * p.Hq + head) * D;
         if (direct && two) {
             // a row's thread writes its output
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float inv = STATE ? 1.0f : 1.0f / l;  // (not used where l is 0)
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -626,13 +654,9 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     odd = odd || (live && l != 0.0f && !finite(asf(o[k])));
                     y[k] = l == 0.0f ? 0.0f : asf(o[k]) * inv;
                 }
-                if (live) {  // (odd rows are written again)
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8) store8(orow + c, y, k);
-                }
+                if (live) store32(c, y);  // (odd rows are written again)
             }
-            if (live && p.lse)
-                p.lse[(long long)tok * p.Hq + head] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+            if (live) finish(tok, head, l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m), l);
             __syncwarp();
             again(__ballot_sync(0xffffffffu, odd));
         } else if (direct) {
@@ -670,7 +694,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const float M = fmaxf(ml.x, ml.z);
             const float f0 = ml.y == 0.0f ? 0.0f : ptx::ex2(ml.x - M), f1 = ml.w == 0.0f ? 0.0f : ptx::ex2(ml.z - M);
             const float Lt = fmaf(f0, ml.y, f1 * ml.w);
-            const float inv = Lt == 0.0f ? 0.0f : 1.0f / Lt;
+            const float inv = STATE ? 1.0f : Lt == 0.0f ? 0.0f : 1.0f / Lt;
             const float fm = (w ? f1 : f0) * inv, fo = (w ? f0 : f1) * inv;  // own and other slot's weight
             const bool none = (w ? ml.w : ml.y) == 0.0f, onone = (w ? ml.y : ml.w) == 0.0f;
             odd = live && Lt != 0.0f && !finite(Lt);
@@ -685,13 +709,9 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     for (int e = 0; e < 4; ++e)
                         y[k + e] = (none ? 0.0f : asf(keep[c + k + e]) * fm) + (onone ? 0.0f : ov[e] * fo);
                 }
-                if (live) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8) store8(orow + w * HC + c, y, k);
-                }
+                if (live) store32(w * HC + c, y);
             }
-            if (live && p.lse && !w)
-                p.lse[(long long)tok * p.Hq + head] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * kLn2;
+            if (live && !w) finish(tok, head, M, Lt);
             if (__any_sync(0xffffffffu, odd)) {
                 ptx::bar_sync(kBarOdd + (warp & 3), 64);  // after both halves' stores
                 if (!w) again(__ballot_sync(0xffffffffu, odd));
@@ -745,9 +765,9 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         auto state = [&](int r, int k) {
             return ptx::dsmem_addr(rows + (r0 + r + (k % slots) * kTile) * L::rs, k / slots);
         };
-        auto out_row = [&](int r) {
+        auto out_at = [&](int r) {  // the share's row r: token row and head
             const int i = pages::div_group(p, j_begin + r0 + r);
-            return (long long)(b.q0 + i_begin + i) * p.Hq + g * p.G + j_begin + r0 + r - i * p.G;
+            return make_int2(b.q0 + i_begin + i, g * p.G + j_begin + r0 + r - i * p.G);
         };
         for (int r = tid; r < cnt; r += kThreads) {
             float2 ml[kMaxParts];
@@ -762,11 +782,15 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 ml[k].x = ml[k].y == 0.0f ? 0.0f : ptx::ex2(ml[k].x - M);  // a state of nothing: 0
                 Lt = fmaf(ml[k].x, ml[k].y, Lt);
             }
-            const float inv = Lt == 0.0f ? 0.0f : 1.0f / Lt;
+            const float inv = STATE ? 1.0f : Lt == 0.0f ? 0.0f : 1.0f / Lt;
 #pragma unroll
             for (int k = 0; k < kMaxParts; ++k)
                 if (k < parts) weights[r * parts + k] = ml[k].y == 0.0f ? -1.0f : ml[k].x * inv;
-            if (p.lse) p.lse[out_row(r)] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * kLn2;
+            const int2 at = out_at(r);
+            if constexpr (STATE)
+                *pages::state_ml(p, at.x, at.y) = make_float2(M, Lt);
+            else if (p.lse)
+                p.lse[(long long)at.x * p.Hq + at.y] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * kLn2;
         }
         __syncthreads();
         constexpr int C4 = D / 4;
@@ -792,7 +816,10 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     a.z = fmaf(f[u], v[u].z, a.z), a.w = fmaf(f[u], v[u].w, a.w);
                 }
             }
-            *reinterpret_cast<uint2*>(p.out + out_row(r) * D + c4 * 4) = make_uint2(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w));
+            const int2 ot = out_at(r);
+            const long long at = ((long long)ot.x * p.Hq + ot.y) * D + c4 * 4;
+            if constexpr (STATE) *reinterpret_cast<float4*>(p.st_acc + at) = a;
+            else *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w));
         }
         if (S > 1) {  // no CTA goes away while another reads its rows
             ptx::cluster_arrive();
@@ -814,10 +841,10 @@ struct Fit {
     cudaError_t err;
     int clusters[4];
 };
-template <int D, bool SCORED>
+template <int D, bool SCORED, bool STATE>
 const Fit& fit() {
     static const Fit f = [] {
-        auto kern = pages_chunk_kernel<D, SCORED>;
+        auto kern = pages_chunk_kernel<D, SCORED, STATE>;
         Fit x{cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::total), {}};
         for (int i = 0; i < 4 && x.err == cudaSuccess; ++i) {
             cudaLaunchConfig_t cfg = {};
@@ -838,9 +865,9 @@ const Fit& fit() {
     return f;
 }
 
-template <int D, bool SCORED>
+template <int D, bool SCORED, bool STATE>
 cudaError_t launch(const PagedAttend& a, int max_q, int max_kv, cudaStream_t st) {
-    const Fit& f = fit<D, SCORED>();
+    const Fit& f = fit<D, SCORED, STATE>();
     if (f.err != cudaSuccess) return f.err;
     const long long rows = (long long)a.s.tokens * a.G;
     const long long blocks = rows / kRows + a.s.seqs;  // at least as many as there are
@@ -880,15 +907,19 @@ cudaError_t launch(const PagedAttend& a, int max_q, int max_kv, cudaStream_t st)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, pages_chunk_kernel<D, SCORED>, kmap, vmap, a);
+    return cudaLaunchKernelEx(&cfg, pages_chunk_kernel<D, SCORED, STATE>, kmap, vmap, a);
 }
 
 }  // namespace
 
 cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_q, int max_kv, cudaStream_t st) {
     const bool scored = paged_scored(a);
-    if (head_dim == 64) return scored ? launch<64, true>(a, max_q, max_kv, st) : launch<64, false>(a, max_q, max_kv, st);
-    return scored ? launch<128, true>(a, max_q, max_kv, st) : launch<128, false>(a, max_q, max_kv, st);
+    if (a.st_acc != nullptr)
+        return head_dim == 64 ? launch<64, false, true>(a, max_q, max_kv, st)
+                              : launch<128, false, true>(a, max_q, max_kv, st);
+    if (head_dim == 64)
+        return scored ? launch<64, true, false>(a, max_q, max_kv, st) : launch<64, false, false>(a, max_q, max_kv, st);
+    return scored ? launch<128, true, false>(a, max_q, max_kv, st) : launch<128, false, false>(a, max_q, max_kv, st);
 }
 
 }  // namespace kvp

@@ -327,14 +327,7 @@ pages_rows_kernel(const PagedAttend p) {
             const long long row = (long long)t * p.Hq + hd;
             if constexpr (STATE) {
                 *reinterpret_cast<float4*>(p.st_acc + row * D + c4 * 4) = a;
-                if (c4 == 0) {
-                    const int sl = t / p.st_tokens, tl = t - sl * p.st_tokens;
-                    const int in = min(p.st_tokens, s.tokens - sl * p.st_tokens);
-                    float* ml = p.st_ml + 2 * ((long long)sl * p.st_tokens * p.G * s.Hk +
-                                               ((long long)g * in + tl) * p.G + (hd - g * p.G));
-                    ml[0] = M;
-                    ml[1] = L;
-                }
+                if (c4 == 0) *pages::state_ml(p, t, hd) = make_float2(M, L);
             } else {
                 const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                 *reinterpret_cast<uint2*>(p.out + row * D + c4 * 4) =

@@ -122,6 +122,10 @@ _SIGS = {
     "kvpool_pages_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p]),
+    "kvpool_attend_pages": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                           ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "kvpool_attend_pages_ws_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int]),
     "kvpool_pages_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "kvpool_pager_create": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int, ctypes.c_int]),
     "kvpool_pager_destroy": (None, [ctypes.c_void_p]),
@@ -444,6 +448,110 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
     return out if lse is None else (out, lse)
 
 
+class PagedCache:
+    """The agents' private caches: bf16 pages of every layer (K, V tensors
+    [layers, pages, kv_heads, page_tokens, head_dim]) on the current CUDA
+    device, and the pager that says whose they are. Page copies that a fork or
+    a compaction makes due are enqueued before the call returns."""
+
+    def __init__(self, layers, kv_heads, head_dim, pages, page_tokens=64):
+        import torch
+
+        self.pager = Pager(pages, page_tokens)
+        shape = (layers, pages, kv_heads, page_tokens, head_dim)
+        self.K = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        self.V = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        self.status_word = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.page_tokens = page_tokens
+
+    def close(self):
+        self.pager.close()
+
+    def new(self) -> int:
+        """A new empty sequence's number."""
+        return self.pager.new()
+
+    def fork(self, seq) -> int:
+        """A new sequence with seq's tokens, which stay shared until one of the two writes."""
+        return self.pager.fork(seq)
+
+    def free(self, seq):
+        """End a sequence; pages that no other owns are free."""
+        self.pager.free(seq)
+
+    def truncate(self, seq, length):
+        """Cut a sequence to its first `length` tokens."""
+        self.pager.truncate(seq, length)
+
+    def compact(self, stream=None):
+        """Move owned pages into the lowest numbers; how many moved. Batches
+        made before are void."""
+        src, dst = self.pager.compact()
+        pages_copy(self.K, self.V, src, dst, stream)
+        return len(src)
+
+    def grow(self, seqs, counts, stream=None):
+        """Room for counts[i] new tokens at the end of seqs[i]: the batch that
+        append and attend take, rows in this order. Fewer free pages than it
+        takes: KVPoolError (OOM), and no sequence has grown."""
+        if len(seqs) != len(counts) or not len(seqs) or len(set(seqs)) != len(seqs):
+            raise ValueError("one count per sequence, each sequence once")
+        before = [self.pager.length(s) for s in seqs]
+        src, dst = [], []
+        try:
+            for s, n in zip(seqs, counts):
+                pair = self.pager.extend(s, n)
+                if pair:
+                    src.append(pair[0])
+                    dst.append(pair[1])
+        except KVPoolError:
+            # (a page of its own that a sequence got already is copied below and kept)
+            for s, n in zip(seqs, before):
+                self.pager.truncate(s, n)
+            live = [(a, b) for a, b in zip(src, dst) if self.pager.owners(b)]
+            pages_copy(self.K, self.V, [a for a, _ in live], [b for _, b in live], stream)
+            raise
+        pages_copy(self.K, self.V, src, dst, stream)
+        return PagedBatch(self, seqs, counts, stream)
+
+    def append(self, layer, K, V, batch, stream=None):
+        """Write the batch's new tokens: K, V bf16 [tokens, kv_heads, d]."""
+        pages_append(self.K, self.V, layer, K, V, batch.table, batch.kv_len, batch.q_start, self.status_word, stream)
+
+    def attend(self, layer, Q, batch, **options):
+        """pages_attend of the batch's new tokens over their sequences."""
+        return pages_attend(self.K, self.V, layer, Q, batch.table, batch.kv_len, batch.q_start, batch.max_q,
+                            batch.max_kv, status=self.status_word, **options)
+
+    def status(self, stream=None) -> int:
+        """Synchronise and return (and clear) the device status code of the pages' calls."""
+        pg = _pages(self.K, self.V, self.status_word)
+        return int(_lib().kvpool_pages_status(ctypes.byref(pg), _stream_ptr(stream)))
+
+
+class PagedBatch:
+    """The sequences of one step, as the calls take them: table, kv_len and
+    q_start (device), max_q and max_kv (host)."""
+
+    def __init__(self, cache, seqs, counts, stream=None):
+        import torch
+
+        tables = [cache.pager.table(s) for s in seqs]
+        lens = [cache.pager.length(s) for s in seqs]
+        width = max(1, max(len(t) for t in tables))
+        start = [0]
+        for n in counts:
+            start.append(start[-1] + n)
+        host = torch.tensor([x for t in tables for x in t + [-1] * (width - len(t))] + lens + start, dtype=torch.int32)
+        with torch.cuda.stream(stream):
+            dev = host.to(cache.K.device)  # one copy
+        n = len(seqs)
+        self.table = dev[: n * width].view(n, width)
+        self.kv_len = dev[n * width: n * width + n]
+        self.q_start = dev[n * width + n:]
+        self.tokens, self.max_q, self.max_kv = start[-1], max(counts), max(lens)
+
+
 class KVPool:
     """One shared pool (a ``kvpool_t``) on the current CUDA device."""
 
@@ -572,6 +680,37 @@ class KVPool:
                                        _dev_ptr(out, torch.float32, "out"), softmax_scale,
                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                        _stream_ptr(stream)), "kvpool_attend_ws")
+        return out
+
+    def attend_pages_ws_bytes(self, tokens, q_heads) -> int:
+        """Workspace bytes kvpool_attend_pages needs for this many tokens."""
+        return int(_lib().kvpool_attend_pages_ws_bytes(self._h, int(tokens), int(q_heads)))
+
+    def attend_pages(self, layer, Q, cache, batch, page_layer=None, workspace=None, out=None, softmax_scale=0.0,
+                     stream=None):
+        """kvpool_attend_pages: the new tokens of a PagedCache's batch over this
+        pool's layer and their own pages (page_layer, by default the same
+        number). Q: bf16 [tokens, q_heads, d]. Returns out: float32, like Q."""
+        import torch
+
+        n, hq, d = Q.shape
+        pg = _pages(cache.K, cache.V, cache.status_word)
+        if d != pg.head_dim:
+            raise ValueError("Q must be [tokens, q_heads, head_dim]")
+        sq = _seqs(batch.table, batch.kv_len, batch.q_start, n, batch.max_q, batch.max_kv)
+        _one_device(("Q", Q), ("out", out), ("workspace", workspace))
+        if out is not None and tuple(out.shape) != (n, hq, d):
+            raise ValueError(f"out must have shape {(n, hq, d)}")
+        with torch.cuda.stream(stream):  # on the stream that uses them, so that the allocator knows it
+            if out is None:
+                out = torch.empty((n, hq, d), dtype=torch.float32, device=Q.device)
+            if workspace is None:
+                workspace = torch.empty(max(self.attend_pages_ws_bytes(n, hq), 16), dtype=torch.uint8, device=Q.device)
+        _check(_lib().kvpool_attend_pages(self._h, layer, ctypes.byref(pg), layer if page_layer is None else page_layer,
+                                          ctypes.byref(sq), _dev_ptr(Q, torch.bfloat16, "Q"), hq,
+                                          _dev_ptr(out, torch.float32, "out"), softmax_scale, workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+               "kvpool_attend_pages")
         return out
 
     def attend_partial(self, layer, Q, t_begin, t_end, ml=None, acc=None, softmax_scale=0.0, stream=None):
