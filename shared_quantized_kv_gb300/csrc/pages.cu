@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <new>
 #include <vector>
 
@@ -151,15 +152,25 @@ int check_seqs(const kvpool_seqs_t* s) {
     return KVPOOL_OK;
 }
 
-// The current device: sm_103 or KVPOOL_ERR_UNSUPPORTED; its SM count.
+// The current device: sm_103 or KVPOOL_ERR_UNSUPPORTED; its SM count (asked
+// for once per device: a device's properties do not change).
+constexpr int kMaxDevices = 64;
 int check_device(int& sms) {
-    int dev = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return KVPOOL_ERR_UNSUPPORTED;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return KVPOOL_ERR_CUDA;
-    return major * 10 + minor == 103 ? KVPOOL_OK : KVPOOL_ERR_UNSUPPORTED;
+    static std::atomic<int> known[kMaxDevices];  // SM count, -1 for another architecture, 0 not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return KVPOOL_ERR_UNSUPPORTED;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return KVPOOL_ERR_CUDA;
+        if (major * 10 + minor != 103) n = -1;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    sms = n;
+    return n > 0 ? KVPOOL_OK : KVPOOL_ERR_UNSUPPORTED;
 }
 
 int map_cuda(cudaError_t e) { return e == cudaSuccess ? KVPOOL_OK : KVPOOL_ERR_CUDA; }

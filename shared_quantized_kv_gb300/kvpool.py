@@ -8,6 +8,7 @@ device is not an sm_103 GPU the calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -330,48 +331,66 @@ class Pager:
         return self._count(_lib().kvpool_pager_owners(self._h, page), "kvpool_pager_owners")
 
 
-def _one_device(*named):
-    """The tensors given, in order, are on the current CUDA device."""
+def _here():
+    """The current CUDA device's number."""
     import torch
 
-    dev = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and (t.device.type != "cuda" or t.device.index != dev):
-            raise ValueError(f"{name} must be on the current CUDA device ({dev}), not {t.device}")
+    return torch.cuda.current_device()
 
 
-def _pages(K_pages, V_pages, status=None):
+def _need(t, dtype, name, dev):
+    """Address of a contiguous tensor of dtype on device dev (these calls are
+    short: a step makes one per layer)."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dtype} on the current CUDA device ({dev}), "
+                         f"not {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    """cudaStream_t of `stream`, or of the current stream."""
     import torch
 
-    if K_pages.dim() != 5 or V_pages.shape != K_pages.shape:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device.index != dev:
+        raise ValueError(f"stream must be one of the current CUDA device ({dev})")
+    return stream.cuda_stream
+
+
+def _pages(K_pages, V_pages, status=None, dev=None):
+    import torch
+
+    dev = _here() if dev is None else dev
+    shape = K_pages.shape
+    if len(shape) != 5 or V_pages.shape != shape:
         raise ValueError("K_pages and V_pages must be [layers, pages, kv_heads, page_tokens, head_dim]")
-    L, n, hk, P, d = K_pages.shape
-    kp, vp = _dev_ptr(K_pages, torch.bfloat16, "K_pages"), _dev_ptr(V_pages, torch.bfloat16, "V_pages")
-    _one_device(("K_pages", K_pages), ("V_pages", V_pages), ("status", status))
-    return Pages(kp.value, vp.value, L, n, hk, P, d, None if status is None else
-                 _dev_ptr(status, torch.int32, "status").value)
+    return Pages(_need(K_pages, torch.bfloat16, "K_pages", dev), _need(V_pages, torch.bfloat16, "V_pages", dev), *shape,
+                 None if status is None else _need(status, torch.int32, "status", dev))
 
 
-def _seqs(table, kv_len, q_start, tokens, max_q, max_kv):
+def _seqs(table, kv_len, q_start, tokens, max_q, max_kv, dev=None):
     import torch
 
-    if table.dim() != 2 or kv_len.shape != (table.shape[0],) or q_start.shape != (table.shape[0] + 1,):
+    dev = _here() if dev is None else dev
+    shape = table.shape
+    if len(shape) != 2 or kv_len.shape != shape[:1] or q_start.dim() != 1 or q_start.shape[0] != shape[0] + 1:
         raise ValueError("table [seqs, pages], kv_len [seqs] and q_start [seqs + 1] do not fit together")
-    _one_device(("table", table), ("kv_len", kv_len), ("q_start", q_start))
-    return Seqs(table.shape[0], table.shape[1], _dev_ptr(table, torch.int32, "table").value,
-                _dev_ptr(kv_len, torch.int32, "kv_len").value, _dev_ptr(q_start, torch.int32, "q_start").value, tokens,
-                int(max_q or 0), int(max_kv or 0))
+    i32 = torch.int32
+    return Seqs(shape[0], shape[1], _need(table, i32, "table", dev), _need(kv_len, i32, "kv_len", dev),
+                _need(q_start, i32, "q_start", dev), tokens, max_q or 0, max_kv or 0)
 
 
-def _token_rows(t, name, heads, d):
-    """Pointer and token stride of a bf16 [tokens, heads, d] tensor whose heads lie together."""
+def _token_rows(t, name, heads, d, dev):
+    """Address and token stride of a bf16 [tokens, heads, d] tensor whose heads lie together."""
     import torch
 
-    if t.dim() != 3 or t.shape[1:] != (heads, d) or t.dtype != torch.bfloat16 or not t.is_cuda or \
-            t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-        raise ValueError(f"{name} must be a bf16 CUDA tensor [tokens, {heads}, {d}] whose heads lie together")
-    _one_device((name, t))
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype is not torch.bfloat16 or \
+            t.get_device() != dev or stride[2] != 1 or (heads > 1 and stride[1] != d):
+        raise ValueError(f"{name} must be a bf16 tensor [tokens, {heads}, {d}] on the current CUDA device ({dev}) whose "
+                         "heads lie together")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * d
 
 
 def pages_append(K_pages, V_pages, layer, K, V, table, kv_len, q_start, status=None, stream=None):
@@ -382,14 +401,16 @@ def pages_append(K_pages, V_pages, layer, K, V, table, kv_len, q_start, status=N
     q_start int32 [seqs + 1]: sequence s's new tokens are rows q_start[s] ...
     q_start[s + 1] - 1. status: None or an int32 [1] word that records page
     numbers out of range. All on the current device."""
-    pg = _pages(K_pages, V_pages, status)
-    if V.shape != K.shape:
+    dev = _here()
+    pg = _pages(K_pages, V_pages, status, dev)
+    n = K.shape[0]
+    if V.shape[0] != n:
         raise ValueError("K and V must have the same shape")
-    kp, ks = _token_rows(K, "K", pg.kv_heads, pg.head_dim)
-    vp, vs = _token_rows(V, "V", pg.kv_heads, pg.head_dim)
-    sq = _seqs(table, kv_len, q_start, K.shape[0], 0, 0)
-    _check(_lib().kvpool_pages_append(ctypes.byref(pg), layer, ctypes.byref(sq), kp, ks, vp, vs, _stream_ptr(stream)),
-           "kvpool_pages_append")
+    kp, ks = _token_rows(K, "K", pg.kv_heads, pg.head_dim, dev)
+    vp, vs = _token_rows(V, "V", pg.kv_heads, pg.head_dim, dev)
+    sq = _seqs(table, kv_len, q_start, n, 0, 0, dev)
+    _check(_lib().kvpool_pages_append(ctypes.byref(pg), layer, ctypes.byref(sq), kp, ks, vp, vs,
+                                      _raw_stream(stream, dev)), "kvpool_pages_append")
 
 
 def pages_copy(K_pages, V_pages, src, dst, stream=None):
@@ -398,9 +419,10 @@ def pages_copy(K_pages, V_pages, src, dst, stream=None):
     n = len(src)
     if len(dst) != n:
         raise ValueError("src and dst must have the same length")
+    dev = _here()
     arr = ctypes.c_int32 * max(n, 1)
-    pg = _pages(K_pages, V_pages)
-    _check(_lib().kvpool_pages_copy(ctypes.byref(pg), arr(*src), arr(*dst), n, _stream_ptr(stream)),
+    pg = _pages(K_pages, V_pages, None, dev)
+    _check(_lib().kvpool_pages_copy(ctypes.byref(pg), arr(*src), arr(*dst), n, _raw_stream(stream, dev)),
            "kvpool_pages_copy")
 
 
@@ -419,32 +441,38 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
     gets 0 and -inf; rows behind the last sequence are left as they are."""
     import torch
 
-    pg = _pages(K_pages, V_pages, status)
+    dev = _here()
+    pg = _pages(K_pages, V_pages, status, dev)
     if Q.dim() != 3:
         raise ValueError("Q must be [tokens, q_heads, head_dim]")
     n, hq, d = Q.shape
-    qp, qs = _token_rows(Q, "Q", hq, pg.head_dim)
-    sq = _seqs(table, kv_len, q_start, n, max_q, max_kv)
-    for name, t, shape in (("slopes", slopes, (hq,)), ("first", first, (n,)), ("prefix", prefix, (sq.seqs,)),
-                           ("out", out, (n, hq, d)), ("lse", lse, (n, hq))):
-        if t is not None and tuple(t.shape) != shape:
+    qp, qs = _token_rows(Q, "Q", hq, pg.head_dim, dev)
+    sq = _seqs(table, kv_len, q_start, n, max_q, max_kv, dev)
+
+    def given(t, dtype, name, *shape):
+        if t is None:
+            return None
+        if tuple(t.shape) != shape:
             raise ValueError(f"{name} must have shape {shape}")
-    _one_device(("slopes", slopes), ("first", first), ("prefix", prefix), ("out", out), ("lse", lse))
+        return _need(t, dtype, name, dev)
+
     sc = None
     if cap or window or slopes is not None or first is not None or prefix is not None:
-        ptr = lambda t, dt, name: None if t is None else _dev_ptr(t, dt, name).value
-        sc = ctypes.byref(Score(cap, window, ptr(slopes, torch.float32, "slopes"), ptr(first, torch.int32, "first"),
-                                ptr(prefix, torch.int32, "prefix")))
-    if out is None or (return_lse and lse is None):
+        sc = ctypes.byref(Score(cap, window, given(slopes, torch.float32, "slopes", hq),
+                                given(first, torch.int32, "first", n), given(prefix, torch.int32, "prefix", sq.seqs)))
+    raw = _raw_stream(stream, dev)
+    op, lp = given(out, torch.bfloat16, "out", n, hq, d), given(lse, torch.float32, "lse", n, hq)
+    if op is None or (return_lse and lp is None):
         # on the stream that writes them, so that the allocator knows it
-        with torch.cuda.stream(stream):
-            if out is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            if op is None:
                 out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=Q.device)
-            if return_lse and lse is None:
+                op = out.data_ptr()
+            if return_lse and lp is None:
                 lse = torch.empty((n, hq), dtype=torch.float32, device=Q.device)
-    _check(_lib().kvpool_pages_attend(ctypes.byref(pg), layer, ctypes.byref(sq), qp, qs, hq, sc,
-                                      _dev_ptr(out, torch.bfloat16, "out"), _dev_ptr(lse, torch.float32, "lse"),
-                                      softmax_scale, _stream_ptr(stream)), "kvpool_pages_attend")
+                lp = lse.data_ptr()
+    _check(_lib().kvpool_pages_attend(ctypes.byref(pg), layer, ctypes.byref(sq), qp, qs, hq, sc, op, lp, softmax_scale,
+                                      raw), "kvpool_pages_attend")
     return out if lse is None else (out, lse)
 
 
@@ -694,22 +722,24 @@ class KVPool:
         import torch
 
         n, hq, d = Q.shape
-        pg = _pages(cache.K, cache.V, cache.status_word)
+        dev = _here()
+        pg = _pages(cache.K, cache.V, cache.status_word, dev)
         if d != pg.head_dim:
             raise ValueError("Q must be [tokens, q_heads, head_dim]")
-        sq = _seqs(batch.table, batch.kv_len, batch.q_start, n, batch.max_q, batch.max_kv)
-        _one_device(("Q", Q), ("out", out), ("workspace", workspace))
+        sq = _seqs(batch.table, batch.kv_len, batch.q_start, n, batch.max_q, batch.max_kv, dev)
+        qp = _need(Q, torch.bfloat16, "Q", dev)
         if out is not None and tuple(out.shape) != (n, hq, d):
             raise ValueError(f"out must have shape {(n, hq, d)}")
-        with torch.cuda.stream(stream):  # on the stream that uses them, so that the allocator knows it
+        # on the stream that uses them, so that the allocator knows it
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             if out is None:
                 out = torch.empty((n, hq, d), dtype=torch.float32, device=Q.device)
             if workspace is None:
                 workspace = torch.empty(max(self.attend_pages_ws_bytes(n, hq), 16), dtype=torch.uint8, device=Q.device)
         _check(_lib().kvpool_attend_pages(self._h, layer, ctypes.byref(pg), layer if page_layer is None else page_layer,
-                                          ctypes.byref(sq), _dev_ptr(Q, torch.bfloat16, "Q"), hq,
-                                          _dev_ptr(out, torch.float32, "out"), softmax_scale, workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+                                          ctypes.byref(sq), qp, hq, _need(out, torch.float32, "out", dev),
+                                          softmax_scale, _need(workspace, workspace.dtype, "workspace", dev),
+                                          workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
                "kvpool_attend_pages")
         return out
 
