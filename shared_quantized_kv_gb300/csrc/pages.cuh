@@ -171,15 +171,39 @@ __device__ __forceinline__ float2* state_ml(const PagedAttend& a, int t, int hd)
            ((long long)g * in + tl) * a.G + (hd - g * a.G);
 }
 
-// <q, k> -> the score in log2 units. tanh(y) = 1 - 2 / (e^(2y) + 1): off by a
-// few units of 2^-24 whatever y, which the cap turns into cap * 2^-22 of a
-// score; the reciprocal of an overflowed e^(2y) is 0, as it should be.
+// <q, k> -> the score in log2 units, N consecutive keys from j0 on. tanh(y) =
+// 1 - 2 / (e^(2y) + 1): off by a few units of 2^-24 whatever y, which the cap
+// turns into cap * 2^-22 of a score; the reciprocal of an overflowed e^(2y) is
+// 0, as it should be. (One loop per modifier: a choice per key costs more than
+// the modifiers do.)
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float capped(const PagedAttend& a, float s) {
+    return fmaf(-2.0f * a.cap2, rcp(ptx::ex2(s * a.cap_in) + 1.0f), a.cap2);
+}
+template <bool SCORED, int N>
+__device__ __forceinline__ void scores(const PagedAttend& a, float (&x)[N], float slope2, int pos, int j0) {
+    if (!SCORED || !(a.cap2 > 0.0f)) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] *= a.scale_log2;
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = capped(a, x[k]);
+    }
+    if (SCORED && a.slopes) {
+        const float far = (float)(pos - j0);
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = fmaf(-slope2, fabsf(far - (float)k), x[k]);
+    }
+}
 template <bool SCORED>
 __device__ __forceinline__ float score(const PagedAttend& a, float s, float slope2, int pos, int j) {
-    if constexpr (!SCORED) return s * a.scale_log2;
-    float x = s * a.scale_log2;
-    if (a.cap2 > 0.0f) x = a.cap2 * (1.0f - __fdividef(2.0f, ptx::ex2(s * a.cap_in) + 1.0f));
-    return fmaf(-slope2, (float)abs(pos - j), x);
+    float x[1] = {s};
+    scores<SCORED>(a, x, slope2, pos, j);
+    return x[0];
 }
 
 // One row over the keys j it sees among [t0, t1) with (j >> sh) % us == u0,

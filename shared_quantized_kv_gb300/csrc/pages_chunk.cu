@@ -172,7 +172,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int lr = tid & 127;              // row of the slot
     const int row = two ? w * kTile + lr : lr;
     const bool live = warp >= 4 && row < nr;
-    Seen see = {0, INT_MAX, 0, 0};  // rows past the block: Q is 0, nothing to mask, dropped at the end
+    Seen see = {0, INT_MAX, 0, 0};  // rows past the block: nothing to mask, dropped at the end
     int tok = 0, head = 0, pos = 0;
     if (live) {
         const int i = pages::div_group(p, j_begin + row);
@@ -412,28 +412,25 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         // ------------------------------------------------------------ softmax
         if (two || w == 0) {
-            // 16-byte pieces, consecutive lanes on consecutive pieces of a row
+            // 16-byte pieces, consecutive lanes on consecutive pieces of a row, all
+            // of a thread's under way before the first is stored (rows past the
+            // block repeat its last: a load under a condition waits for the one
+            // before it, 16 thousand cycles in all instead of 4)
             constexpr int CH = D / 8;
             unsigned char* dst = sm + w * L::stage;
             const int first = two ? w * kTile : 0;
+            uint4 v[CH];
 #pragma unroll
-            for (int k0 = 0; k0 < CH; k0 += 8) {
-                uint4 v[8];
+            for (int k = 0; k < CH; ++k) {
+                const int x = k * kTile + (tid & 127), r = min(first + x / CH, nr - 1), c = x % CH;
+                const int i = pages::div_group(p, j_begin + r);
+                v[k] = ptx::ldg16(p.Q + (long long)(b.q0 + i_begin + i) * p.q_stride +
+                                  (long long)(g * p.G + j_begin + r - i * p.G) * D + c * 8);
+            }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int x = (k0 + k) * kTile + (tid & 127), r = x / CH, c = x % CH;
-                    const int i = pages::div_group(p, j_begin + first + r);
-                    v[k] = make_uint4(0, 0, 0, 0);
-                    if (first + r < nr)
-                        v[k] = __ldg(reinterpret_cast<const uint4*>(
-                                         p.Q + (long long)(b.q0 + i_begin + i) * p.q_stride +
-                                         (long long)(g * p.G + j_begin + first + r - i * p.G) * D) + c);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int x = (k0 + k) * kTile + (tid & 127), r = x / CH, c = x % CH;
-                    *reinterpret_cast<uint4*>(dst + (c / 8) * (kTile * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v[k];
-                }
+            for (int k = 0; k < CH; ++k) {
+                const int x = k * kTile + (tid & 127), r = x / CH, c = x % CH;
+                *reinterpret_cast<uint4*>(dst + (c / 8) * (kTile * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v[k];
             }
             ptx::fence_proxy_async();  // the MMAs read Q through the async proxy
         }
@@ -498,26 +495,22 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const bool whole = __all_sync(0xffffffffu, see.all(k0, k0 + 64));
                 uint32_t pw[2][16], pl[STATE ? 2 : 1][16];  // (pl: STATE)
                 float2 sum[2];
-#pragma unroll 1
-                for (;;) {
-                    const float ref = m == -CUDART_INF_F ? 0.0f : m;
-                    const float2 sc = SCORED ? make_float2(1.f, 1.f) : make_float2(p.scale_log2, p.scale_log2);
-                    const float2 nm = make_float2(-ref, -ref);
+                if constexpr (SCORED) {
+                    // forming the scores again would cost more than waiting for the maxima
+                    uint32_t u0[32], u1[32];
                     float mm[2];
-                    sum[0] = sum[1] = make_float2(0.f, 0.f);
-                    auto form = [&](int c, uint32_t (&u)[32]) {
-                        if constexpr (SCORED) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                u[k] = asu(pages::score<true>(p, asf(u[k]), slope2, pos, k0 + 32 * c + k));
-                        }
+                    // chunk c (32 keys): scores, masked
+                    auto finish_s = [&](int c, uint32_t (&u)[32]) {
+                        pages::scores<true>(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0 + 32 * c);
                         if (!whole) {
                             uint32_t bits = span_bits(see.a1 - k0, see.b1 - k0, c);
-                            if constexpr (SCORED) bits |= span_bits(see.a2 - k0, see.b2 - k0, c);
+                            bits |= span_bits(see.a2 - k0, see.b2 - k0, c);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 if (!(bits >> k & 1u)) u[k] = asu(-CUDART_INF_F);
                         }
+                    };
+                    auto max_of = [&](int c, const uint32_t (&u)[32]) {
                         auto f = [&](int k) { return asf(u[k]); };
                         float x[11];
 #pragma unroll
@@ -525,47 +518,120 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         x[10] = fmaxf(f(30), f(31));
                         mm[c] = ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
                                           ptx::max3(x[7], x[8], x[9]), x[10]);
+                    };
+                    auto weights_of = [&](int c, const uint32_t (&u)[32]) {
+                        const float ref = m == -CUDART_INF_F ? 0.0f : m;
+                        const float2 nm = make_float2(-ref, -ref);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const float2 d = __ffma2_rn(make_float2(f(2 * k), f(2 * k + 1)), sc, nm);
+                            const float2 d = __fadd2_rn(make_float2(asf(u[2 * k]), asf(u[2 * k + 1])), nm);
                             const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
                             sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                             pw[c][k] = pack_bf2(e.x, e.y);
-                            if constexpr (STATE)
-                                pl[c][k] = pack_bf2(e.x - asf(pw[c][k] << 16), e.y - asf(pw[c][k] & 0xFFFF0000u));
                         }
                     };
-                    uint32_t u0[32], u1[32];  // the second chunk is on its way while the first is worked on
-                    ptx::tmem_ld32(tSh, u0);
-                    ptx::tmem_wait_ld(u0);
-                    ptx::tmem_ld32(tSh + 32, u1);
-                    form(0, u0);
-                    ptx::tmem_wait_ld(u1);
-                    form(1, u1);
-                    const float top = fmaxf(mm[0], mm[1]);
-                    // plain scores are scaled in the exponent's fused step (the scale is positive)
-                    const float mt = SCORED ? top : top * p.scale_log2;
-                    const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
-                    if (!__any_sync(0xffffffffu, move)) break;
-                    const int before = 2 * it + h;  // half tiles of the slot before this one
-                    if (before > 0) {
-                        // O in the old reference: the P V of the half before has to be done
-                        // (the one before that is: S of this tile came after it)
-                        warp_wait(b_o + 8 * w, (before - 1) & 1, bad);
-                        ptx::tc_fence_after();
-                        const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
-                        l *= al;
+                    // the reference moves where the maximum passes it
+                    auto move_ref = [&]() {
+                        const float mt = fmaxf(mm[0], mm[1]);
+                        const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
+                        if (!__any_sync(0xffffffffu, move)) return;
+                        const int before = 2 * it + h;  // half tiles of the slot before this one
+                        if (before > 0) {
+                            // O in the old reference: the P V of the half before has to be done
+                            // (the one before that is: S of this tile came after it)
+                            warp_wait(b_o + 8 * w, (before - 1) & 1, bad);
+                            ptx::tc_fence_after();
+                            const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
+                            l *= al;
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            ptx::tmem_ld32(tO + c, u0);
-                            ptx::tmem_wait_ld(u0);
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                ptx::tmem_ld32(tO + c, o);
+                                ptx::tmem_wait_ld(o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) u0[k] = asu(asf(u0[k]) * al);
-                            ptx::tmem_st32x(tO + c, u0);
+                                for (int k = 0; k < 32; ++k) o[k] = asu(asf(o[k]) * al);
+                                ptx::tmem_st32x(tO + c, o);
+                            }
+                            ptx::tmem_wait_st();
                         }
-                        ptx::tmem_wait_st();
+                        if (move) m = mt;
+                    };
+                    ptx::tmem_ld32(tSh, u0);
+                    ptx::tmem_ld32(tSh + 32, u1);
+                    ptx::tmem_wait_ld(u0);
+                    ptx::tmem_wait_ld(u1);
+                    finish_s(0, u0);
+                    finish_s(1, u1);
+                    max_of(0, u0);
+                    max_of(1, u1);
+                    move_ref();
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
+                    weights_of(0, u0);
+                    weights_of(1, u1);
+                } else {
+#pragma unroll 1
+                    for (;;) {
+                        const float ref = m == -CUDART_INF_F ? 0.0f : m;
+                        const float2 sc = make_float2(p.scale_log2, p.scale_log2);
+                        const float2 nm = make_float2(-ref, -ref);
+                        float mm[2];
+                        sum[0] = sum[1] = make_float2(0.f, 0.f);
+                        auto form = [&](int c, uint32_t (&u)[32]) {
+                            if (!whole) {
+                                uint32_t bits = span_bits(see.a1 - k0, see.b1 - k0, c);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!(bits >> k & 1u)) u[k] = asu(-CUDART_INF_F);
+                            }
+                            auto f = [&](int k) { return asf(u[k]); };
+                            float x[11];
+#pragma unroll
+                            for (int k = 0; k < 10; ++k) x[k] = ptx::max3(f(3 * k), f(3 * k + 1), f(3 * k + 2));
+                            x[10] = fmaxf(f(30), f(31));
+                            mm[c] = ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
+                                              ptx::max3(x[7], x[8], x[9]), x[10]);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float2 d = __ffma2_rn(make_float2(f(2 * k), f(2 * k + 1)), sc, nm);
+                                const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
+                                sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+                                pw[c][k] = pack_bf2(e.x, e.y);
+                                if constexpr (STATE)
+                                    pl[c][k] = pack_bf2(e.x - asf(pw[c][k] << 16), e.y - asf(pw[c][k] & 0xFFFF0000u));
+                            }
+                        };
+                        uint32_t u0[32], u1[32];  // the second chunk is on its way while the first is worked on
+                        ptx::tmem_ld32(tSh, u0);
+                        ptx::tmem_wait_ld(u0);
+                        ptx::tmem_ld32(tSh + 32, u1);
+                        form(0, u0);
+                        ptx::tmem_wait_ld(u1);
+                        form(1, u1);
+                        const float top = fmaxf(mm[0], mm[1]);
+                        // plain scores are scaled in the exponent's fused step (the scale is positive)
+                        const float mt = top * p.scale_log2;
+                        const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
+                        if (!__any_sync(0xffffffffu, move)) break;
+                        const int before = 2 * it + h;  // half tiles of the slot before this one
+                        if (before > 0) {
+                            // O in the old reference: the P V of the half before has to be done
+                            // (the one before that is: S of this tile came after it)
+                            warp_wait(b_o + 8 * w, (before - 1) & 1, bad);
+                            ptx::tc_fence_after();
+                            const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
+                            l *= al;
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                ptx::tmem_ld32(tO + c, u0);
+                                ptx::tmem_wait_ld(u0);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) u0[k] = asu(asf(u0[k]) * al);
+                                ptx::tmem_st32x(tO + c, u0);
+                            }
+                            ptx::tmem_wait_st();
+                        }
+                        if (move) m = mt;
                     }
-                    if (move) m = mt;
                 }
                 // P over the half's own columns of S
 #pragma unroll
@@ -641,8 +707,11 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
         };
         if (direct && two) {
-            // a row's thread writes its output
+            // A row's thread has its output; the slot's Q (no MMA reads it any more)
+            // takes it as bf16, and the warp writes whole rows of it.
             const float inv = STATE ? 1.0f : 1.0f / l;  // (not used where l is 0)
+            constexpr int CH = D / 8;
+            unsigned char* stage = sm + w * L::stage + (warp & 3) * 32 * (D * 2);
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -654,11 +723,30 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     odd = odd || (live && l != 0.0f && !finite(asf(o[k])));
                     y[k] = l == 0.0f ? 0.0f : asf(o[k]) * inv;
                 }
-                if (live) store32(c, y);  // (odd rows are written again)
+                if constexpr (STATE) {
+                    if (live) store32(c, y);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        *reinterpret_cast<uint4*>(stage + lane * (D * 2) + ((((c + k) / 8) ^ (lane & 7)) << 4)) =
+                            make_uint4(pack_bf2(y[k], y[k + 1]), pack_bf2(y[k + 2], y[k + 3]),
+                                       pack_bf2(y[k + 4], y[k + 5]), pack_bf2(y[k + 6], y[k + 7]));
+                }
             }
             if (live) finish(tok, head, l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m), l);
             __syncwarp();
-            again(__ballot_sync(0xffffffffu, odd));
+            if constexpr (!STATE) {
+                const long long at = live ? ((long long)tok * p.Hq + head) * D : -1;
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int x = k * 32 + lane, r = x / CH, c = x % CH;
+                    const long long to = __shfl_sync(0xffffffffu, at, r);
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * (D * 2) + ((c ^ (r & 7)) << 4));
+                    if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + c * 8) = v;
+                }
+                __syncwarp();
+            }
+            again(__ballot_sync(0xffffffffu, odd));  // (writes odd rows once more)
         } else if (direct) {
             // Both slots have the row: each hands half its channels to the other
             // and writes the rest. A row: the half of slot 0, of slot 1, then

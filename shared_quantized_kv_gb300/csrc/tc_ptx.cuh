@@ -85,6 +85,15 @@ __device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
                  ::"l"(map), "r"(x), "r"(y) : "memory");
 }
 
+// 16 bytes of read-only global memory, requested where it stands (a batch of
+// these is under way together)
+__device__ __forceinline__ uint4 ldg16(const void* src) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
+    return v;
+}
+
 // ------------------------------------------------------- programmatic launch
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() {
