@@ -40,6 +40,14 @@ class Batch:
         self.tokens = int(sum(q)) + extra_rows
         self.Q = bf16(r.standard_normal((max(self.tokens, 1), hq, d), dtype=np.float32))
 
+    def many(self, room=1 << 16):
+        """Room for `room` tokens in every row of the table: with a max_kv of that,
+        the attention kernel for many rows takes the call, its keys split over
+        clusters where there are many of them."""
+        self.table = np.pad(self.table, ((0, 0), (0, max(0, room // self.P - self.table.shape[1]))), constant_values=-9)
+        assert reads(self, self.tokens, room) >= 1 << 27
+        return self
+
     def dev(self):
         """(K, V, layer, Q, table, kv_len, q_start) on the GPU."""
         import torch
@@ -51,6 +59,13 @@ class Batch:
     def ref(self, **score):
         with np.errstate(invalid="ignore"):
             return paged.attend(self.K, self.V, self.layer, self.Q, self.table, self.kv_len, self.q_start, **score)
+
+
+def reads(b, max_q, max_kv):
+    """Bytes by which the library chooses between its two attention kernels:
+    blocks of 16 rows, each through all keys; 2^27 and more go to the kernel for
+    many rows."""
+    return len(b.q) * -(-max_q * (b.hq // b.hk) // 16) * b.hk * max_kv * b.d * 4
 
 
 def check_attend(out, lse, ref, T):
