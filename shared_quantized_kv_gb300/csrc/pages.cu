@@ -154,11 +154,10 @@ int check_seqs(const kvpool_seqs_t* s) {
 
 // The current device: sm_103 or KVPOOL_ERR_UNSUPPORTED; its SM count (asked
 // for once per device: a device's properties do not change).
-constexpr int kMaxDevices = 64;
 int check_device(int& sms) {
-    static std::atomic<int> known[kMaxDevices];  // SM count, -1 for another architecture, 0 not asked yet
+    static std::atomic<int> known[kvp::kPagedDevices];  // SM count, -1 for another architecture, 0 not asked yet
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return KVPOOL_ERR_UNSUPPORTED;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kvp::kPagedDevices) return KVPOOL_ERR_UNSUPPORTED;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n == 0) {
         int major = 0, minor = 0;
@@ -250,9 +249,9 @@ cudaError_t kvp::launch_pages_attend(const PagedAttend& a, int head_dim, int max
     // and 128 rows per KV head it takes 14 us against 21 of the kernel for many
     // rows, of 16K keys and 32 rows 31 against 33; on 16K keys and 128 rows 72
     // against 39, on 16 sequences of 1,024 keys and 32 rows 35 against 25.
-    const long long blocks = a.s.seqs * (((long long)max_q * a.G + 15) / 16);
-    const long long reads = blocks * a.s.Hk * max_kv * head_dim * 4;
-    if ((long long)max_q * a.G <= 16 || reads < (1LL << 27))
+    const double blocks = (double)a.s.seqs * (((long long)max_q * a.G + 15) / 16);
+    const double reads = blocks * a.s.Hk * max_kv * head_dim * 4;
+    if ((long long)max_q * a.G <= 16 || reads < (double)(1 << 27))
         return launch_pages_rows(a, head_dim, max_q, max_kv, sm_count, st);
     return launch_pages_chunk(a, head_dim, max_q, max_kv, st);
 }

@@ -12,6 +12,8 @@
 
 namespace kvp {
 
+constexpr int kPagedDevices = 64;  // devices of a process that the paged calls may run on
+
 // Bits of kvpool_pages_t.status.
 enum : int { kPgBadPage = 1, kPgTimeout = 2 };
 

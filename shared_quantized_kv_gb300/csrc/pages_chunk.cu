@@ -35,6 +35,7 @@
 // halves; no register spills (the roles' registers shifted between the
 // warpgroups). The MMAs alone, with no softmax, take 338 us.
 #include <algorithm>
+#include <mutex>
 
 #include "pages.cuh"
 
@@ -922,18 +923,21 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     }
 }
 
-// Per instance, once (a static initialiser: thread-safe): the shared memory
-// opted in, and how many clusters of 1, 2, 4 and 8 CTAs the GPU holds at once
-// (a cluster's CTAs share a group of SMs whose number need not be a multiple).
+// Per instance and device, once: the shared memory opted in, and how many
+// clusters of 1, 2, 4 and 8 CTAs the GPU holds at once (a cluster's CTAs share
+// a group of SMs whose number need not be a multiple).
 struct Fit {
-    cudaError_t err;
-    int clusters[4];
+    cudaError_t err = cudaSuccess;
+    int clusters[4] = {};
 };
 template <int D, bool SCORED, bool STATE>
-const Fit& fit() {
-    static const Fit f = [] {
+const Fit& fit(int device) {
+    static std::once_flag once[kPagedDevices];
+    static Fit fits[kPagedDevices];
+    std::call_once(once[device], [device] {
         auto kern = pages_chunk_kernel<D, SCORED, STATE>;
-        Fit x{cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::total), {}};
+        Fit& x = fits[device];
+        x.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::total);
         for (int i = 0; i < 4 && x.err == cudaSuccess; ++i) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(1 << i, 1, 1);
@@ -948,14 +952,17 @@ const Fit& fit() {
             cfg.numAttrs = 1;
             x.err = cudaOccupancyMaxActiveClusters(&x.clusters[i], kern, &cfg);
         }
-        return x;
-    }();
-    return f;
+    });
+    return fits[device];
 }
 
 template <int D, bool SCORED, bool STATE>
 cudaError_t launch(const PagedAttend& a, int max_q, int max_kv, cudaStream_t st) {
-    const Fit& f = fit<D, SCORED, STATE>();
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device >= kPagedDevices) return cudaErrorInvalidDevice;
+    const Fit& f = fit<D, SCORED, STATE>(device);
     if (f.err != cudaSuccess) return f.err;
     const long long rows = (long long)a.s.tokens * a.G;
     const long long blocks = rows / kRows + a.s.seqs;  // at least as many as there are

@@ -27,6 +27,7 @@
 // Measured: those 32 sequences, 4.1 GB of keys and values, in 577 us, 7.1 TB/s;
 // 3 sequences of up to 129 keys in 3.8 us of a captured graph.
 #include <algorithm>
+#include <mutex>
 
 #include "pages.cuh"
 
@@ -400,13 +401,19 @@ pages_rows_kernel(const PagedAttend p) {
 template <int D, bool SCORED, bool STATE, bool DIRECT>
 cudaError_t launch(const PagedAttend& a, int split, long long blocks, cudaStream_t st) {
     auto kern = pages_rows_kernel<D, SCORED, STATE, DIRECT>;
-    // opted in once per instance (a static initialiser: thread-safe)
-    static const cudaError_t opt = [&] {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        return e;
-    }();
-    if (opt != cudaSuccess) return opt;
+    // opted in once per instance and device
+    static std::once_flag once[kPagedDevices];
+    static cudaError_t opt[kPagedDevices];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device >= kPagedDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[device], [&] {
+        opt[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+        if (opt[device] == cudaSuccess)
+            opt[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (opt[device] != cudaSuccess) return opt[device];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(split * blocks), a.s.Hk, 1);
     cfg.blockDim = dim3(kWarps * 32, 1, 1);
