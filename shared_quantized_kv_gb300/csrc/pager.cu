@@ -1,7 +1,6 @@
 // The pager of the paged private caches: which pages each sequence owns.
-// Host only. Pages are reference counted; the free ones are kept in a bitmap
-// that is searched from a hint, so that the lowest free page is always the one
-// taken (a cache that shrinks keeps its owned pages low, and the same calls
+// Host only. Pages are reference counted and searched from a hint below which
+// none is free, so that the lowest free page is always the one taken (a cache that shrinks keeps its owned pages low, and the same calls
 // always give the same pages).
 #include <limits.h>
 #include <stdint.h>

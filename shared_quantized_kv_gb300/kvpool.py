@@ -292,12 +292,12 @@ class Pager:
         """Room for n more tokens: None, or the (shared page, own page) pair
         that has to be copied before they are written."""
         pair = (ctypes.c_int32 * 2)()
-        due = self._count(_lib().kvpool_pager_extend(self._h, seq, n, pair), "kvpool_pager_extend")
+        due = self._count(_lib().kvpool_pager_extend(self._h, seq, _i32(n, "n"), pair), "kvpool_pager_extend")
         return (pair[0], pair[1]) if due else None
 
     def truncate(self, seq, length):
         """Cut a sequence to its first `length` tokens."""
-        _check(_lib().kvpool_pager_truncate(self._h, seq, length), "kvpool_pager_truncate")
+        _check(_lib().kvpool_pager_truncate(self._h, seq, _i32(length, "length")), "kvpool_pager_truncate")
 
     def fork(self, seq) -> int:
         """A new sequence that shares all pages of seq."""
@@ -329,6 +329,13 @@ class Pager:
     def owners(self, page) -> int:
         """Sequences that own the page (0: free)."""
         return self._count(_lib().kvpool_pager_owners(self._h, page), "kvpool_pager_owners")
+
+
+def _i32(x, name):
+    """x, which ctypes would cut to 32 bits without a word."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, not {x}")
+    return x
 
 
 def _here():
@@ -378,7 +385,7 @@ def _seqs(table, kv_len, q_start, tokens, max_q, max_kv, dev=None):
         raise ValueError("table [seqs, pages], kv_len [seqs] and q_start [seqs + 1] do not fit together")
     i32 = torch.int32
     return Seqs(shape[0], shape[1], _need(table, i32, "table", dev), _need(kv_len, i32, "kv_len", dev),
-                _need(q_start, i32, "q_start", dev), tokens, max_q or 0, max_kv or 0)
+                _need(q_start, i32, "q_start", dev), tokens, _i32(max_q or 0, "max_q"), _i32(max_kv or 0, "max_kv"))
 
 
 def _token_rows(t, name, heads, d, dev):
@@ -419,6 +426,8 @@ def pages_copy(K_pages, V_pages, src, dst, stream=None):
     n = len(src)
     if len(dst) != n:
         raise ValueError("src and dst must have the same length")
+    for x in (src, dst) if n else ():
+        _i32(min(x), "page"), _i32(max(x), "page")
     dev = _here()
     arr = ctypes.c_int32 * max(n, 1)
     pg = _pages(K_pages, V_pages, None, dev)
@@ -458,7 +467,7 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
 
     sc = None
     if cap or window or slopes is not None or first is not None or prefix is not None:
-        sc = ctypes.byref(Score(cap, window, given(slopes, torch.float32, "slopes", hq),
+        sc = ctypes.byref(Score(cap, _i32(window, "window"), given(slopes, torch.float32, "slopes", hq),
                                 given(first, torch.int32, "first", n), given(prefix, torch.int32, "prefix", sq.seqs)))
     raw = _raw_stream(stream, dev)
     op, lp = given(out, torch.bfloat16, "out", n, hq, d), given(lse, torch.float32, "lse", n, hq)

@@ -148,6 +148,12 @@ def test_python_refusals(kp):
             kp.pages_attend(**{**ok, **bad})
     with pytest.raises(kp.KVPoolError):
         kp.pages_attend(**ok, window=-1)
+    for bad in (dict(window=(1 << 32) + 1), dict(max_q=1 << 32), dict(max_kv=1 << 31)):
+        with pytest.raises(ValueError):
+            kp.pages_attend(**ok, **bad)
+    for src, dst in (([1 << 32], [1]), ([0], [(1 << 32) + 1]), ([0, -(1 << 32)], [1, 2]), ([0], [])):
+        with pytest.raises(ValueError):
+            kp.pages_copy(K, V, src, dst)
     with pytest.raises(kp.KVPoolError):
         kp.pages_attend(**{**ok, "layer": 1})
     new = torch.zeros(21, 2, 64, dtype=torch.bfloat16, device="cuda")

@@ -82,6 +82,18 @@ def test_pager_compacts_in_parts(kp):
     p.close()
 
 
+def test_numbers_past_32_bits(kp):
+    """They are refused, not cut to their low bits."""
+    p = kp.Pager(4, 16)
+    s = p.new()
+    for f in (lambda n: p.extend(s, n), lambda n: p.truncate(s, n)):
+        for n in (1 << 31, 1 << 32, -(1 << 31) - 1):
+            with pytest.raises(ValueError):
+                f(n)
+    assert p.length(s) == 0
+    p.close()
+
+
 def test_pager_refusals(kp):
     lib = kp.lib()
     h = ctypes.c_void_p()
