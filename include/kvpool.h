@@ -513,8 +513,9 @@ int kvpool_pages_copy(const kvpool_pages_t* pages, const int32_t* src, const int
  * kv_heads). score: NULL for the causal mask alone. out: bf16
  * [tokens][q_heads][head_dim], 16-byte aligned; lse: float [tokens][q_heads],
  * log sum exp of the row's scores (natural units), or NULL. A row that sees no
- * key gets out 0 and lse -inf. softmax_scale: 0 means 1/sqrt(head_dim).
- * Needs no workspace and allocates nothing. */
+ * key gets out 0 and lse -inf. softmax_scale: 0 means 1/sqrt(head_dim). out
+ * and lse may overlap none of the inputs. Needs no workspace and allocates
+ * nothing. */
 int kvpool_pages_attend(const kvpool_pages_t* pages, int layer, const kvpool_seqs_t* seqs, const void* Q,
                         long long q_stride, int q_heads, const kvpool_score_t* score, void* out, float* lse,
                         float softmax_scale, void* stream);

@@ -145,6 +145,8 @@ struct Seen {
         return (a1 <= u0 && b1 >= u1) || (a2 <= u0 && b2 >= u1);
     }
     __device__ __forceinline__ int lo() const { return min(b1 > a1 ? a1 : INT_MAX, b2 > a2 ? a2 : INT_MAX); }
+    __device__ __forceinline__ int prefix_end() const { return b2 > a2 ? b2 : 0; }
+    __device__ __forceinline__ int window_lo() const { return b1 > a1 ? a1 : INT_MAX; }
     __device__ __forceinline__ int hi() const { return max(b1 > a1 ? b1 : 0, b2 > a2 ? b2 : 0); }
 };
 // Row `tok` (of the call) at position pos of sequence seq, which holds T tokens.
@@ -164,6 +166,22 @@ __device__ __forceinline__ Seen row_seen(const PagedAttend& a, int seq, int tok,
     }
     return r;
 }
+
+// Units (or tiles) of keys, counted without those between a prefix and the
+// windows behind it, which no row of a block sees: unit u of the count is
+// number u + len of the sequence from `at` on.
+struct Gap {
+    int at, len;
+    // prefix_end: the last end of a part [a2, b2) of the block's rows, 0 for none;
+    // window_lo: the first begin of a part [a1, b1), INT_MAX for none
+    __device__ __forceinline__ Gap(int prefix_end, int window_lo, int unit) {
+        at = (prefix_end + unit - 1) / unit;
+        len = prefix_end > 0 && window_lo < INT_MAX ? max(window_lo / unit - at, 0) : 0;
+    }
+    __device__ __forceinline__ Gap() : at(0), len(0) {}
+    __device__ __forceinline__ int number(int u) const { return u >= at ? u + len : u; }
+    __device__ __forceinline__ int count(int n) const { return n > at ? max(n - len, at) : n; }  // of numbers below n
+};
 
 // Where the state (m, l) of token row t and query head hd goes.
 __device__ __forceinline__ float2* state_ml(const PagedAttend& a, int t, int hd) {
@@ -208,14 +226,14 @@ __device__ __forceinline__ float score(const PagedAttend& a, float s, float slop
     return x[0];
 }
 
-// One row over the keys j it sees among [t0, t1) with (j >> sh) % us == u0,
-// with nothing that it does not see touching the result: the slow
-// path of rows whose sums came out infinite or NaN, which a matrix product
+// One row over the keys it sees in the units [u0, u1) of 2^sh keys, counted
+// without the gap, every us-th one, with nothing that it does not see
+// touching the result: the slow path of rows whose sums came out infinite or NaN, which a matrix product
 // gives for 0 * NaN where a masked key's V is not finite. One warp; lane holds
 // D / 32 consecutive channels of acc.
 template <int D, bool SCORED>
 __device__ __noinline__ void careful_row(const PagedAttend& a, int seq, int tok, int head, int pos, const Seen& see,
-                                         int t0, int t1, int sh, int u0, int us, float& m, float& l,
+                                         const Gap gap, int sh, int u0, int u1, int us, float& m, float& l,
                                          float (&acc)[D / 32]) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
@@ -229,8 +247,10 @@ __device__ __noinline__ void careful_row(const PagedAttend& a, int seq, int tok,
     l = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int j = t0; j < t1; ++j) {
-        if ((j >> sh) % us != u0 || !see.has(j)) continue;
+    // (a sum that is NaN stays NaN, and with it the row)
+    for (int k = 0; l == l && (u0 + (k >> sh) * us) < u1; ++k) {
+        const int j = (gap.number(u0 + (k >> sh) * us) << sh) + (k & ((1 << sh) - 1));
+        if (!see.has(j)) continue;
         const int page = __ldg(s.table + (long long)seq * s.tstride + (j >> s.pshift));
         const bool ok = page >= 0 && page < s.pages;
         const long long at =

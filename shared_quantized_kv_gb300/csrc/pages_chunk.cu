@@ -32,7 +32,7 @@
 // tensor cores idle: 466 us; two without turns fell into step: 592 us);
 // operands of the MMAs in uniform registers (509 us before); P formed under
 // the reference as it is, the maxima checked beside it, and handed over in
-// halves; no register spills (the roles' registers shifted between the
+// halves; hardly a register spilled (the roles' registers shifted between the
 // warpgroups). The MMAs alone, with no softmax, take 338 us.
 #include <algorithm>
 #include <mutex>
@@ -68,7 +68,7 @@ struct Lay {
     static constexpr int bars = ring + nst * stage;
     // barriers: full, empty per ring stage; per slot S, P (of each half), O, all done
     static constexpr int bar_s = bars + 2 * nst * 8, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_fin = bar_o + 16;
-    static constexpr int info = bar_fin + 16;  // rng[2][2], tensor memory address
+    static constexpr int info = bar_fin + 16;  // rng[2][2], tensor memory address, prefixes' end, windows' begin
     static constexpr int total = info + 32 + 1024;  // + alignment of the base
     static constexpr int rs = D + 4;             // floats of a merge row: O, m, l
     static_assert(kRows * (rs + kMaxParts) * 4 <= bars, "merge rows and weights fit in the tiles");
@@ -130,6 +130,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     int* rng = reinterpret_cast<int*>(sm + L::info);  // [slot] {first key seen, end of the keys seen}
     uint32_t* tslot = reinterpret_cast<uint32_t*>(rng + 4);
+    int* gapped = rng + 5;                              // end of the prefixes, begin of the windows seen
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tslot), kCols);  // beside the search
     // blocks of a sequence from its last (the one that sees most) to its first
     const int job = blockIdx.x / CS, g = job % s.Hk;
@@ -164,6 +165,8 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             rng[2 * w] = INT_MAX;
             rng[2 * w + 1] = 0;
         }
+        gapped[0] = 0;
+        gapped[1] = INT_MAX;
         ptx::mbar_init_fence();
     }
     if constexpr (SCORED) __syncthreads();
@@ -190,6 +193,14 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 atomicMin(&rng[2 * w], lo);
                 atomicMax(&rng[2 * w + 1], hi);
             }
+            if (p.prefix && p.window > 0) {
+                const int end = __reduce_max_sync(0xffffffffu, live ? see.prefix_end() : 0);
+                const int begin = __reduce_min_sync(0xffffffffu, live ? see.window_lo() : INT_MAX);
+                if (lane == 0) {
+                    atomicMax(&gapped[0], end);
+                    atomicMin(&gapped[1], begin);
+                }
+            }
         }
     }
     ptx::tc_fence_before();
@@ -204,21 +215,23 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const int last = two && slot == 0 ? kTile - 1 : nr - 1;
         return max(0, min(T, T - b.n + i_begin + pages::div_group(p, j_begin + last) + 1));
     };
-    // this CTA's key tiles [ta, ta + n): the cluster's share of the tiles that
-    // any row sees; slot w takes the first nt[w] of them (two row tiles), or
+    // this CTA's key tiles [ta, ta + n), counted without the gap: the cluster's
+    // share of the tiles that any row sees; slot w takes the first nt[w] of them (two row tiles), or
     // every second one. Few tiles are not split: the cluster's first CTA takes
     // them all, as a merge costs about what kFewTiles cost.
     const int hi = max(seen_end(0), seen_end(1));
     int t_lo = 0;
     if constexpr (SCORED) t_lo = hi > 0 ? min(rng[0], rng[2]) / kTile : 0;
-    const int t_hi = (hi + kTile - 1) / kTile;
+    pages::Gap gap;
+    if constexpr (SCORED) gap = pages::Gap(gapped[0], gapped[1], kTile);
+    const int t_hi = gap.count((hi + kTile - 1) / kTile);
     const int S = t_hi - t_lo <= kFewTiles ? 1 : CS;
     const int per = (t_hi - t_lo + S - 1) / S;
     const int ta = t_lo + rank * per;
     const int n = max(0, min(t_hi, ta + per) - ta);
     auto tiles_of = [&](int slot) {
         if (!two) return (n - slot + 1) / 2;
-        return max(0, min(n, (seen_end(slot) + kTile - 1) / kTile - ta));
+        return max(0, min(n, gap.count((seen_end(slot) + kTile - 1) / kTile) - ta));
     };
     if (rank >= S) {  // not a split block's: nothing to do, and nobody waits for this CTA
         if (warp == 1) ptx::tmem_dealloc(tmem, kCols);
@@ -237,7 +250,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const int none = s.pages * (s.Hk << s.pshift);  // a row behind the last: reads as zeros
             // first token row of this lane's page of tile i, -1 for none
             auto page_row = [&](int i) {
-                const int t = (ta + i) * kTile + lane * P;
+                const int t = gap.number(ta + i) * kTile + lane * P;
                 if (i >= n || lane >= np || t >= T) return -1;
                 const int page = __ldg(table + (t >> s.pshift));
                 if (page < 0 || page >= s.pages) {
@@ -443,7 +456,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         if (!SCORED && mine > 0 && some) {
             // the maximum of the first half tile, where no key is masked, is the
             // first reference
-            const int t0 = (ta + (two ? 0 : w)) * kTile;
+            const int t0 = (ta + (two ? 0 : w)) * kTile;  // (plain scores: no gap)
             if (__all_sync(0xffffffffu, see.all(t0, t0 + 64))) {
                 warp_wait(b_s + 8 * w, 0, bad);
                 ptx::tc_fence_after();
@@ -461,7 +474,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         for (int it = 0; it < mine; ++it) {
             const int i = two ? it : 2 * it + w;  // tile of this CTA
-            const int t0 = (ta + i) * kTile;
+            const int t0 = gap.number(ta + i) * kTile;
             warp_wait(b_s + 8 * w, it & 1, bad);
             ptx::tc_fence_after();
             // keys behind the sequence's end: whatever their V holds becomes 0 (a
@@ -665,8 +678,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             se.b2 = __shfl_sync(0xffffffffu, see.b2, of);
             pages::careful_row<D, SCORED>(p, b.seq, __shfl_sync(0xffffffffu, tok, of),
                                           __shfl_sync(0xffffffffu, head, of), __shfl_sync(0xffffffffu, pos, of), se,
-                                          ta * kTile, (ta + n) * kTile, 7, two || all ? 0 : (ta + w) & 1,
-                                          two || all ? 1 : 2, cm, cl, acc);
+                                          gap, 7, two || all ? ta : ta + w, ta + n, two || all ? 1 : 2, cm, cl, acc);
         };
         bool odd = live && l != 0.0f && !finite(l);  // sums that a masked key may have spoilt
         // a row's last numbers: m and l, or their logarithm

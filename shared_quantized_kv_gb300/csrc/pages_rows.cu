@@ -152,7 +152,11 @@ pages_rows_kernel(const PagedAttend p) {
             lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
             hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        const int u_lo = hi > 0 ? lo / kUnit : 0, u_hi = (hi + kUnit - 1) / kUnit;
+        pages::Gap gap;
+        if (SCORED && p.prefix && p.window > 0)
+            gap = pages::Gap(__reduce_max_sync(0xffffffffu, max(see[0].prefix_end(), see[1].prefix_end())),
+                             __reduce_min_sync(0xffffffffu, min(see[0].window_lo(), see[1].window_lo())), kUnit);
+        const int u_lo = hi > 0 ? lo / kUnit : 0, u_hi = gap.count((hi + kUnit - 1) / kUnit);
         const int per = (u_hi - u_lo + S - 1) / S;
         const int ua = u_lo + rank * per, ub = min(u_hi, ua + per);
         const int nu = ub - ua > warp ? (ub - ua - warp + kWarps - 1) / kWarps : 0;  // this warp's units
@@ -160,7 +164,7 @@ pages_rows_kernel(const PagedAttend p) {
         const uint32_t ring = ptx::smem_u32(sm) + warp * (kStages * 2 * UB);
         // the pages of this warp's next 32 units, one per lane
         auto pages_at = [&](int k) {
-            const int u = ua + warp + (k + lane) * kWarps;
+            const int u = gap.number(ua + warp + (k + lane) * kWarps);
             return k + lane < nu ? __ldg(table + ((u * kUnit) >> s.pshift)) : 0;
         };
         int pg_now = pages_at(0), pg_next = 0;
@@ -171,7 +175,7 @@ pages_rows_kernel(const PagedAttend p) {
             }
             if (k < nu) {
                 const int page = __shfl_sync(0xffffffffu, pg_now, k & 31);
-                const int t0 = (ua + warp + k * kWarps) * kUnit;
+                const int t0 = gap.number(ua + warp + k * kWarps) * kUnit;
                 const bool ok = page >= 0 && page < s.pages;
                 if (!ok && lane == 0) pages::flag(s.status, kPgBadPage);
                 const long long at =
@@ -201,7 +205,7 @@ pages_rows_kernel(const PagedAttend p) {
             cp_wait<kStages - 1>();
             __syncwarp();
             const uint32_t sk = ring + (k % kStages) * (2 * UB), sv = sk + UB;
-            const int t0 = (ua + warp + k * kWarps) * kUnit;
+            const int t0 = gap.number(ua + warp + k * kWarps) * kUnit;
             float c[2][4] = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
@@ -316,8 +320,8 @@ pages_rows_kernel(const PagedAttend p) {
                 const int i = (r_begin + r) / p.G, hd = g * p.G + (r_begin + r) - i * p.G;
                 const Seen se = pages::row_seen<SCORED>(p, b.seq, b.q0 + i, T - b.n + i, T);
                 float mm, ll, acc[D / 32];
-                pages::careful_row<D, SCORED>(p, b.seq, b.q0 + i, hd, T - b.n + i, se, ua * kUnit, ub * kUnit, 4,
-                                              (ua + warp) % kWarps, kWarps, mm, ll, acc);
+                pages::careful_row<D, SCORED>(p, b.seq, b.q0 + i, hd, T - b.n + i, se, gap, 4, ua + warp,
+                                              ub, kWarps, mm, ll, acc);
                 float* dst = rows + r * RS;
                 __syncwarp();
 #pragma unroll

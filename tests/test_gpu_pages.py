@@ -84,6 +84,7 @@ SCORES = {
     "cap_slopes_window": dict(cap=20.0, slopes=True, window=100),
     "documents": dict(first=True),
     "prefix": dict(prefix=True),
+    "prefix_window": dict(prefix=True, window=20),
     "prefix_window_documents_cap": dict(prefix=True, window=20, first=True, cap=30.0, slopes=True),
 }
 

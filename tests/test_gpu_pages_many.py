@@ -101,6 +101,39 @@ def test_masked_keys_may_hold_anything(kp, T, chunk, score):
     check_attend(out, lse, ref, T)
 
 
+@pytest.mark.parametrize("room", [0, 1 << 17])  # (the kernel for few rows, that for many)
+@pytest.mark.parametrize("chunk", [1, 20, 100])
+@pytest.mark.parametrize("T,window,prefix", [(1900, 150, 130), (5001, 1, 3), (6000, 1500, 700), (700, 500, 200)])
+def test_between_prefix_and_window(kp, T, window, prefix, chunk, room):
+    """Keys behind the prefix and before every window hold NaN and are passed
+    over; with a chunk, so does its last token, which its own row alone sees."""
+    import torch
+
+    b = Batch(1, 4, 128, 32, [chunk, 1], [T, T - 40], seed=21)
+    if room:
+        b.many(room)
+    pre = np.array([prefix, prefix // 2], np.int32)
+    for s in range(2):
+        gap = max(0, T - 40 * s - b.q[s] - window + 1 - pre[s])
+        page, slot = paged.token_slots(b.table[s], pre[s], gap, b.P)
+        b.K[0, page, :, slot] = np.nan
+        b.V[0, page, :, slot] = np.inf
+    run(kp, b, window=window, prefix=pre)
+    if chunk == 1:
+        return
+    page, slot = paged.token_slots(b.table[0], T - 1, 1, b.P)
+    b.V[0, page, :, slot] = np.nan
+    K, V, layer, Q, table, kv_len, q_start = b.dev()
+    out, lse = kp.pages_attend(K, V, layer, Q, table, kv_len, q_start, return_lse=True, window=window,
+                               prefix=torch.from_numpy(pre).cuda())
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    assert np.isnan(out[chunk - 1]).all()
+    ref = [x.copy() for x in b.ref(window=window, prefix=pre)]
+    for x in ref:
+        x[chunk - 1] = np.nan
+    check_attend(out, lse, ref, T)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_many_sequences(kp, d):
     """More sequences than a warp's lanes, most of one token, some empty."""
