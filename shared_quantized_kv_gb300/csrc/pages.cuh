@@ -144,6 +144,10 @@ struct Seen {
     __device__ __forceinline__ bool all(int u0, int u1) const {
         return (a1 <= u0 && b1 >= u1) || (a2 <= u0 && b2 >= u1);
     }
+    // any key of [u0, u1)
+    __device__ __forceinline__ bool some(int u0, int u1) const {
+        return max(a1, u0) < min(b1, u1) || max(a2, u0) < min(b2, u1);
+    }
     __device__ __forceinline__ int lo() const { return min(b1 > a1 ? a1 : INT_MAX, b2 > a2 ? a2 : INT_MAX); }
     __device__ __forceinline__ int prefix_end() const { return b2 > a2 ? b2 : 0; }
     __device__ __forceinline__ int window_lo() const { return b1 > a1 ? a1 : INT_MAX; }
@@ -191,7 +195,7 @@ __device__ __forceinline__ float2* state_ml(const PagedAttend& a, int t, int hd)
            ((long long)g * in + tl) * a.G + (hd - g * a.G);
 }
 
-// <q, k> -> the score in log2 units, N consecutive keys from j0 on. tanh(y) =
+// <q, k> -> the score in log2 units, of one key and of 32. tanh(y) =
 // 1 - 2 / (e^(2y) + 1): off by a few units of 2^-24 whatever y, which the cap
 // turns into cap * 2^-22 of a score; the reciprocal of an overflowed e^(2y) is
 // 0, as it should be. (One loop per modifier: a choice per key costs more than
@@ -201,29 +205,44 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float capped(const PagedAttend& a, float s) {
-    return fmaf(-2.0f * a.cap2, rcp(ptx::ex2(s * a.cap_in) + 1.0f), a.cap2);
-}
-template <bool SCORED, int N>
-__device__ __forceinline__ void scores(const PagedAttend& a, float (&x)[N], float slope2, int pos, int j0) {
-    if (!SCORED || !(a.cap2 > 0.0f)) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] *= a.scale_log2;
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = capped(a, x[k]);
-    }
-    if (SCORED && a.slopes) {
-        const float far = (float)(pos - j0);
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = fmaf(-slope2, fabsf(far - (float)k), x[k]);
-    }
-}
 template <bool SCORED>
 __device__ __forceinline__ float score(const PagedAttend& a, float s, float slope2, int pos, int j) {
-    float x[1] = {s};
-    scores<SCORED>(a, x, slope2, pos, j);
-    return x[0];
+    if (!SCORED || !(a.cap2 > 0.0f)) s *= a.scale_log2;
+    else s = fmaf(-2.0f * a.cap2, rcp(ptx::ex2(s * a.cap_in) + 1.0f), a.cap2);
+    if (SCORED && a.slopes) s = fmaf(-slope2, fabsf((float)(pos - j)), s);
+    return s;
+}
+// The scores of 32 keys. behind: no key lies behind the row's position, so the
+// distance to key j0 joins the constant and each key costs one more step.
+__device__ __forceinline__ void scores32(const PagedAttend& a, float (&x)[32], float slope2, int pos, int j0,
+                                         bool behind) {
+    const float far = (float)(pos - j0), base = a.slopes && behind ? -slope2 * far : 0.0f;
+    if (!(a.cap2 > 0.0f)) {
+        const float2 f = make_float2(a.scale_log2, a.scale_log2), c = make_float2(base, base);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), f, c);
+            x[k] = y.x, x[k + 1] = y.y;
+        }
+    } else {
+        const float2 in = make_float2(a.cap_in, a.cap_in), one = make_float2(1.0f, 1.0f);
+        const float2 f = make_float2(-2.0f * a.cap2, -2.0f * a.cap2), c = make_float2(a.cap2 + base, a.cap2 + base);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            float2 y = __fmul2_rn(make_float2(x[k], x[k + 1]), in);
+            y = __fadd2_rn(make_float2(ptx::ex2(y.x), ptx::ex2(y.y)), one);
+            y = __ffma2_rn(make_float2(rcp(y.x), rcp(y.y)), f, c);
+            x[k] = y.x, x[k + 1] = y.y;
+        }
+    }
+    if (!a.slopes) return;
+    if (behind) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = fmaf(slope2, (float)k, x[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = fmaf(-slope2, fabsf(far - (float)k), x[k]);
+    }
 }
 
 // One row over the keys it sees in the units [u0, u1) of 2^sh keys, counted
