@@ -15,10 +15,11 @@
 // than 128 rows the slots are the two row tiles, and each K and V tile serves
 // both; with fewer, both slots have the same rows and take every second key
 // tile, and their states are merged at the end.
-//   warp 0        loader: pages by TMA, one box of 64 channels per page, K and
-//                 V tiles through one ring in the order they are needed
-//   warps 1, 2    issuers of the MMAs, one per slot (one lane each)
-//   warps 4-11    softmax, a thread per row of its slot
+//   warps 0, 3    loaders of K and of V: pages by TMA, one box of 64 channels
+//                 per page, through one ring in the order they are needed
+//   warps 1, 2    issuers of the MMAs, one per slot
+//   warps 4-19    softmax, two threads per row of a slot: 32 keys of every 64
+//                 each, and half the channels of the output
 // S_{i+1} of a slot may overwrite P_i because the MMAs of a thread run in the
 // order they are issued. V comes as [key][channel], which the MMA takes as an
 // MN-major operand. The keys may be split over the CTAs of a cluster, whose
@@ -27,13 +28,17 @@
 // the CTA runs to its end without waiting again.
 //
 // Measured on 2,432 new tokens over 16K keys, 32 query heads on 8 KV heads of
-// 128 (two full waves of CTAs): 406 us, 1488 TFLOP/s. What got it there: one
+// 128 (two full waves of CTAs): 341 us, 1770 TFLOP/s. What got it there: one
 // issuer per slot, taking turns (a single one's waits and commits left the
 // tensor cores idle: 466 us; two without turns fell into step: 592 us);
-// operands of the MMAs in uniform registers (509 us before); P formed under
-// the reference as it is, the maxima checked beside it, and handed over in
-// halves; hardly a register spilled (the roles' registers shifted between the
-// warpgroups). The MMAs alone, with no softmax, take 338 us.
+// operands of the MMAs in uniform registers (509 us before; not all of them
+// known to be uniform and no elected lane: 413 us); two threads per row (402 us
+// with one and the same issue, its P too late for its turn); P formed under the
+// reference as it is, the maxima looked at after it, and handed over in halves;
+// hardly a register spilled (the roles' registers shifted between the
+// warpgroups). Pages of 16 tokens are 32 boxes per pair of tiles: one loader
+// issues them in 1.4 times as long as the rest takes (470 us against 341 on
+// 2,048 tokens over 16K), two keep up.
 #include <algorithm>
 #include <mutex>
 
@@ -44,7 +49,7 @@ namespace {
 
 using pages::Seen;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kTile = 128;              // keys per tile, rows per slot
 constexpr int kRows = 2 * kTile;        // rows per CTA
 constexpr int kFewTiles = 8;            // key tiles that a cluster does not split
@@ -53,12 +58,12 @@ constexpr float kLazyMax = 8.0f;        // log2 units the reference may trail th
 constexpr uint32_t kTryNs = 1000, kTries = 1u << 18;
 constexpr uint32_t kCols = 512;         // tensor memory: S0, S1, O0, O1
 // named barriers: Q is staged (issuers and softmax warps); every role is done; the merge rows are written;
-// a slot's turn at the tensor cores; both slots' stores of 32 rows are done
-constexpr uint32_t kBarQ = 1, kBarDone = 2, kBarRows = 3, kBarTurn = 4, kBarOdd = 6;
-constexpr int kSoftmax = 256;           // softmax threads
+// a slot's turn at the tensor cores; the two warps of 32 rows (8 barriers)
+constexpr uint32_t kBarQ = 1, kBarDone = 2, kBarRows = 3, kBarTurn = 4, kBarPair = 6, kBarLoad = 14;
+constexpr int kSoftmax = 512;           // softmax threads
 constexpr float kLn2 = 0.6931471805599453f;
-// registers: 3 warpgroups launched with 168 each; 88 + 2 x 208 = 3 x 168
-constexpr int kRegsFew = 88, kRegsMany = 208;
+// registers: 5 warpgroups launched with 96 each; 64 + 4 x 104 = 5 x 96
+constexpr int kRegsFew = 64, kRegsMany = 104;
 
 template <int D>
 struct Lay {
@@ -69,7 +74,8 @@ struct Lay {
     // barriers: full, empty per ring stage; per slot S, P (of each half), O, all done
     static constexpr int bar_s = bars + 2 * nst * 8, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_fin = bar_o + 16;
     static constexpr int info = bar_fin + 16;  // rng[2][2], tensor memory address, prefixes' end, windows' begin
-    static constexpr int total = info + 32 + 1024;  // + alignment of the base
+    static constexpr int pair = info + 32;       // per slot a float per row, then a word per 32 rows
+    static constexpr int total = pair + 2 * kTile * 4 + 32 + 1024;  // + alignment of the base
     static constexpr int rs = D + 4;             // floats of a merge row: O, m, l
     static_assert(kRows * (rs + kMaxParts) * 4 <= bars, "merge rows and weights fit in the tiles");
     static_assert(total <= 227 * 1024, "shared memory");
@@ -158,8 +164,8 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         for (int w = 0; w < 2; ++w) {
             ptx::mbar_init(b_s + 8 * w, 1);
-            ptx::mbar_init(b_p + 16 * w, 4);  // P of the tile's first half, of its second
-            ptx::mbar_init(b_p + 16 * w + 8, 4);
+            ptx::mbar_init(b_p + 16 * w, 8);  // P of the tile's first half, of its second
+            ptx::mbar_init(b_p + 16 * w + 8, 8);
             ptx::mbar_init(b_o + 8 * w, 1);
             ptx::mbar_init(b_fin + 8 * w, 1);
             rng[2 * w] = INT_MAX;
@@ -172,7 +178,8 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     if constexpr (SCORED) __syncthreads();
 
     // softmax threads: their row and what it sees
-    const int w = (warp - 4) / 4;          // slot
+    const int w = (warp - 4) / 8;          // slot
+    const int part = ((warp - 4) / 4) & 1; // of a row: 32 keys of every 64, half the channels
     const int lr = tid & 127;              // row of the slot
     const int row = two ? w * kTile + lr : lr;
     const bool live = warp >= 4 && row < nr;
@@ -237,14 +244,14 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         if (warp == 1) ptx::tmem_dealloc(tmem, kCols);
         return;
     }
-    const bool direct = S == 1;  // the rows' states never leave this CTA
+    const bool direct = S == 1 && two;  // a row has one state
     bool bad = false;
     float* rows = reinterpret_cast<float*>(sm);  // merge rows, once the tiles are done with
 
     if (warp < 4) {
         ptx::regs_dec<kRegsFew>();
-        if (warp == 0) {
-            // ------------------------------------------------------- loader
+        if (warp == 0 || warp == 3) {
+            // ------------------------------------------------------- loaders
             const int P = 1 << s.pshift, np = kTile >> s.pshift;  // pages per tile
             const int32_t* table = s.table + (long long)b.seq * s.tstride;
             const int none = s.pages * (s.Hk << s.pshift);  // a row behind the last: reads as zeros
@@ -274,15 +281,22 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 __syncwarp();
             };
+            // warp 0 loads K, warp 3 V, tile by tile together (a stage's wait by parity
+            // needs its load before to be under way)
             int r0 = page_row(0), r1 = page_row(1);
-            if (n > 0) load(0, r0, &kmap);
+            if (n > 0 && warp == 0) load(0, r0, &kmap);
             for (int i = 0; i < n; ++i) {
                 const int r2 = page_row(i + 2);
-                if (i + 1 < n) load(k_entry(i + 1), r1, &kmap);
-                load(v_entry(i, n), r0, &vmap);
+                ptx::bar_sync(kBarLoad, 64);
+                if (warp == 0) {
+                    if (i + 1 < n) load(k_entry(i + 1), r1, &kmap);
+                } else {
+                    load(v_entry(i, n), r0, &vmap);
+                }
                 r0 = r1;
                 r1 = r2;
             }
+            ptx::bar_sync(kBarLoad, 64);
             // every requested tile has landed before the CTA may go on
             for (int e = max(0, 2 * n - L::nst); e < 2 * n; ++e)
             {
@@ -296,12 +310,10 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             // left the tensor cores idle). The whole warp runs this with uniform
             // values; lane 0 issues.
             ptx::bar_sync(kBarQ, 64 + kSoftmax);  // Q is in shared memory
-            const uint32_t lead = lane == 0;
-            const int slot = __shfl_sync(0xffffffffu, warp - 1, 0);
-            const int nn = __shfl_sync(0xffffffffu, n, 0), nt = __shfl_sync(0xffffffffu, tiles_of(slot), 0);
-            const bool pairs = __shfl_sync(0xffffffffu, (int)two, 0) != 0;
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t base = __shfl_sync(0xffffffffu, ptx::smem_u32(sm), 0), ring = base + L::ring;
+            auto uniform = [](auto x) { return __reduce_max_sync(0xffffffffu, x); };
+            const int slot = uniform(warp - 1), nn = uniform(n), nt = uniform(tiles_of(slot));
+            const bool pairs = __any_sync(0xffffffffu, two);
+            const uint32_t tm = uniform(tmem), base = uniform(ptx::smem_u32(sm)), ring = base + L::ring;
             const uint32_t tS = tm + kColS + 128 * slot, tO = tm + kColO + 128 * slot;
             const uint32_t idS = ptx::idesc_bf16(kTile, kTile, 0, 0);
             const uint32_t idO = ptx::idesc_bf16(kTile, D, 0, 1);
@@ -310,15 +322,15 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const uint32_t u_o = base + L::bar_o + 8 * slot, u_fin = base + L::bar_fin + 8 * slot;
             const uint64_t dq = ptx::sdesc(base + (pairs ? slot : 0) * L::stage, 16, 1024);
             auto full = [&](int e) { warp_wait(u_full + 8 * (e % L::nst), (e / L::nst) & 1, bad); };
-            auto release = [&](int e) { ptx::mma_commit_lead(lead, u_empty + 8 * (e % L::nst)); };
+            auto release = [&](int e) { ptx::mma_commit_elect(u_empty + 8 * (e % L::nst)); };
             auto qk = [&](int e) {
                 const uint64_t dk = ptx::sdesc(ring + (e % L::nst) * L::stage, 16, 1024);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t o = ((ks / 4) * (kTile * 128) + (ks % 4) * 32) >> 4;  // descriptor units
-                    ptx::mma_f16_lead(lead, tS, dq + o, dk + o, idS, ks > 0 ? 1u : 0u);
+                    ptx::mma_f16_elect(tS, dq + o, dk + o, idS, ks > 0 ? 1u : 0u);
                 }
-                ptx::mma_commit_lead(lead, u_s);
+                ptx::mma_commit_elect(u_s);
             };
             auto pv = [&](int e, int it) {
                 const uint64_t dv = ptx::sdesc(ring + (e % L::nst) * L::stage, kTile * 128, 1024);
@@ -329,13 +341,12 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         ptx::tc_fence_after();
                     }
 #pragma unroll
-                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks) {  // P of half h: 32 columns from column 64 h on
-                        ptx::mma_f16_ta_lead(lead, tO, tS + 32 * h + ks * 8, dv + ks * (2048 >> 4), idO,
-                                             (it > 0 || ks > 0) ? 1u : 0u);
-                        if constexpr (STATE)
-                            ptx::mma_f16_ta_lead(lead, tO, tS + 32 * h + ks * 8 + 32, dv + ks * (2048 >> 4), idO, 1u);
+                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks) {  // P of 32 keys: 16 columns at S's 32
+                        const uint32_t tP = tS + 32 * (ks / 2) + 8 * (ks % 2);
+                        ptx::mma_f16_ta_elect(tO, tP, dv + ks * (2048 >> 4), idO, (it > 0 || ks > 0) ? 1u : 0u);
+                        if constexpr (STATE) ptx::mma_f16_ta_elect(tO, tP + 16, dv + ks * (2048 >> 4), idO, 1u);
                     }
-                    ptx::mma_commit_lead(lead, u_o);
+                    if (SCORED && h == 0) ptx::mma_commit_elect(u_o);
                 }
             };
             // The slots take turns: P V and the next Q K^T of one, then of the other, so
@@ -355,14 +366,14 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (own) pv(ev, it);
                 if (more) qk(ek);
                 ptx::bar_arrive(kBarTurn + 1 - slot, 64);
-                if (own && !more) ptx::mma_commit_lead(lead, u_fin);  // the slot's last MMAs
+                if (own && !more) ptx::mma_commit_elect(u_fin);  // the slot's last MMAs
                 if (own) release(ev);
                 if (more) release(ek);
             };
             // a tile that the other slot alone works on: its K or V is not needed here
             auto pass = [&](int e) {
                 full(e);
-                if (lead) ptx::mbar_arrive(u_empty + 8 * (e % L::nst));
+                if (lane == 0) ptx::mbar_arrive(u_empty + 8 * (e % L::nst));
             };
             if (pairs) {
                 if (nn > 0) {
@@ -418,8 +429,10 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             __syncwarp();
         }
         if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
-        if (!direct || !two) ptx::bar_sync(kBarDone, kThreads);
-        if (!direct) ptx::bar_sync(kBarRows, kThreads);
+        if (!direct) {
+            ptx::bar_sync(kBarDone, kThreads);
+            ptx::bar_sync(kBarRows, kThreads);
+        }
     } else {
         ptx::regs_inc<kRegsMany>();
         float m = -CUDART_INF_F, l = 0.0f;
@@ -432,18 +445,18 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             // before it, 16 thousand cycles in all instead of 4)
             constexpr int CH = D / 8;
             unsigned char* dst = sm + w * L::stage;
-            const int first = two ? w * kTile : 0;
-            uint4 v[CH];
+            const int first = two ? w * kTile : 0, at = tid & 255;
+            uint4 v[CH / 2];
 #pragma unroll
-            for (int k = 0; k < CH; ++k) {
-                const int x = k * kTile + (tid & 127), r = min(first + x / CH, nr - 1), c = x % CH;
+            for (int k = 0; k < CH / 2; ++k) {
+                const int x = k * 256 + at, r = min(first + x / CH, nr - 1), c = x % CH;
                 const int i = pages::div_group(p, j_begin + r);
                 v[k] = ptx::ldg16(p.Q + (long long)(b.q0 + i_begin + i) * p.q_stride +
                                   (long long)(g * p.G + j_begin + r - i * p.G) * D + c * 8);
             }
 #pragma unroll
-            for (int k = 0; k < CH; ++k) {
-                const int x = k * kTile + (tid & 127), r = x / CH, c = x % CH;
+            for (int k = 0; k < CH / 2; ++k) {
+                const int x = k * 256 + at, r = x / CH, c = x % CH;
                 *reinterpret_cast<uint4*>(dst + (c / 8) * (kTile * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v[k];
             }
             ptx::fence_proxy_async();  // the MMAs read Q through the async proxy
@@ -453,28 +466,80 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const bool some = __any_sync(0xffffffffu, live);
         const float slope2 = SCORED && live && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.0f;
         const uint32_t tS = tmem + kColS + 128 * w + lane_off, tO = tmem + kColO + 128 * w + lane_off;
-        if (!SCORED && mine > 0 && some) {
-            // the maximum of the first half tile, where no key is masked, is the
-            // first reference
-            const int t0 = (ta + (two ? 0 : w)) * kTile;  // (plain scores: no gap)
-            if (__all_sync(0xffffffffu, see.all(t0, t0 + 64))) {
-                warp_wait(b_s + 8 * w, 0, bad);
-                ptx::tc_fence_after();
-                float x = -CUDART_INF_F;
-#pragma unroll 1
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t u[32];
-                    ptx::tmem_ld32(tS + c, u);
-                    ptx::tmem_wait_ld(u);
+        float* xch = reinterpret_cast<float*>(sm + L::pair) + w * kTile + lr;
+        const uint32_t b_pair = kBarPair + 4 * w + (warp & 3);
+        // both threads of a row: the maximum (or the sum, part 0's first) of their values
+        auto joined = [&](float x, bool add) {
+            if (!part) *xch = x;
+            ptx::bar_sync(b_pair, 64);
+            if (part) *xch = x = add ? *xch + x : fmaxf(*xch, x);
+            ptx::bar_sync(b_pair, 64);
+            return part ? x : *xch;
+        };
+        // keys of the part's 32 that the row does not see, in tile half k0: -inf
+        auto mask = [&](int k0, uint32_t (&u)[32]) {
+            uint32_t bits = span_bits(see.a1 - k0, see.b1 - k0, 0);
+            if constexpr (SCORED) bits |= span_bits(see.a2 - k0, see.b2 - k0, 0);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) x = ptx::max3(x, asf(u[k]), asf(u[k + 1]));
+            for (int k = 0; k < 32; ++k)
+                if (!(bits >> k & 1u)) u[k] = asu(-CUDART_INF_F);
+        };
+        auto max_of = [&](const uint32_t (&u)[32]) {
+            auto f = [&](int k) { return asf(u[k]); };
+            float x[11];
+#pragma unroll
+            for (int k = 0; k < 10; ++k) x[k] = ptx::max3(f(3 * k), f(3 * k + 1), f(3 * k + 2));
+            x[10] = fmaxf(f(30), f(31));
+            return ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
+                             ptx::max3(x[7], x[8], x[9]), x[10]);
+        };
+        // the row's reference becomes mt (its maximum in both parts) where that passes
+        // it; O, which no MMA works on, follows
+        auto move_ref = [&](float mine_max, bool summed) {
+            const float mt = joined(mine_max, false);
+            const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
+            if (summed) {
+                const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
+                l *= al;
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 32) {
+                    uint32_t o[32];
+                    ptx::tmem_ld32(tO + part * (D / 2) + c, o);
+                    ptx::tmem_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = asu(asf(o[k]) * al);
+                    ptx::tmem_st32x(tO + part * (D / 2) + c, o);
                 }
-                m = x * p.scale_log2;
+                ptx::tmem_wait_st();
             }
+            if (move) m = mt;
+        };
+        if (!SCORED && mine > 0 && some) {
+            // The first reference is the maximum of the first half tile. (A row that
+            // sees none of its keys sees none at all: the causal mask alone.)
+            const int t0 = (ta + (two ? 0 : w)) * kTile;  // (plain scores: no gap)
+            warp_wait(b_s + 8 * w, 0, bad);
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t u[32];
+                ptx::tmem_ld32(tS + c, u);
+                ptx::tmem_wait_ld(u);
+                mask(t0 + c, u);
+                m = fmaxf(m, max_of(u));
+            }
+            m *= p.scale_log2;
+            ptx::bar_sync(b_pair, 64);  // P of either part overwrites what both have read
         }
+        float top = -CUDART_INF_F;  // plain scores: the part's maximum in the tile before
         for (int it = 0; it < mine; ++it) {
             const int i = two ? it : 2 * it + w;  // tile of this CTA
             const int t0 = gap.number(ta + i) * kTile;
+            // Plain scores: a maximum that passes the reference by 2^8 moves it before
+            // the next tile (until then the weights are that much larger, which they
+            // may be by 2^118; rows beyond it come out infinite and are done again).
+            // The two threads of a row ask one another while S is on its way.
+            const bool moves = !SCORED && it > 0 && some && ptx::bar_or(b_pair, 64, top > m + kLazyMax);
             warp_wait(b_s + 8 * w, it & 1, bad);
             ptx::tc_fence_after();
             // keys behind the sequence's end: whatever their V holds becomes 0 (a
@@ -487,8 +552,10 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (t0 + lr >= T) {
                     unsigned char* v = sm + L::ring + (e % L::nst) * L::stage + lr * 128;
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        *reinterpret_cast<uint4*>(v + (c / 8) * (kTile * 128) + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < D / 16; ++c) {
+                        const int ch = part * (D / 16) + c;
+                        *reinterpret_cast<uint4*>(v + (ch / 8) * (kTile * 128) + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    }
                 }
                 ptx::fence_proxy_async();
             }
@@ -497,174 +564,59 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (lane < 2) ptx::mbar_arrive(b_p + 16 * w + 8 * lane);
                 continue;
             }
+            if (moves) move_ref(top, true);  // (S came after every P V before it)
+            top = -CUDART_INF_F;
             // The tile's keys in two halves, so that P V of the first runs while P of
-            // the second is formed. P under the reference as it is, its row maxima on
-            // the way; only where a maximum passes the reference (the first half
-            // tile, and rarely after it) is the reference moved and P formed again:
-            // the maxima cost no time of their own on the chain from S to P.
+            // the second is formed; a thread has 32 keys of each.
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                const int k0 = t0 + 64 * h;  // first key of the half
-                const uint32_t tSh = tS + 64 * h;
-                const bool whole = __all_sync(0xffffffffu, see.all(k0, k0 + 64));
-                // nothing seen (beyond the diagonal, other documents): weights of 0 whatever S
-                // holds. (Plain scores: only the diagonal's halves, which save less than this
-                // test costs every tile: 404 us against 418 on the tiles of the header.)
-                const bool any = !SCORED || __any_sync(0xffffffffu, live && see.some(k0, k0 + 64));
-                uint32_t pw[2][16], pl[STATE ? 2 : 1][16];  // (pl: STATE)
-                float2 sum[2];
-                if (!any) {
-                    sum[0] = sum[1] = make_float2(0.f, 0.f);
+                const int half = t0 + 64 * h, k0 = half + 32 * part;  // first keys of the half, of the part
+                const uint32_t tSh = tS + 64 * h + 32 * part;
+                const bool whole = __all_sync(0xffffffffu, see.all(k0, k0 + 32));
+                // nothing seen by either part (beyond the diagonal, other documents): weights
+                // of 0 whatever S holds
+                const bool any = !SCORED || __any_sync(0xffffffffu, live && see.some(half, half + 64));
+                uint32_t pw[16], pl[STATE ? 16 : 1];
+                float2 sum[2] = {};
+                if (any) {
+                    uint32_t u[32];
+                    ptx::tmem_ld32(tSh, u);
+                    const bool behind = SCORED && p.slopes && __all_sync(0xffffffffu, !live || pos >= k0 + 31);
+                    ptx::tmem_wait_ld(u);
+                    if constexpr (SCORED)
+                        pages::scores32(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0, behind);
+                    if (!whole) mask(k0, u);
+                    const float x = max_of(u);
+                    if constexpr (SCORED) {
+                        if (ptx::bar_or(b_pair, 64, x > m + kLazyMax || (m == -CUDART_INF_F && x > m))) {
+                            if (h) {  // (S came after every P V but the first half's)
+                                warp_wait(b_o + 8 * w, it & 1, bad);
+                                ptx::tc_fence_after();
+                            }
+                            move_ref(x, it > 0 || h > 0);
+                        }
+                    } else {
+                        top = fmaxf(top, x * p.scale_log2);
+                    }
+                    const float ref = m == -CUDART_INF_F ? 0.0f : m;
+                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), nm = make_float2(-ref, -ref);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        pw[0][k] = pw[1][k] = 0u;
-                        if constexpr (STATE) pl[0][k] = pl[1][k] = 0u;
+                        const float2 y = make_float2(asf(u[2 * k]), asf(u[2 * k + 1]));
+                        const float2 d = SCORED ? __fadd2_rn(y, nm) : __ffma2_rn(y, sc, nm);
+                        const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
+                        sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+                        pw[k] = pack_bf2(e.x, e.y);
+                        if constexpr (STATE)
+                            pl[k] = pack_bf2(e.x - asf(pw[k] << 16), e.y - asf(pw[k] & 0xFFFF0000u));
                     }
-                } else if constexpr (SCORED) {
-                    // forming the scores again would cost more than waiting for the maxima
-                    uint32_t u0[32], u1[32];
-                    float mm[2];
-                    const bool behind = p.slopes && __all_sync(0xffffffffu, !live || pos >= k0 + 63);
-                    // chunk c (32 keys): scores, masked
-                    auto finish_s = [&](int c, uint32_t (&u)[32]) {
-                        pages::scores32(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0 + 32 * c, behind);
-                        if (!whole) {
-                            uint32_t bits = span_bits(see.a1 - k0, see.b1 - k0, c);
-                            bits |= span_bits(see.a2 - k0, see.b2 - k0, c);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(bits >> k & 1u)) u[k] = asu(-CUDART_INF_F);
-                        }
-                    };
-                    auto max_of = [&](int c, const uint32_t (&u)[32]) {
-                        auto f = [&](int k) { return asf(u[k]); };
-                        float x[11];
-#pragma unroll
-                        for (int k = 0; k < 10; ++k) x[k] = ptx::max3(f(3 * k), f(3 * k + 1), f(3 * k + 2));
-                        x[10] = fmaxf(f(30), f(31));
-                        mm[c] = ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
-                                          ptx::max3(x[7], x[8], x[9]), x[10]);
-                    };
-                    auto weights_of = [&](int c, const uint32_t (&u)[32]) {
-                        const float ref = m == -CUDART_INF_F ? 0.0f : m;
-                        const float2 nm = make_float2(-ref, -ref);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float2 d = __fadd2_rn(make_float2(asf(u[2 * k]), asf(u[2 * k + 1])), nm);
-                            const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
-                            sum[k & 1] = __fadd2_rn(sum[k & 1], e);
-                            pw[c][k] = pack_bf2(e.x, e.y);
-                        }
-                    };
-                    // the reference moves where the maximum passes it
-                    auto move_ref = [&]() {
-                        const float mt = fmaxf(mm[0], mm[1]);
-                        const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
-                        if (!__any_sync(0xffffffffu, move)) return;
-                        const int before = 2 * it + h;  // half tiles of the slot before this one
-                        if (before > 0) {
-                            // O in the old reference: the P V of the half before has to be done
-                            // (the one before that is: S of this tile came after it)
-                            warp_wait(b_o + 8 * w, (before - 1) & 1, bad);
-                            ptx::tc_fence_after();
-                            const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
-                            l *= al;
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                ptx::tmem_ld32(tO + c, o);
-                                ptx::tmem_wait_ld(o);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = asu(asf(o[k]) * al);
-                                ptx::tmem_st32x(tO + c, o);
-                            }
-                            ptx::tmem_wait_st();
-                        }
-                        if (move) m = mt;
-                    };
-                    ptx::tmem_ld32(tSh, u0);
-                    ptx::tmem_ld32(tSh + 32, u1);
-                    ptx::tmem_wait_ld(u0);
-                    ptx::tmem_wait_ld(u1);
-                    finish_s(0, u0);
-                    finish_s(1, u1);
-                    max_of(0, u0);
-                    max_of(1, u1);
-                    move_ref();
-                    sum[0] = sum[1] = make_float2(0.f, 0.f);
-                    weights_of(0, u0);
-                    weights_of(1, u1);
                 } else {
-#pragma unroll 1
-                    for (;;) {
-                        const float ref = m == -CUDART_INF_F ? 0.0f : m;
-                        const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-                        const float2 nm = make_float2(-ref, -ref);
-                        float mm[2];
-                        sum[0] = sum[1] = make_float2(0.f, 0.f);
-                        auto form = [&](int c, uint32_t (&u)[32]) {
-                            if (!whole) {
-                                uint32_t bits = span_bits(see.a1 - k0, see.b1 - k0, c);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (!(bits >> k & 1u)) u[k] = asu(-CUDART_INF_F);
-                            }
-                            auto f = [&](int k) { return asf(u[k]); };
-                            float x[11];
-#pragma unroll
-                            for (int k = 0; k < 10; ++k) x[k] = ptx::max3(f(3 * k), f(3 * k + 1), f(3 * k + 2));
-                            x[10] = fmaxf(f(30), f(31));
-                            mm[c] = ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
-                                              ptx::max3(x[7], x[8], x[9]), x[10]);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float2 d = __ffma2_rn(make_float2(f(2 * k), f(2 * k + 1)), sc, nm);
-                                const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
-                                sum[k & 1] = __fadd2_rn(sum[k & 1], e);
-                                pw[c][k] = pack_bf2(e.x, e.y);
-                                if constexpr (STATE)
-                                    pl[c][k] = pack_bf2(e.x - asf(pw[c][k] << 16), e.y - asf(pw[c][k] & 0xFFFF0000u));
-                            }
-                        };
-                        uint32_t u0[32], u1[32];  // the second chunk is on its way while the first is worked on
-                        ptx::tmem_ld32(tSh, u0);
-                        ptx::tmem_wait_ld(u0);
-                        ptx::tmem_ld32(tSh + 32, u1);
-                        form(0, u0);
-                        ptx::tmem_wait_ld(u1);
-                        form(1, u1);
-                        const float top = fmaxf(mm[0], mm[1]);
-                        // plain scores are scaled in the exponent's fused step (the scale is positive)
-                        const float mt = top * p.scale_log2;
-                        const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
-                        if (!__any_sync(0xffffffffu, move)) break;
-                        const int before = 2 * it + h;  // half tiles of the slot before this one
-                        if (before > 0) {
-                            // O in the old reference: the P V of the half before has to be done
-                            // (the one before that is: S of this tile came after it)
-                            warp_wait(b_o + 8 * w, (before - 1) & 1, bad);
-                            ptx::tc_fence_after();
-                            const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
-                            l *= al;
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                ptx::tmem_ld32(tO + c, u0);
-                                ptx::tmem_wait_ld(u0);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) u0[k] = asu(asf(u0[k]) * al);
-                                ptx::tmem_st32x(tO + c, u0);
-                            }
-                            ptx::tmem_wait_st();
-                        }
-                        if (move) m = mt;
-                    }
+                    for (int k = 0; k < 16; ++k) pw[k] = 0u;
                 }
-                // P over the half's own columns of S
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    ptx::tmem_st16(tSh + 16 * c, pw[c]);
-                    if constexpr (STATE) ptx::tmem_st16(tSh + 32 + 16 * c, pl[c]);
-                }
+                // P over the part's own columns of S
+                ptx::tmem_st16(tSh, pw);
+                if constexpr (STATE) ptx::tmem_st16(tSh + 16, pl);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -673,9 +625,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
         }
         if (mine > 0) {
-            // every MMA of the slot (a barrier of one phase: of b_o's last two phases
-            // either may be the one under way here, which a parity cannot tell)
-            warp_wait(b_fin + 8 * w, 0, bad);
+            warp_wait(b_fin + 8 * w, 0, bad);  // every MMA of the slot
             ptx::tc_fence_after();
         }
         if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
@@ -692,7 +642,9 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                                           __shfl_sync(0xffffffffu, head, of), __shfl_sync(0xffffffffu, pos, of), se,
                                           gap, 7, two || all ? ta : ta + w, ta + n, two || all ? 1 : 2, cm, cl, acc);
         };
+        l = joined(l, true);
         bool odd = live && l != 0.0f && !finite(l);  // sums that a masked key may have spoilt
+        uint32_t* flags = reinterpret_cast<uint32_t*>(sm + L::pair + 2 * kTile * 4) + 4 * w + (warp & 3);
         // a row's last numbers: m and l, or their logarithm
         auto finish = [&](int t, int hd, float rm, float rl) {
             if constexpr (STATE)
@@ -731,14 +683,17 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
             }
         };
-        if (direct && two) {
-            // A row's thread has its output; the slot's Q (no MMA reads it any more)
-            // takes it as bf16, and the warp writes whole rows of it.
+        // a row's channels of this thread
+        constexpr int HC = D / 2;
+        const int c0 = part * HC;
+        if (direct) {
+            // The slot's Q (no MMA reads it any more) takes the output as bf16, and the
+            // two warps write whole rows of it, 16 each.
             const float inv = STATE ? 1.0f : 1.0f / l;  // (not used where l is 0)
             constexpr int CH = D / 8;
             unsigned char* stage = sm + w * L::stage + (warp & 3) * 32 * (D * 2);
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = c0; c < c0 + HC; c += 32) {
                 uint32_t o[32];
                 float y[32];
                 ptx::tmem_ld32(tO + c, o);
@@ -758,98 +713,47 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                                        pack_bf2(y[k + 4], y[k + 5]), pack_bf2(y[k + 6], y[k + 7]));
                 }
             }
-            if (live) finish(tok, head, l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m), l);
-            __syncwarp();
+            if (live && !part) finish(tok, head, l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m), l);
+            const unsigned odds = __ballot_sync(0xffffffffu, odd);
+            if (part && lane == 0) *flags = odds;
+            ptx::bar_sync(b_pair, 64);
             if constexpr (!STATE) {
                 const long long at = live ? ((long long)tok * p.Hq + head) * D : -1;
 #pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    const int x = k * 32 + lane, r = x / CH, c = x % CH;
+                for (int k = 0; k < CH / 2; ++k) {
+                    const int x = k * 32 + lane, r = 16 * part + x / CH, c = x % CH;
                     const long long to = __shfl_sync(0xffffffffu, at, r);
                     const uint4 v = *reinterpret_cast<const uint4*>(stage + r * (D * 2) + ((c ^ (r & 7)) << 4));
                     if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + c * 8) = v;
                 }
-                __syncwarp();
+                ptx::bar_sync(b_pair, 64);  // both warps' rows are written
             }
-            again(__ballot_sync(0xffffffffu, odd));  // (writes odd rows once more)
-        } else if (direct) {
-            // Both slots have the row: each hands half its channels to the other
-            // and writes the rest. A row: the half of slot 0, of slot 1, then
-            // (m, l) of both; l = NaN marks a state with sums that are not finite.
-            ptx::bar_sync(kBarDone, kThreads);  // no MMA reads the tiles any more, every load has landed
-            float* mine_at = rows + lr * L::rs;
-            constexpr int HC = D / 2;
-            uint32_t keep[HC];
-#pragma unroll
-            for (int c = 0; c < HC; c += 32) {
-                uint32_t o[32];
-                ptx::tmem_ld32(tO + (1 - w) * HC + c, o);
-                ptx::tmem_wait_ld(o);
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    const float4 v = make_float4(asf(o[k]), asf(o[k + 1]), asf(o[k + 2]), asf(o[k + 3]));
-                    odd = odd || (live && l != 0.0f && !(finite(v.x) && finite(v.y) && finite(v.z) && finite(v.w)));
-                    *reinterpret_cast<float4*>(mine_at + w * HC + c + k) = v;
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < HC; c += 32) {
-                uint32_t (&o)[32] = *reinterpret_cast<uint32_t (*)[32]>(keep + c);
-                ptx::tmem_ld32(tO + w * HC + c, o);
-                ptx::tmem_wait_ld(o);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) odd = odd || (live && l != 0.0f && !finite(asf(o[k])));
-            }
-            *reinterpret_cast<float2*>(mine_at + D + 2 * w) =
-                make_float2(l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m), odd ? CUDART_NAN_F : l);
-            ptx::bar_sync(kBarRows, kSoftmax);
-            const float4 ml = *reinterpret_cast<const float4*>(mine_at + D);
-            const float M = fmaxf(ml.x, ml.z);
-            const float f0 = ml.y == 0.0f ? 0.0f : ptx::ex2(ml.x - M), f1 = ml.w == 0.0f ? 0.0f : ptx::ex2(ml.z - M);
-            const float Lt = fmaf(f0, ml.y, f1 * ml.w);
-            const float inv = STATE ? 1.0f : Lt == 0.0f ? 0.0f : 1.0f / Lt;
-            const float fm = (w ? f1 : f0) * inv, fo = (w ? f0 : f1) * inv;  // own and other slot's weight
-            const bool none = (w ? ml.w : ml.y) == 0.0f, onone = (w ? ml.y : ml.w) == 0.0f;
-            odd = live && Lt != 0.0f && !finite(Lt);
-#pragma unroll
-            for (int c = 0; c < HC; c += 32) {
-                float y[32];
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(mine_at + (1 - w) * HC + c + k);
-                    const float ov[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[k + e] = (none ? 0.0f : asf(keep[c + k + e]) * fm) + (onone ? 0.0f : ov[e] * fo);
-                }
-                if (live) store32(w * HC + c, y);
-            }
-            if (live && !w) finish(tok, head, M, Lt);
-            if (__any_sync(0xffffffffu, odd)) {
-                ptx::bar_sync(kBarOdd + (warp & 3), 64);  // after both halves' stores
-                if (!w) again(__ballot_sync(0xffffffffu, odd));
-            }
+            if (!part) again(odds | *flags);  // (writes odd rows once more)
         } else {
             // states into shared memory, once no MMA reads the tiles any more and
             // every load has landed
             ptx::bar_sync(kBarDone, kThreads);
             float* dst = rows + (w * kTile + lr) * L::rs;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = c0; c < c0 + HC; c += 32) {
                 uint32_t o[32];
-                ptx::tmem_ld32(tO + 32 * c, o);
+                ptx::tmem_ld32(tO + c, o);
                 ptx::tmem_wait_ld(o);
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     const float4 v = make_float4(asf(o[k]), asf(o[k + 1]), asf(o[k + 2]), asf(o[k + 3]));
                     odd = odd || (live && l != 0.0f && !(finite(v.x) && finite(v.y) && finite(v.z) && finite(v.w)));
-                    *reinterpret_cast<float4*>(dst + c * 32 + k) = v;
+                    *reinterpret_cast<float4*>(dst + c + k) = v;
                 }
             }
-            dst[D] = l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m);
-            dst[D + 1] = l;
-            __syncwarp();
-            for (unsigned odds = __ballot_sync(0xffffffffu, odd); odds; odds &= odds - 1) {
+            if (!part) {
+                dst[D] = l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m);
+                dst[D + 1] = l;
+            }
+            const unsigned mine_odd = __ballot_sync(0xffffffffu, odd);
+            if (part && lane == 0) *flags = mine_odd;
+            ptx::bar_sync(b_pair, 64);
+            for (unsigned odds = part ? 0u : mine_odd | *flags; odds; odds &= odds - 1) {
                 const int of = __ffs(odds) - 1;
                 float cm, cl, acc[D / 32];
                 careful(of, false, cm, cl, acc);
