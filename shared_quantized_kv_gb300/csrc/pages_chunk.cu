@@ -71,7 +71,7 @@ struct Lay {
     static constexpr int nst = D == 128 ? 5 : 10;
     static constexpr int ring = 2 * stage;       // after the two Q tiles
     static constexpr int bars = ring + nst * stage;
-    // barriers: full, empty per ring stage; per slot S, P (of each half), O, all done
+    // barriers: full, empty per ring stage; per slot S, P (of each half), P V of the first, all done
     static constexpr int bar_s = bars + 2 * nst * 8, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_fin = bar_o + 16;
     static constexpr int info = bar_fin + 16;  // rng[2][2], tensor memory address, prefixes' end, windows' begin
     static constexpr int pair = info + 32;       // per slot a float per row, then a word per 32 rows
@@ -119,14 +119,19 @@ __device__ __forceinline__ uint32_t span_bits(int a, int b, int c) {
     return upto & ~(x == 32 ? 0xffffffffu : (1u << x) - 1u);
 }
 
+// KIND: the causal mask alone; other masks too; scores that a cap or a bias by
+// distance changes (the two costs are apart: 2,432 tokens over 16K keys take
+// 342 us, 434 and 850).
+enum { kPlain, kMasks, kScores };
 // STATE: the rows' states for a merge instead of the output; the weights then
 // go through the product with V as bf16 hi and lo (16 bits; lo in the half of
 // S's columns that hi leaves), as the merged output is float32.
-template <int D, bool SCORED, bool STATE>
+template <int D, int KIND, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1)
 pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const PagedAttend p) {
     using L = Lay<D>;
+    constexpr bool SCORED = KIND != kPlain;
     constexpr uint32_t kColS = 0, kColO = 256;  // slot w: 128 w columns on
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(
@@ -346,7 +351,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         ptx::mma_f16_ta_elect(tO, tP, dv + ks * (2048 >> 4), idO, (it > 0 || ks > 0) ? 1u : 0u);
                         if constexpr (STATE) ptx::mma_f16_ta_elect(tO, tP + 16, dv + ks * (2048 >> 4), idO, 1u);
                     }
-                    if (SCORED && h == 0) ptx::mma_commit_elect(u_o);
+                    if (KIND == kScores && h == 0) ptx::mma_commit_elect(u_o);  // (it takes over 100 cycles)
                 }
             };
             // The slots take turns: P V and the next Q K^T of one, then of the other, so
@@ -531,15 +536,24 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             m *= p.scale_log2;
             ptx::bar_sync(b_pair, 64);  // P of either part overwrites what both have read
         }
-        float top = -CUDART_INF_F;  // plain scores: the part's maximum in the tile before
+        float top = -CUDART_INF_F;  // the part's maximum in the tile before
+        const float scale = KIND == kScores ? 1.0f : p.scale_log2;  // of scores in units of log2 already, or not
+        // the scores of the part's 32 keys from k0 on, -inf where the row sees none
+        auto in_log2 = [&](int k0, bool whole, uint32_t (&u)[32]) {
+            if constexpr (KIND == kScores) {
+                const bool behind = p.slopes && __all_sync(0xffffffffu, !live || pos >= k0 + 31);
+                pages::scores32(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0, behind);
+            }
+            if (!whole) mask(k0, u);
+        };
         for (int it = 0; it < mine; ++it) {
             const int i = two ? it : 2 * it + w;  // tile of this CTA
             const int t0 = gap.number(ta + i) * kTile;
-            // Plain scores: a maximum that passes the reference by 2^8 moves it before
-            // the next tile (until then the weights are that much larger, which they
-            // may be by 2^118; rows beyond it come out infinite and are done again).
-            // The two threads of a row ask one another while S is on its way.
-            const bool moves = !SCORED && it > 0 && some && ptx::bar_or(b_pair, 64, top > m + kLazyMax);
+            // A maximum that passes the reference by 2^8 moves it: where scores cost much
+            // to form or may rise fast (kScores) at once, else before the next tile (until then the weights are that much larger, which they may be by 2^118;
+            // rows beyond it come out infinite and are done again). The two threads of a
+            // row ask one another while S is on its way.
+            const bool moves = KIND != kScores && it > 0 && some && ptx::bar_or(b_pair, 64, top > m + kLazyMax);
             warp_wait(b_s + 8 * w, it & 1, bad);
             ptx::tc_fence_after();
             // keys behind the sequence's end: whatever their V holds becomes 0 (a
@@ -564,8 +578,21 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (lane < 2) ptx::mbar_arrive(b_p + 16 * w + 8 * lane);
                 continue;
             }
-            if (moves) move_ref(top, true);  // (S came after every P V before it)
+            // (S came after every P V before it: O rests)
+            if (moves) move_ref(top, true);
             top = -CUDART_INF_F;
+            // a row's first keys are its first reference (both of its warps see that)
+            if (KIND == kMasks && __any_sync(0xffffffffu, live && m == -CUDART_INF_F && see.some(t0, t0 + kTile))) {
+#pragma unroll 1
+                for (int k0 = t0 + 32 * part; k0 < t0 + kTile; k0 += 64) {
+                    uint32_t u[32];
+                    ptx::tmem_ld32(tS + (k0 - t0), u);
+                    ptx::tmem_wait_ld(u);
+                    in_log2(k0, false, u);
+                    top = fmaxf(top, max_of(u) * scale);
+                }
+                if (ptx::bar_or(b_pair, 64, top > m + kLazyMax || (m == -CUDART_INF_F && top > m))) move_ref(top, it > 0);
+            }
             // The tile's keys in two halves, so that P V of the first runs while P of
             // the second is formed; a thread has 32 keys of each.
 #pragma unroll 1
@@ -574,20 +601,18 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const uint32_t tSh = tS + 64 * h + 32 * part;
                 const bool whole = __all_sync(0xffffffffu, see.all(k0, k0 + 32));
                 // nothing seen by either part (beyond the diagonal, other documents): weights
-                // of 0 whatever S holds
+                // of 0 whatever S holds (with the causal mask alone these are the diagonal's
+                // few, and the test costs every tile more than they save)
                 const bool any = !SCORED || __any_sync(0xffffffffu, live && see.some(half, half + 64));
                 uint32_t pw[16], pl[STATE ? 16 : 1];
                 float2 sum[2] = {};
                 if (any) {
                     uint32_t u[32];
                     ptx::tmem_ld32(tSh, u);
-                    const bool behind = SCORED && p.slopes && __all_sync(0xffffffffu, !live || pos >= k0 + 31);
                     ptx::tmem_wait_ld(u);
-                    if constexpr (SCORED)
-                        pages::scores32(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0, behind);
-                    if (!whole) mask(k0, u);
-                    const float x = max_of(u);
-                    if constexpr (SCORED) {
+                    in_log2(k0, whole, u);
+                    const float x = max_of(u) * scale;
+                    if constexpr (KIND == kScores) {
                         if (ptx::bar_or(b_pair, 64, x > m + kLazyMax || (m == -CUDART_INF_F && x > m))) {
                             if (h) {  // (S came after every P V but the first half's)
                                 warp_wait(b_o + 8 * w, it & 1, bad);
@@ -596,14 +621,13 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                             move_ref(x, it > 0 || h > 0);
                         }
                     } else {
-                        top = fmaxf(top, x * p.scale_log2);
+                        top = fmaxf(top, x);
                     }
                     const float ref = m == -CUDART_INF_F ? 0.0f : m;
-                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), nm = make_float2(-ref, -ref);
+                    const float2 sc = make_float2(scale, scale), nm = make_float2(-ref, -ref);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float2 y = make_float2(asf(u[2 * k]), asf(u[2 * k + 1]));
-                        const float2 d = SCORED ? __fadd2_rn(y, nm) : __ffma2_rn(y, sc, nm);
+                        const float2 d = __ffma2_rn(make_float2(asf(u[2 * k]), asf(u[2 * k + 1])), sc, nm);
                         const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
                         sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                         pw[k] = pack_bf2(e.x, e.y);
@@ -858,12 +882,12 @@ struct Fit {
     cudaError_t err = cudaSuccess;
     int clusters[4] = {};
 };
-template <int D, bool SCORED, bool STATE>
+template <int D, int KIND, bool STATE>
 const Fit& fit(int device) {
     static std::once_flag once[kPagedDevices];
     static Fit fits[kPagedDevices];
     std::call_once(once[device], [device] {
-        auto kern = pages_chunk_kernel<D, SCORED, STATE>;
+        auto kern = pages_chunk_kernel<D, KIND, STATE>;
         Fit& x = fits[device];
         x.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::total);
         for (int i = 0; i < 4 && x.err == cudaSuccess; ++i) {
@@ -884,13 +908,13 @@ const Fit& fit(int device) {
     return fits[device];
 }
 
-template <int D, bool SCORED, bool STATE>
+template <int D, int KIND, bool STATE>
 cudaError_t launch(const PagedAttend& a, int max_q, int max_kv, cudaStream_t st) {
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     if (device >= kPagedDevices) return cudaErrorInvalidDevice;
-    const Fit& f = fit<D, SCORED, STATE>(device);
+    const Fit& f = fit<D, KIND, STATE>(device);
     if (f.err != cudaSuccess) return f.err;
     const long long rows = (long long)a.s.tokens * a.G;
     const long long blocks = rows / kRows + a.s.seqs;  // at least as many as there are
@@ -930,19 +954,19 @@ cudaError_t launch(const PagedAttend& a, int max_q, int max_kv, cudaStream_t st)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, pages_chunk_kernel<D, SCORED, STATE>, kmap, vmap, a);
+    return cudaLaunchKernelEx(&cfg, pages_chunk_kernel<D, KIND, STATE>, kmap, vmap, a);
 }
 
 }  // namespace
 
 cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_q, int max_kv, cudaStream_t st) {
-    const bool scored = paged_scored(a);
-    if (a.st_acc != nullptr)
-        return head_dim == 64 ? launch<64, false, true>(a, max_q, max_kv, st)
-                              : launch<128, false, true>(a, max_q, max_kv, st);
-    if (head_dim == 64)
-        return scored ? launch<64, true, false>(a, max_q, max_kv, st) : launch<64, false, false>(a, max_q, max_kv, st);
-    return scored ? launch<128, true, false>(a, max_q, max_kv, st) : launch<128, false, false>(a, max_q, max_kv, st);
+    const int kind = a.cap2 > 0.0f || a.slopes ? kScores : paged_scored(a) ? kMasks : kPlain;
+#define KVP_PG_CHUNK(KK, SS) \
+    (head_dim == 64 ? launch<64, KK, SS>(a, max_q, max_kv, st) : launch<128, KK, SS>(a, max_q, max_kv, st))
+    if (a.st_acc) return KVP_PG_CHUNK(kPlain, true);
+    if (kind == kScores) return KVP_PG_CHUNK(kScores, false);
+    return kind == kMasks ? KVP_PG_CHUNK(kMasks, false) : KVP_PG_CHUNK(kPlain, false);
+#undef KVP_PG_CHUNK
 }
 
 }  // namespace kvp

@@ -101,6 +101,40 @@ def test_masked_keys_may_hold_anything(kp, T, chunk, score):
     check_attend(out, lse, ref, T)
 
 
+@pytest.mark.parametrize("room", [0, 1 << 16])  # (the kernel for few rows, that for many)
+@pytest.mark.parametrize("chunk,T", [(20, 900), (100, 900), (100, 2500)])
+@pytest.mark.parametrize("rise,jump", [(0.02, 0), (0.3, 0), (0.02, 300), (-0.3, 0)])
+@pytest.mark.parametrize("score", [dict(), dict(window=600)])
+def test_scores_that_rise(kp, rise, jump, score, chunk, T, room):
+    """Maxima that move on with every tile, by a little and by much, and one that
+    jumps by more than float32 weights have room for."""
+    b = Batch(1, 4, 64, 16, [chunk, 1], [T, 70], seed=22)
+    if room:
+        b.many(room)
+    u = np.zeros(64, np.float32)
+    u[:16] = 1
+    at = np.arange(T)
+    level = rise * at + jump * (at >= 2 * T // 3)
+    page, slot = paged.token_slots(b.table[0], 0, T, b.P)
+    K = b.K[0, page, 0, slot] * 0.1
+    K[:, :16] = (level / 2)[:, None]  # <u, k> / sqrt(64) = level
+    b.K[0, page, 0, slot] = bf16(K)
+    b.Q = bf16(b.Q * 0.1 * (u == 0) + u)
+    run(kp, b, **score)
+
+
+@pytest.mark.parametrize("room", [0, 1 << 16])
+@pytest.mark.parametrize("top", [0.004, 0.2, 2.0, -0.05])
+@pytest.mark.parametrize("score", [dict(), dict(cap=20.0), dict(prefix=True, window=90)])
+def test_slopes(kp, top, score, room):
+    """A bias by distance from flat to one that leaves the nearest keys alone, in
+    heads side by side."""
+    b = Batch(1, 4, 128, 32, [100, 20], [2100, 900], seed=23)
+    if room:
+        b.many(room)
+    run(kp, b, slopes=np.array([0.0, 0.3, 0.7, 1.0], np.float32) * np.float32(top), **scores(b, **score))
+
+
 @pytest.mark.parametrize("room", [0, 1 << 17])  # (the kernel for few rows, that for many)
 @pytest.mark.parametrize("chunk", [1, 20, 100])
 @pytest.mark.parametrize("T,window,prefix", [(1900, 150, 130), (5001, 1, 3), (6000, 1500, 700), (700, 500, 200)])
