@@ -229,6 +229,9 @@ int kvp::paged_attend_args(const kvpool_pages_t* pg, int layer, const kvpool_seq
         if (score->cap > 0.0f) {
             a.cap2 = score->cap * 1.4426950408889634f;
             a.cap_in = 2.0f * 1.4426950408889634f * scale / score->cap;
+            a.cap_z = scale / score->cap;
+            a.cap_near = 0.7f * score->cap / scale;
+            for (int i = 0; i < 5; ++i) a.cap_q[i] = kTanh[i] * a.scale_log2;
         }
         a.slopes = score->slopes;
         a.window = score->window;

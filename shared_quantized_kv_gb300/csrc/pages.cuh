@@ -37,6 +37,8 @@ struct PagedAttend {
     uint32_t g_magic;      // 2^32 / G, rounded up (see div_group)
     float scale_log2;      // softmax scale * log2(e)
     float cap2, cap_in;    // cap * log2(e); 2 * log2(e) * softmax scale / cap
+    float cap_z, cap_near; // softmax scale / cap; the products up to which tanh is a polynomial
+    float cap_q[5];        // its coefficients times scale_log2
     const float* slopes;
     int window;
     const int32_t* first;
@@ -51,6 +53,9 @@ struct PagedAttend {
     float* st_ml;
     int st_tokens;
 };
+
+// tanh(z) = z (1 + z^2 q(z^2)) for |z| <= 0.7 within 1.5e-8: q's coefficients.
+constexpr float kTanh[5] = {-0.333331913f, 0.13329111f, -0.05355886f, 0.0200919714f, -0.00513866264f};
 
 // Does any score modifier apply (else the causal mask alone, which the plain
 // instances of the kernels handle).
@@ -195,11 +200,14 @@ __device__ __forceinline__ float2* state_ml(const PagedAttend& a, int t, int hd)
            ((long long)g * in + tl) * a.G + (hd - g * a.G);
 }
 
-// <q, k> -> the score in log2 units, of one key and of 32. tanh(y) =
-// 1 - 2 / (e^(2y) + 1): off by a few units of 2^-24 whatever y, which the cap
-// turns into cap * 2^-22 of a score; the reciprocal of an overflowed e^(2y) is
-// 0, as it should be. (One loop per modifier: a choice per key costs more than
-// the modifiers do.)
+// <q, k> -> the score in log2 units, of one key and of 32. The cap's tanh(z):
+// up to |z| = 0.7 a polynomial, z + z^3 q(z^2), q fitted to tanh's least largest
+// relative error (1.4e-8), so that scores far below the cap keep float32's
+// relative precision; beyond, 1 - 2 / (e^(2z) + 1), off by a few units of 2^-24,
+// which the cap turns into cap * 2^-22 of a score that is at least 0.6 cap (the
+// reciprocal of an overflowed e^(2z) is 0, as it should be). 32 keys take the
+// polynomial where all of a warp's are near (no exponential and no reciprocal
+// per key), else the other form, whose error is the same part of the cap.
 __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -207,8 +215,15 @@ __device__ __forceinline__ float rcp(float x) {
 }
 template <bool SCORED>
 __device__ __forceinline__ float score(const PagedAttend& a, float s, float slope2, int pos, int j) {
-    if (!SCORED || !(a.cap2 > 0.0f)) s *= a.scale_log2;
-    else s = fmaf(-2.0f * a.cap2, rcp(ptx::ex2(s * a.cap_in) + 1.0f), a.cap2);
+    if (!SCORED || !(a.cap2 > 0.0f)) {
+        s *= a.scale_log2;
+    } else {
+        const float z = s * a.cap_z, u = z * z;
+        float q = fmaf(u, a.cap_q[4], a.cap_q[3]);
+        q = fmaf(u, q, a.cap_q[2]), q = fmaf(u, q, a.cap_q[1]), q = fmaf(u, q, a.cap_q[0]);
+        const float far = fmaf(-2.0f * a.cap2, rcp(ptx::ex2(s * a.cap_in) + 1.0f), a.cap2);
+        s = fabsf(s) <= a.cap_near ? s * fmaf(u, q, a.scale_log2) : far;
+    }
     if (SCORED && a.slopes) s = fmaf(-slope2, fabsf((float)(pos - j)), s);
     return s;
 }
@@ -217,11 +232,30 @@ __device__ __forceinline__ float score(const PagedAttend& a, float s, float slop
 __device__ __forceinline__ void scores32(const PagedAttend& a, float (&x)[32], float slope2, int pos, int j0,
                                          bool behind) {
     const float far = (float)(pos - j0), base = a.slopes && behind ? -slope2 * far : 0.0f;
+    auto near = [&] {  // (a NaN is passed over, and stays one in either form)
+        float most = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) most = ptx::max3(most, fabsf(x[k]), fabsf(x[k + 1]));
+        return __all_sync(0xffffffffu, most <= a.cap_near);
+    };
     if (!(a.cap2 > 0.0f)) {
         const float2 f = make_float2(a.scale_log2, a.scale_log2), c = make_float2(base, base);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float2 y = __ffma2_rn(make_float2(x[k], x[k + 1]), f, c);
+            x[k] = y.x, x[k + 1] = y.y;
+        }
+    } else if (near()) {
+        auto both = [](float v) { return make_float2(v, v); };
+        const float2 cz = both(a.cap_z), f = both(a.scale_log2), c = both(base);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const float2 s = make_float2(x[k], x[k + 1]), z = __fmul2_rn(s, cz), u = __fmul2_rn(z, z);
+            float2 q = __ffma2_rn(u, both(a.cap_q[4]), both(a.cap_q[3]));
+            q = __ffma2_rn(u, q, both(a.cap_q[2]));
+            q = __ffma2_rn(u, q, both(a.cap_q[1]));
+            q = __ffma2_rn(u, q, both(a.cap_q[0]));
+            const float2 y = __ffma2_rn(s, __ffma2_rn(u, q, f), c);
             x[k] = y.x, x[k + 1] = y.y;
         }
     } else {

@@ -54,7 +54,10 @@ constexpr int kTile = 128;              // keys per tile, rows per slot
 constexpr int kRows = 2 * kTile;        // rows per CTA
 constexpr int kFewTiles = 8;            // key tiles that a cluster does not split
 constexpr int kMaxParts = 16;           // states of a row: 8 CTAs, 2 slots
-constexpr float kLazyMax = 8.0f;        // log2 units the reference may trail the maximum
+// log2 units the reference may trail the maximum: by little where the next tile
+// may add to it before it is looked at again, else by what a float32 sum has room
+// for (with a bias by distance it moves often)
+constexpr float kLazyMax = 8.0f, kLazyScores = 60.0f;
 constexpr uint32_t kTryNs = 1000, kTries = 1u << 18;
 constexpr uint32_t kCols = 512;         // tensor memory: S0, S1, O0, O1
 // named barriers: Q is staged (issuers and softmax warps); every role is done; the merge rows are written;
@@ -120,8 +123,8 @@ __device__ __forceinline__ uint32_t span_bits(int a, int b, int c) {
 }
 
 // KIND: the causal mask alone; other masks too; scores that a cap or a bias by
-// distance changes (the two costs are apart: 2,432 tokens over 16K keys take
-// 342 us, 434 and 850).
+// distance changes (their costs are apart: 2,432 tokens over 16K keys take
+// 342 us, 433 with a window, 830 with a cap, 650 with a bias and 865 with both).
 enum { kPlain, kMasks, kScores };
 // STATE: the rows' states for a merge instead of the output; the weights then
 // go through the product with V as bf16 hi and lo (16 bits; lo in the half of
@@ -132,6 +135,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                    const PagedAttend p) {
     using L = Lay<D>;
     constexpr bool SCORED = KIND != kPlain;
+    constexpr float kLazy = KIND == kScores ? kLazyScores : kLazyMax;
     constexpr uint32_t kColS = 0, kColO = 256;  // slot w: 128 w columns on
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(
@@ -241,8 +245,12 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int per = (t_hi - t_lo + S - 1) / S;
     const int ta = t_lo + rank * per;
     const int n = max(0, min(t_hi, ta + per) - ta);
+    // Modified scores take the tiles from the last to the first: with a bias by
+    // distance the first then holds the maxima, and the reference hardly moves.
+    auto tile_at = [&](int i) { return gap.number(KIND == kScores ? ta + n - 1 - i : ta + i); };
     auto tiles_of = [&](int slot) {
         if (!two) return (n - slot + 1) / 2;
+        if (KIND == kScores) return n;  // (of the tiles that the other slot alone sees, the halves are passed over)
         return max(0, min(n, gap.count((seen_end(slot) + kTile - 1) / kTile) - ta));
     };
     if (rank >= S) {  // not a split block's: nothing to do, and nobody waits for this CTA
@@ -262,7 +270,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const int none = s.pages * (s.Hk << s.pshift);  // a row behind the last: reads as zeros
             // first token row of this lane's page of tile i, -1 for none
             auto page_row = [&](int i) {
-                const int t = gap.number(ta + i) * kTile + lane * P;
+                const int t = tile_at(i) * kTile + lane * P;
                 if (i >= n || lane >= np || t >= T) return -1;
                 const int page = __ldg(table + (t >> s.pshift));
                 if (page < 0 || page >= s.pages) {
@@ -502,7 +510,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         // it; O, which no MMA works on, follows
         auto move_ref = [&](float mine_max, bool summed) {
             const float mt = joined(mine_max, false);
-            const bool move = mt > m + kLazyMax || (m == -CUDART_INF_F && mt > m);
+            const bool move = mt > m + kLazy || (m == -CUDART_INF_F && mt > m);
             if (summed) {
                 const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
                 l *= al;
@@ -548,12 +556,12 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         };
         for (int it = 0; it < mine; ++it) {
             const int i = two ? it : 2 * it + w;  // tile of this CTA
-            const int t0 = gap.number(ta + i) * kTile;
+            const int t0 = tile_at(i) * kTile;
             // A maximum that passes the reference by 2^8 moves it: where scores cost much
             // to form or may rise fast (kScores) at once, else before the next tile (until then the weights are that much larger, which they may be by 2^118;
             // rows beyond it come out infinite and are done again). The two threads of a
             // row ask one another while S is on its way.
-            const bool moves = KIND != kScores && it > 0 && some && ptx::bar_or(b_pair, 64, top > m + kLazyMax);
+            const bool moves = KIND != kScores && it > 0 && some && ptx::bar_or(b_pair, 64, top > m + kLazy);
             warp_wait(b_s + 8 * w, it & 1, bad);
             ptx::tc_fence_after();
             // keys behind the sequence's end: whatever their V holds becomes 0 (a
@@ -591,7 +599,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     in_log2(k0, false, u);
                     top = fmaxf(top, max_of(u) * scale);
                 }
-                if (ptx::bar_or(b_pair, 64, top > m + kLazyMax || (m == -CUDART_INF_F && top > m))) move_ref(top, it > 0);
+                if (ptx::bar_or(b_pair, 64, top > m + kLazy || (m == -CUDART_INF_F && top > m))) move_ref(top, it > 0);
             }
             // The tile's keys in two halves, so that P V of the first runs while P of
             // the second is formed; a thread has 32 keys of each.
@@ -613,7 +621,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     in_log2(k0, whole, u);
                     const float x = max_of(u) * scale;
                     if constexpr (KIND == kScores) {
-                        if (ptx::bar_or(b_pair, 64, x > m + kLazyMax || (m == -CUDART_INF_F && x > m))) {
+                        if (ptx::bar_or(b_pair, 64, x > m + kLazy || (m == -CUDART_INF_F && x > m))) {
                             if (h) {  // (S came after every P V but the first half's)
                                 warp_wait(b_o + 8 * w, it & 1, bad);
                                 ptx::tc_fence_after();
@@ -664,7 +672,8 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             se.b2 = __shfl_sync(0xffffffffu, see.b2, of);
             pages::careful_row<D, SCORED>(p, b.seq, __shfl_sync(0xffffffffu, tok, of),
                                           __shfl_sync(0xffffffffu, head, of), __shfl_sync(0xffffffffu, pos, of), se,
-                                          gap, 7, two || all ? ta : ta + w, ta + n, two || all ? 1 : 2, cm, cl, acc);
+                                          gap, 7, two || all ? ta : ta + (KIND == kScores ? (n - 1 - w) & 1 : w), ta + n,
+                                          two || all ? 1 : 2, cm, cl, acc);
         };
         l = joined(l, true);
         bool odd = live && l != 0.0f && !finite(l);  // sums that a masked key may have spoilt
