@@ -482,7 +482,7 @@ typedef struct {
  * see may hold anything, infinities and NaN included. Zeroed: the causal mask
  * alone. */
 typedef struct {
-    float cap;             /* >= 0; 0: none */
+    float cap;             /* >= 0; 0: none; 3 softmax_scale / cap has to be finite */
     int window;            /* >= 0; 0: none; else the last `window` keys, the row's own among them */
     const float* slopes;   /* device float [q_heads], or NULL */
     const int32_t* first;  /* device int32 [tokens], or NULL */

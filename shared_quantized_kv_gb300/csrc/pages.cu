@@ -225,11 +225,13 @@ int kvp::paged_attend_args(const kvpool_pages_t* pg, int layer, const kvpool_seq
     a.g_magic = (uint32_t)(((1ull << 32) + group - 1) / group);
     const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf((float)pg->head_dim);
     a.scale_log2 = scale * 1.4426950408889634f;
+    if (isinf(a.scale_log2)) return KVPOOL_ERR_INVALID_ARG;
     if (score) {
         if (score->cap > 0.0f) {
             a.cap2 = score->cap * 1.4426950408889634f;
             a.cap_in = 2.0f * 1.4426950408889634f * scale / score->cap;
             a.cap_z = scale / score->cap;
+            if (isinf(a.cap_in)) return KVPOOL_ERR_INVALID_ARG;  // (0 times it would be NaN)
             a.cap_near = 0.7f * score->cap / scale;
             for (int i = 0; i < 5; ++i) a.cap_q[i] = kTanh[i] * a.scale_log2;
         }
@@ -249,9 +251,9 @@ cudaError_t kvp::launch_pages_attend(const PagedAttend& a, int head_dim, int max
     // The kernel for few rows takes 16 at a time, each block of 16 through all
     // its keys: one block per sequence always; more of them while the keys read
     // over and over (from L2) stay below 128 MiB. On one sequence of 1,024 keys
-    // and 128 rows per KV head it takes 14 us against 21 of the kernel for many
-    // rows, of 16K keys and 32 rows 31 against 33; on 16K keys and 128 rows 72
-    // against 39, on 16 sequences of 1,024 keys and 32 rows 35 against 25.
+    // and 128 rows per KV head it takes 14 us against 22 of the kernel for many
+    // rows, of 16K keys and 32 rows 31 against 33; on 16K keys and 128 rows 59
+    // against 39, on 16 sequences of 1,024 keys and 32 rows 29 against 27.
     const double blocks = (double)a.s.seqs * (((long long)max_q * a.G + 15) / 16);
     const double reads = blocks * a.s.Hk * max_kv * head_dim * 4;
     if ((long long)max_q * a.G <= 16 || reads < (double)(1 << 27))

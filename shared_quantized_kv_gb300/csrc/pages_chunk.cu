@@ -3,15 +3,15 @@
 //
 // Mathematics as in pages_rows.cu: one pass over the keys, a running reference
 // maximum that moves when the maximum passes it by more than 2^8, p = 2^(x - m)
-// rounded to bf16 for the product with V (2^-9 of each weight on average less,
-// against the output's own rounding to bf16), l = sum p in float32.
+// rounded to bf16 for the product with V (off by at most 2^-8 of each weight, as
+// the output's own rounding is of it), l = sum p in float32.
 //
 // Bound: the tensor cores, 4 D FLOP per (row, key). A CTA has up to 256 rows
 // (new tokens x heads of a group) of one sequence and KV head, as two tiles of
 // 128, and walks the keys in tiles of 128. Two slots of tensor memory, each
 // with S (128 columns; P, its bf16 weights, overwrites it) and O (D columns),
 // are worked on in turn: while the tensor cores do P V and the next Q K^T of
-// one slot, the four softmax warps of the other turn its S into P. With more
+// one slot, the eight softmax warps of the other turn its S into P. With more
 // than 128 rows the slots are the two row tiles, and each K and V tile serves
 // both; with fewer, both slots have the same rows and take every second key
 // tile, and their states are merged at the end.
@@ -24,7 +24,7 @@
 // order they are issued. V comes as [key][channel], which the MMA takes as an
 // MN-major operand. The keys may be split over the CTAs of a cluster, whose
 // states meet in distributed shared memory: no workspace, no second launch.
-// Every wait is bounded; one that expires is recorded in the status word, and
+// Every wait on a barrier in memory is bounded; one that expires is recorded in the status word, and
 // the CTA runs to its end without waiting again.
 //
 // Measured on 2,432 new tokens over 16K keys, 32 query heads on 8 KV heads of
@@ -232,9 +232,9 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         return max(0, min(T, T - b.n + i_begin + pages::div_group(p, j_begin + last) + 1));
     };
     // this CTA's key tiles [ta, ta + n), counted without the gap: the cluster's
-    // share of the tiles that any row sees; slot w takes the first nt[w] of them (two row tiles), or
-    // every second one. Few tiles are not split: the cluster's first CTA takes
-    // them all, as a merge costs about what kFewTiles cost.
+    // share of the tiles that any row sees; a slot takes those that its rows see
+    // (two row tiles), or every second one. Few tiles are not split: the cluster's
+    // first CTA takes them all, as a merge costs about what kFewTiles cost.
     const int hi = max(seen_end(0), seen_end(1));
     int t_lo = 0;
     if constexpr (SCORED) t_lo = hi > 0 ? min(rng[0], rng[2]) / kTile : 0;
@@ -311,8 +311,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
             ptx::bar_sync(kBarLoad, 64);
             // every requested tile has landed before the CTA may go on
-            for (int e = max(0, 2 * n - L::nst); e < 2 * n; ++e)
-            {
+            for (int e = max(0, 2 * n - L::nst); e < 2 * n; ++e) {
                 bool late = false;
                 warp_wait(b_full + 8 * (e % L::nst), (e / L::nst) & 1, late);
             }
@@ -321,7 +320,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             // One warp per slot: what one of them waits for costs the other's MMAs
             // nothing (a single issuer's waits and commits, about 1000 cycles per tile,
             // left the tensor cores idle). The whole warp runs this with uniform
-            // values; lane 0 issues.
+            // values; an elected lane issues.
             ptx::bar_sync(kBarQ, 64 + kSoftmax);  // Q is in shared memory
             auto uniform = [](auto x) { return __reduce_max_sync(0xffffffffu, x); };
             const int slot = uniform(warp - 1), nn = uniform(n), nt = uniform(tiles_of(slot));
@@ -938,9 +937,9 @@ cudaError_t launch(const PagedAttend& a, int max_q, int max_kv, cudaStream_t st)
     for (int i = 0; i < 4 && f.clusters[i] > 0; ++i) {
         const int S = 1 << i;
         if (S > 1 && ntiles <= kFewTiles) break;
-        // the time of the GPU's slots in key tiles: waves x (tiles of a CTA, and
-        // about five for its start and end, ten with a merge over the cluster:
-        // 2.8, 7 and 14 thousand cycles)
+        // the time of the GPU's slots in key tiles (2.5 thousand cycles): waves x
+        // (tiles of a CTA, and about five for its start and end, ten with a merge
+        // over the cluster; seven and fourteen choose the same)
         const long long tiles = (ntiles + S - 1) / S;
         const long long cost =
             (std::max(1LL, jobs) + f.clusters[i] - 1) / f.clusters[i] * ((one ? (tiles + 1) / 2 : tiles) + (S > 1 ? 10 : 5));

@@ -82,7 +82,7 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < CUDART_INF_F
 // SCORED: score modifiers apply. STATE: the rows' states for a merge instead
 // of the output; the weights then go through the matrix product as bf16 hi and
 // lo (16 bits), as the merged output is fp32. Otherwise they are rounded to
-// bf16 once (2^-9 of each, against the output's own rounding of 2^-9).
+// bf16 once (off by at most 2^-8 of each, as the output's own rounding is of it).
 // DIRECT: every sequence has one block (no search; if it has more, the CTA
 // takes them in turn). Grid: blocks x the CTAs of a cluster, KV heads.
 template <int D, bool SCORED, bool STATE, bool DIRECT>

@@ -124,6 +124,17 @@ def test_scores_that_rise(kp, rise, jump, score, chunk, T, room):
 
 
 @pytest.mark.parametrize("room", [0, 1 << 16])
+@pytest.mark.parametrize("cap", [1e-30, 0.01, 1.0, 3.0, 1e6, 1e30])
+def test_caps(kp, cap, room):
+    """Caps that leave every score at the cap, between, and untouched; a zero row of Q."""
+    b = Batch(1, 4, 64, 32, [100, 20], [1300, 900], seed=24)
+    b.Q[5] = 0
+    if room:
+        b.many(room)
+    run(kp, b, cap=cap)
+
+
+@pytest.mark.parametrize("room", [0, 1 << 16])
 @pytest.mark.parametrize("top", [0.004, 0.2, 2.0, -0.05])
 @pytest.mark.parametrize("score", [dict(), dict(cap=20.0), dict(prefix=True, window=90)])
 def test_slopes(kp, top, score, room):

@@ -218,6 +218,14 @@ def test_attend_refusals(kp):
     assert kp.lib().kvpool_pages_status(by(pages(kp)), None) == INVALID
 
 
+def test_scales_past_float32_are_refused(kp):
+    f = kp.lib().kvpool_pages_attend
+    by = ctypes.byref
+    for cap, scale in ((0.0, 3e38), (1e-40, 0.0), (1e-38, 10.0), (5.0, 2.9e38)):
+        sc = kp.Score(cap=cap)
+        assert f(by(pages(kp)), 0, by(seqs(kp)), A, 256, 4, by(sc), A, None, scale, None) == INVALID, (cap, scale)
+
+
 def test_oracle_attend_is_a_softmax_over_what_is_seen():
     """The restatement itself, against a row written out by hand."""
     r = np.random.default_rng(0)
