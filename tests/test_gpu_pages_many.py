@@ -131,7 +131,13 @@ def test_caps(kp, cap, room):
     b.Q[5] = 0
     if room:
         b.many(room)
-    run(kp, b, cap=cap)
+    if cap < 1e6:
+        run(kp, b, cap=cap)
+        return
+    # tanh(z) is z within z^3 / 3, 1e-10 of a score here: the bound of plain scores holds
+    K, V, layer, Q, table, kv_len, q_start = b.dev()
+    out, lse = kp.pages_attend(K, V, layer, Q, table, kv_len, q_start, cap=cap, return_lse=True)
+    check_attend(out.float().cpu().numpy(), lse.cpu().numpy(), b.ref(), 1300)
 
 
 @pytest.mark.parametrize("room", [0, 1 << 16])
