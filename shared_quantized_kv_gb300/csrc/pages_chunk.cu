@@ -28,7 +28,7 @@
 // the CTA runs to its end without waiting again.
 //
 // Measured on 2,432 new tokens over 16K keys, 32 query heads on 8 KV heads of
-// 128 (two full waves of CTAs): 341 us, 1770 TFLOP/s. What got it there: one
+// 128 (two full waves of CTAs): 343 us, 1750 TFLOP/s. What got it there: one
 // issuer per slot, taking turns (a single one's waits and commits left the
 // tensor cores idle: 466 us; two without turns fell into step: 592 us);
 // operands of the MMAs in uniform registers (509 us before; not all of them
@@ -37,7 +37,7 @@
 // reference as it is, the maxima looked at after it, and handed over in halves;
 // hardly a register spilled (the roles' registers shifted between the
 // warpgroups). Pages of 16 tokens are 32 boxes per pair of tiles: one loader
-// issues them in 1.4 times as long as the rest takes (470 us against 341 on
+// issues them in 1.4 times as long as the rest takes (470 us against 340 on
 // 2,048 tokens over 16K), two keep up.
 #include <algorithm>
 #include <mutex>
@@ -124,7 +124,7 @@ __device__ __forceinline__ uint32_t span_bits(int a, int b, int c) {
 
 // KIND: the causal mask alone; other masks too; scores that a cap or a bias by
 // distance changes (their costs are apart: 2,432 tokens over 16K keys take
-// 342 us, 433 with a window, 830 with a cap, 650 with a bias and 865 with both).
+// 343 us, 418 with a window, 790 with a cap, 605 with a bias and 826 with both).
 enum { kPlain, kMasks, kScores };
 // STATE: the rows' states for a merge instead of the output; the weights then
 // go through the product with V as bf16 hi and lo (16 bits; lo in the half of
@@ -147,6 +147,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     uint32_t* tslot = reinterpret_cast<uint32_t*>(rng + 4);
     int* gapped = rng + 5;                              // end of the prefixes, begin of the windows seen
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tslot), kCols);  // beside the search
+    if (tid == 0 || tid == 96) ptx::prefetch_map(tid ? &vmap : &kmap);
     // blocks of a sequence from its last (the one that sees most) to its first
     const int job = blockIdx.x / CS, g = job % s.Hk;
     pages::RowBlock b;
@@ -200,6 +201,22 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         head = g * p.G + j_begin + row - i * p.G;
         pos = T - b.n + i_begin + i;
         see = pages::row_seen<SCORED>(p, b.seq, tok, pos, T);
+    }
+    // Q on its way to registers: 16-byte pieces, consecutive lanes on consecutive
+    // pieces of a row, all of a thread's under way before the first is stored
+    // (rows past the block repeat its last: a load under a condition waits for the
+    // one before it, 16 thousand cycles in all instead of 4)
+    constexpr int CH = D / 8;
+    uint4 v[CH / 2];
+    if (warp >= 4 && (two || w == 0)) {
+        const int first = two ? w * kTile : 0;
+#pragma unroll
+        for (int k = 0; k < CH / 2; ++k) {
+            const int x = k * 256 + (tid & 255), r = min(first + x / CH, nr - 1), c = x % CH;
+            const int i = pages::div_group(p, j_begin + r);
+            v[k] = ptx::ldg16(p.Q + (long long)(b.q0 + i_begin + i) * p.q_stride +
+                              (long long)(g * p.G + j_begin + r - i * p.G) * D + c * 8);
+        }
     }
     if constexpr (SCORED) {
         if (warp >= 4) {
@@ -451,21 +468,8 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         // ------------------------------------------------------------ softmax
         if (two || w == 0) {
-            // 16-byte pieces, consecutive lanes on consecutive pieces of a row, all
-            // of a thread's under way before the first is stored (rows past the
-            // block repeat its last: a load under a condition waits for the one
-            // before it, 16 thousand cycles in all instead of 4)
-            constexpr int CH = D / 8;
             unsigned char* dst = sm + w * L::stage;
-            const int first = two ? w * kTile : 0, at = tid & 255;
-            uint4 v[CH / 2];
-#pragma unroll
-            for (int k = 0; k < CH / 2; ++k) {
-                const int x = k * 256 + at, r = min(first + x / CH, nr - 1), c = x % CH;
-                const int i = pages::div_group(p, j_begin + r);
-                v[k] = ptx::ldg16(p.Q + (long long)(b.q0 + i_begin + i) * p.q_stride +
-                                  (long long)(g * p.G + j_begin + r - i * p.G) * D + c * 8);
-            }
+            const int at = tid & 255;
 #pragma unroll
             for (int k = 0; k < CH / 2; ++k) {
                 const int x = k * 256 + at, r = x / CH, c = x % CH;
@@ -722,7 +726,6 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             // The slot's Q (no MMA reads it any more) takes the output as bf16, and the
             // two warps write whole rows of it, 16 each.
             const float inv = STATE ? 1.0f : 1.0f / l;  // (not used where l is 0)
-            constexpr int CH = D / 8;
             unsigned char* stage = sm + w * L::stage + (warp & 3) * 32 * (D * 2);
 #pragma unroll 1
             for (int c = c0; c < c0 + HC; c += 32) {

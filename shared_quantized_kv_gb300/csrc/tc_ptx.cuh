@@ -72,6 +72,10 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
+// The descriptor of later copies, asked for ahead of the first.
+__device__ __forceinline__ void prefetch_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
                  ::"l"(map), "r"(x), "r"(y) : "memory");
