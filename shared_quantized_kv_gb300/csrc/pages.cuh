@@ -228,15 +228,16 @@ __device__ __forceinline__ float score(const PagedAttend& a, float s, float slop
     return s;
 }
 // The scores of 32 keys. behind: no key lies behind the row's position, so the
-// distance to key j0 joins the constant and each key costs one more step.
+// distance to key j0 joins the constant and each key costs one more step. live:
+// the row is one (which form a warp's tanh takes is for its rows to say).
 __device__ __forceinline__ void scores32(const PagedAttend& a, float (&x)[32], float slope2, int pos, int j0,
-                                         bool behind) {
+                                         bool behind, bool live) {
     const float far = (float)(pos - j0), base = a.slopes && behind ? -slope2 * far : 0.0f;
     auto near = [&] {  // (a NaN is passed over, and stays one in either form)
         float most = 0.0f;
 #pragma unroll
         for (int k = 0; k < 32; k += 2) most = ptx::max3(most, fabsf(x[k]), fabsf(x[k + 1]));
-        return __all_sync(0xffffffffu, most <= a.cap_near);
+        return __all_sync(0xffffffffu, !live || most <= a.cap_near);
     };
     if (!(a.cap2 > 0.0f)) {
         const float2 f = make_float2(a.scale_log2, a.scale_log2), c = make_float2(base, base);

@@ -124,7 +124,7 @@ __device__ __forceinline__ uint32_t span_bits(int a, int b, int c) {
 
 // KIND: the causal mask alone; other masks too; scores that a cap or a bias by
 // distance changes (their costs are apart: 2,432 tokens over 16K keys take
-// 343 us, 418 with a window, 790 with a cap, 605 with a bias and 826 with both).
+// 343 us, 417 with a window, 795 with a cap, 618 with a bias and 830 with both).
 enum { kPlain, kMasks, kScores };
 // STATE: the rows' states for a merge instead of the output; the weights then
 // go through the product with V as bf16 hi and lo (16 bits; lo in the half of
@@ -492,13 +492,13 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             ptx::bar_sync(b_pair, 64);
             return part ? x : *xch;
         };
-        // keys of the part's 32 that the row does not see, in tile half k0: -inf
-        auto mask = [&](int k0, uint32_t (&u)[32]) {
+        // keys of the part's 32 from k0 on that the row does not see: `unseen`
+        auto mask = [&](int k0, uint32_t (&u)[32], float unseen) {
             uint32_t bits = span_bits(see.a1 - k0, see.b1 - k0, 0);
             if constexpr (SCORED) bits |= span_bits(see.a2 - k0, see.b2 - k0, 0);
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-                if (!(bits >> k & 1u)) u[k] = asu(-CUDART_INF_F);
+                if (!(bits >> k & 1u)) u[k] = asu(unseen);
         };
         auto max_of = [&](const uint32_t (&u)[32]) {
             auto f = [&](int k) { return asf(u[k]); };
@@ -541,7 +541,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 uint32_t u[32];
                 ptx::tmem_ld32(tS + c, u);
                 ptx::tmem_wait_ld(u);
-                mask(t0 + c, u);
+                mask(t0 + c, u, -CUDART_INF_F);
                 m = fmaxf(m, max_of(u));
             }
             m *= p.scale_log2;
@@ -553,9 +553,11 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         auto in_log2 = [&](int k0, bool whole, uint32_t (&u)[32]) {
             if constexpr (KIND == kScores) {
                 const bool behind = p.slopes && __all_sync(0xffffffffu, !live || pos >= k0 + 31);
-                pages::scores32(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0, behind);
+                // (what an unseen place holds has no say in the form that a cap takes)
+                if (!whole && p.cap2 > 0.0f) mask(k0, u, 0.0f);
+                pages::scores32(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0, behind, live);
             }
-            if (!whole) mask(k0, u);
+            if (!whole) mask(k0, u, -CUDART_INF_F);
         };
         for (int it = 0; it < mine; ++it) {
             const int i = two ? it : 2 * it + w;  // tile of this CTA

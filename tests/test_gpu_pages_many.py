@@ -288,6 +288,25 @@ def test_two_streams_at_once(kp):
             assert torch.equal(o, g[0][0]) and torch.equal(z, g[0][1])
 
 
+@pytest.mark.parametrize("score", [dict(), dict(window=50), dict(cap=8.0), dict(cap=30.0, slopes=True, window=40)])
+def test_same_bits_whatever_lay_in_shared_memory(kp, score):
+    """Short sequences leave most of a tile to what an earlier call left there."""
+    import torch
+
+    q = [1, 3, 40, 130, 1, 2, 77, 20, 5, 1]
+    b = Batch(2, 8, 128, 16, q, [n + 3 * i for i, n in enumerate(q)], seed=25).many()
+    K, V, layer, Q, table, kv_len, q_start = b.dev()
+    dev = {k: torch.from_numpy(v).cuda() if isinstance(v, np.ndarray) else v for k, v in scores(b, **score).items()}
+    other = Batch(2, 8, 128, 16, [300, 200], [1300, 900], seed=26).many()
+    runs = []
+    for scale in (0.01, 1.0, 100.0, -100.0):
+        Ko, Vo, lo, Qo, to, ko, qo = other.dev()
+        kp.pages_attend(Ko * scale, Vo * scale, lo, Qo, to, ko, qo)
+        runs.append(kp.pages_attend(K, V, layer, Q, table, kv_len, q_start, return_lse=True, **dev))
+    for o, z in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(z, runs[0][1])
+
+
 @pytest.mark.parametrize("hk,hq", [(1, 4), (1, 2)])
 def test_captured_graph(kp, hk, hq):
     """The first call in a capture; lengths change between replays."""
