@@ -515,15 +515,17 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const float mt = joined(mine_max, false);
             const bool move = mt > m + kLazy || (m == -CUDART_INF_F && mt > m);
             if (summed) {
-                const float al = move && m != -CUDART_INF_F ? ptx::ex2(m - mt) : 1.0f;
-                l *= al;
+                // (in two steps: a maximum may have passed the reference by up to 2^128, and
+                // ex2 gives 0 below 2^-126)
+                const float al = move && m != -CUDART_INF_F ? ptx::ex2(0.5f * (m - mt)) : 1.0f;
+                l = l * al * al;
 #pragma unroll 1
                 for (int c = 0; c < D / 2; c += 32) {
                     uint32_t o[32];
                     ptx::tmem_ld32(tO + part * (D / 2) + c, o);
                     ptx::tmem_wait_ld(o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = asu(asf(o[k]) * al);
+                    for (int k = 0; k < 32; ++k) o[k] = asu(asf(o[k]) * al * al);
                     ptx::tmem_st32x(tO + part * (D / 2) + c, o);
                 }
                 ptx::tmem_wait_st();
@@ -563,9 +565,10 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const int i = two ? it : 2 * it + w;  // tile of this CTA
             const int t0 = tile_at(i) * kTile;
             // A maximum that passes the reference by 2^8 moves it: where scores cost much
-            // to form or may rise fast (kScores) at once, else before the next tile (until then the weights are that much larger, which they may be by 2^118;
-            // rows beyond it come out infinite and are done again). The two threads of a
-            // row ask one another while S is on its way.
+            // to form or may rise fast (kScores) at once, else before the next tile (until
+            // then the weights are that much larger, which float32 has room for up to 2^128;
+            // rows beyond it come out infinite and are done again). The two threads of a row
+            // ask one another while S is on its way.
             const bool moves = KIND != kScores && it > 0 && some && ptx::bar_or(b_pair, 64, top > m + kLazy);
             warp_wait(b_s + 8 * w, it & 1, bad);
             ptx::tc_fence_after();
@@ -683,6 +686,14 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         l = joined(l, true);
         bool odd = live && l != 0.0f && !finite(l);  // sums that a masked key may have spoilt
         uint32_t* flags = reinterpret_cast<uint32_t*>(sm + L::pair + 2 * kTile * 4) + 4 * w + (warp & 3);
+        // A state that another is merged with has its l within 2^-32 ... 2^64 of its m:
+        // a last tile's maxima may lie far above the reference, up to where the other
+        // state's weight of it (ex2 of the references' difference, 0 below 2^-126) would
+        // lose the larger part of a row.
+        const bool high = l > 0x1p32f;
+        const float down = high ? 0x1p-64f : 1.0f;
+        const float state_m =
+            l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m) + (high ? 64.0f : 0.0f);
         // a row's last numbers: m and l, or their logarithm
         auto finish = [&](int t, int hd, float rm, float rl) {
             if constexpr (STATE)
@@ -727,7 +738,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         if (direct) {
             // The slot's Q (no MMA reads it any more) takes the output as bf16, and the
             // two warps write whole rows of it, 16 each.
-            const float inv = STATE ? 1.0f : 1.0f / l;  // (not used where l is 0)
+            const float inv = STATE ? down : 1.0f / l;  // (not used where l is 0)
             unsigned char* stage = sm + w * L::stage + (warp & 3) * 32 * (D * 2);
 #pragma unroll 1
             for (int c = c0; c < c0 + HC; c += 32) {
@@ -750,7 +761,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                                        pack_bf2(y[k + 4], y[k + 5]), pack_bf2(y[k + 6], y[k + 7]));
                 }
             }
-            if (live && !part) finish(tok, head, l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m), l);
+            if (live && !part) finish(tok, head, state_m, l * down);
             const unsigned odds = __ballot_sync(0xffffffffu, odd);
             if (part && lane == 0) *flags = odds;
             ptx::bar_sync(b_pair, 64);
@@ -780,12 +791,13 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 for (int k = 0; k < 32; k += 4) {
                     const float4 v = make_float4(asf(o[k]), asf(o[k + 1]), asf(o[k + 2]), asf(o[k + 3]));
                     odd = odd || (live && l != 0.0f && !(finite(v.x) && finite(v.y) && finite(v.z) && finite(v.w)));
-                    *reinterpret_cast<float4*>(dst + c + k) = v;
+                    *reinterpret_cast<float4*>(dst + c + k) =
+                        make_float4(v.x * down, v.y * down, v.z * down, v.w * down);
                 }
             }
             if (!part) {
-                dst[D] = l == 0.0f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.0f : m);
-                dst[D + 1] = l;
+                dst[D] = state_m;
+                dst[D + 1] = l * down;
             }
             const unsigned mine_odd = __ballot_sync(0xffffffffu, odd);
             if (part && lane == 0) *flags = mine_odd;
