@@ -547,6 +547,8 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 m = fmaxf(m, max_of(u));
             }
             m *= p.scale_log2;
+            // products of minus infinity alone are no reference: such a row is done again
+            if (live && m == -CUDART_INF_F && see.some(t0, t0 + 64)) l = CUDART_NAN_F;
             ptx::bar_sync(b_pair, 64);  // P of either part overwrites what both have read
         }
         float top = -CUDART_INF_F;  // the part's maximum in the tile before

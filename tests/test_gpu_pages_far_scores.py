@@ -8,7 +8,7 @@ import pytest
 from oracle import attention, codec, paged
 from shared_quantized_kv_gb300 import workloads as wl
 
-from paged_util import Batch, bf16
+from paged_util import Batch, bf16, check_attend
 from parity_util import TOL, to_dev
 from test_gpu_attend_pages import OneCache, reference
 from test_gpu_pages import kp, run  # noqa: F401 (kp: a fixture)
@@ -74,3 +74,27 @@ def test_states_that_lag_join_the_pool(kp, chunk, T, jump):
     err = attention.row_rel_error(got.astype(np.float64), reference(enc, b.Q, b.K, b.V, 0, b.table, b.kv_len, b.q_start))
     assert err <= TOL, err
     pool.close()
+
+
+@pytest.mark.parametrize("chunk,T", [(20, 900), (100, 900), (100, 2500)])
+@pytest.mark.parametrize("level", [0.0, 40.0, -100.0])
+@pytest.mark.parametrize("low", [64, 100, 460])
+@pytest.mark.parametrize("score", [dict(), dict(window=2400), dict(slopes=np.array([0, 0.001, 0.002, 0.003], np.float32))])
+@pytest.mark.parametrize("own", [False, True])  # (the chunk's own tokens too lie at the level, or at 0)
+def test_first_keys_of_the_lowest_value(kp, chunk, T, level, low, score, own):
+    """Keys whose products overflow to minus infinity weigh nothing, wherever the
+    row's other scores lie: as if they were not seen."""
+    import torch
+
+    b = standing_out(chunk, T, {t: level for t in range(T - chunk)})
+    page, slot = paged.token_slots(b.table[0], 0, low, b.P)
+    b.K[0, page, 0, slot, :16] = bf16(np.float32(-3e38))
+    if own:
+        page, slot = paged.token_slots(b.table[0], T - chunk, chunk, b.P)
+        b.K[0, page, 0, slot, :16] = level / 2
+    K, V, layer, Q, table, kv_len, q_start = b.dev()
+    dev = {k: torch.from_numpy(v).cuda() if isinstance(v, np.ndarray) else v for k, v in score.items()}
+    out, lse = kp.pages_attend(K, V, layer, Q, table, kv_len, q_start, return_lse=True, **dev)
+    first = np.full(b.tokens, low, np.int32)
+    first[b.q_start[1]:] = 0
+    check_attend(out.float().cpu().numpy(), lse.cpu().numpy(), b.ref(first=first, **score), T)
