@@ -424,7 +424,8 @@ merge_rows_kernel(const float* __restrict__ part_acc, const float* __restrict__ 
             mt = mnew;
         }
     }
-    const float Mf = fmaxf(M, mt);
+    // (a tail of nothing has no say, whatever its m holds; one whose sum is NaN has)
+    const float Mf = lt == 0.f ? M : fmaxf(M, mt);
     const float wp = (L > 0.f) ? exp2f(M - Mf) : 0.f;
     const float wt = (lt > 0.f) ? exp2f(mt - Mf) : 0.f;
     const float den = L * wp + lt * wt;
