@@ -47,3 +47,80 @@ def test_rows_of_no_sequence_and_a_pool_far_below_0(kp, d, level):
     assert pool.status() == 0
     close(got, reference(encs[0], b.Q, b.K, b.V, 0, b.table, b.kv_len, b.q_start))
     pool.close()
+def test_one_workspace_for_calls_in_turn_and_a_graph(kp):
+    """Two layers' calls share a workspace on a stream of their own, then in a
+    graph whose replays see other lengths."""
+    import torch
+
+    w = wl.custom("turn", 2, 2, 8, 128, 500, 1, "lognormal", bits=(3,))
+    pool, encs = filled(kp, w, layers=2, max_rows=64)
+    b = Batch(2, 8, 128, 16, [30, 1, 7], [200, 90, 7], seed=31, layers=2, layer=0, extra_rows=2)
+    b.K[1], b.V[1] = -b.K[0], 2 * b.V[0]
+    c = OneCache(b)
+    st = torch.cuda.Stream()
+    ws = torch.empty(pool.attend_pages_ws_bytes(b.tokens, 8), dtype=torch.uint8, device="cuda")
+    out = torch.empty(2, b.tokens, 8, 128, device="cuda")
+
+    def refs():
+        return [reference(encs[l], b.Q, np.nan_to_num(b.K), np.nan_to_num(b.V), l, b.table, b.kv_len, b.q_start)
+                for l in range(2)]
+
+    def both(stream):
+        for l in range(2):
+            pool.attend_pages(l, c.Q, c, c, workspace=ws, out=out[l], stream=stream)
+
+    torch.cuda.synchronize()
+    for _ in range(3):
+        both(st)
+    st.synchronize()
+    for l, ref in enumerate(refs()):
+        close(out[l], ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(None)
+    for kv in ([200, 90, 7], [60, 33, 50], [30, 1, 96]):
+        need = [-(-t // b.P) for t in kv]
+        order = np.random.default_rng(sum(kv)).permutation(b.K.shape[1])
+        if sum(need) > len(order):
+            order = np.resize(order, sum(need))
+        b.table[:] = -7
+        at = 0
+        for s, n in enumerate(need):
+            b.table[s, :n] = order[at: at + n]
+            at += n
+        b.kv, b.kv_len = kv, np.array(kv, np.int32)
+        for X in (b.K, b.V):
+            np.nan_to_num(X, copy=False)
+        c.K.copy_(torch.from_numpy(b.K)), c.V.copy_(torch.from_numpy(b.V))
+        c.table.copy_(torch.from_numpy(b.table)), c.kv_len.copy_(torch.from_numpy(b.kv_len))
+        out.fill_(float("nan"))
+        graph.replay()
+        for l, ref in enumerate(refs()):
+            close(out[l], ref)
+    assert pool.status() == 0 and int(c.status_word.cpu()[0]) == 0
+    pool.close()
+
+
+def test_two_streams_at_once(kp):
+    """Calls on two streams, each with a workspace of its own, many times: the same bits each time."""
+    import torch
+
+    w = wl.custom("streams", 1, 2, 8, 128, 700, 1, "lognormal", bits=(3,))
+    pool, encs = filled(kp, w, max_rows=128)
+    bs = [Batch(2, 8, 128, 16, [1, 1, 2], [700, 30, 300], seed=32, extra_rows=1),
+          Batch(2, 8, 128, 16, [120, 50], [600, 400], seed=33).many()]
+    cs = [OneCache(b) for b in bs]
+    cs[1].max_q, cs[1].max_kv = bs[1].tokens, 1 << 16
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for st, c, g in zip(streams, cs, got):
+            g.append(pool.attend_pages(0, c.Q, c, c, stream=st))
+    torch.cuda.synchronize()
+    for b, g in zip(bs, got):
+        close(g[0], reference(encs[0], b.Q, b.K, b.V, 0, b.table, b.kv_len, b.q_start))
+        for x in g[1:]:
+            assert torch.equal(x, g[0])
+    assert pool.status() == 0
+    pool.close()
