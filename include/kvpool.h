@@ -451,7 +451,8 @@ typedef struct {
     int page_tokens;  /* 16, 32, 64 or 128 */
     int head_dim;     /* 64 or 128 */
     int32_t* status;  /* device word that the kernels OR error bits into (zeroed by the caller), or NULL:
-                         1 a page number out of range, 2 a bounded wait expired; see kvpool_pages_status */
+                         1 a page number out of range, or none for a token; 2 a bounded wait expired; see
+                         kvpool_pages_status */
 } kvpool_pages_t;
 
 /* The sequences of one call. Sequence s holds kv_len[s] tokens, this call's
@@ -459,8 +460,11 @@ typedef struct {
  * page_table[s * table_stride + j / page_tokens]. The rows [q_start[s],
  * q_start[s + 1]) of the call's inputs are its new tokens: n of them, the i-th
  * at position kv_len[s] - n + i. Entries of the table behind a sequence's last
- * token are not read. Rows from q_start[seqs] on (padding) belong to nobody:
- * nothing is written for them. */
+ * token are not read. Tokens that the table has no room for (kv_len[s] >
+ * table_stride * page_tokens) are written to nowhere and seen by no row, and
+ * are recorded as a page number out of range is; positions before 0 (more new
+ * tokens than held ones) are written to nowhere and see nothing. Rows from
+ * q_start[seqs] on (padding) belong to nobody: nothing is written for them. */
 typedef struct {
     int seqs;                  /* >= 1 */
     int table_stride;          /* table entries per sequence, >= 1 */
@@ -544,8 +548,9 @@ int kvpool_attend_pages(kvpool_t* pool, int pool_layer, const kvpool_pages_t* pa
 size_t kvpool_attend_pages_ws_bytes(const kvpool_t* pool, int tokens, int q_heads);
 
 /* Synchronise `stream`, then return and clear *pages->status: KVPOOL_OK,
- * KVPOOL_ERR_INVALID_ARG (a page number was out of range) or
- * KVPOOL_ERR_TIMEOUT. KVPOOL_ERR_INVALID_ARG too when status is NULL. */
+ * KVPOOL_ERR_INVALID_ARG (a page number was out of range, or a sequence longer
+ * than its table has room for) or KVPOOL_ERR_TIMEOUT. KVPOOL_ERR_INVALID_ARG
+ * too when status is NULL. */
 int kvpool_pages_status(const kvpool_pages_t* pages, void* stream);
 
 /* The pager: which pages each sequence owns. Host only, no device work: its

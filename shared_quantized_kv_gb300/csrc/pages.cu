@@ -42,8 +42,8 @@ pages_append_kernel(const PagedSeqs s, uint4* __restrict__ Kp, uint4* __restrict
     // blocks of one row each are numbered over the sequences' rows alone; rows
     // that belong to nobody lie behind them, so the block's row is the token
     // (q_start ascending from 0, as documented)
-    const int pos = b.T - b.n + b.blk;
-    if (pos < 0 || b.q0 + b.blk != tok) return;
+    const int pos = b.p0 + b.blk;
+    if (pos < 0 || pos >= b.T || b.q0 + b.blk != tok) return;  // (at T and behind it: no room in the table)
     const int page = __ldg(s.table + (long long)b.seq * s.tstride + (pos >> s.pshift));
     if (page < 0 || page >= s.pages) {
         if (lane == 0) flag(s.status, kPgBadPage);

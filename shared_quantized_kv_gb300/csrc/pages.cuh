@@ -90,29 +90,32 @@ __device__ __forceinline__ void flag(int* status, int bit) {
 // First row of sequence i: entry i of q_start, held inside [0, tokens].
 __device__ __forceinline__ int row_begin(const PagedSeqs& s, int i) { return min(max(__ldg(s.q_start + i), 0), s.tokens); }
 
-// Tokens that sequence i holds, at most what its table has room for.
-__device__ __forceinline__ int held_tokens(const PagedSeqs& s, int i) {
-    return (int)min((long long)max(__ldg(s.kv_len + i), 0), (long long)s.tstride << s.pshift);
+// Tokens that sequence i holds by its length, and those that its table has room for.
+__device__ __forceinline__ int length_of(const PagedSeqs& s, int i) { return max(__ldg(s.kv_len + i), 0); }
+__device__ __forceinline__ int held_tokens(const PagedSeqs& s, int length) {
+    return (int)min((long long)length, (long long)s.tstride << s.pshift);
 }
 
 // The rows of all sequences cut into blocks of RB rows (a row: a new token and
 // one of the G query heads of a KV head; a block holds rows of one sequence).
 // Block z: its sequence, its number there, the sequence's first token row q0,
-// new tokens n and held tokens T. False past the last block. Whole warps call
-// it; 32 sequences at a time, their loads independent of one another.
+// new tokens n, the first one's position p0 (the others follow) and held tokens
+// T: a sequence longer than its table has room for holds the tokens that fit,
+// and is recorded. False past the last block. Whole warps call it; 32 sequences
+// at a time, their loads independent of one another.
 struct RowBlock {
-    int seq, blk, q0, n, T;
+    int seq, blk, q0, n, p0, T;
 };
 __device__ __forceinline__ bool find_block(const PagedSeqs& s, int G, int RB, int z, RowBlock& b) {
     const int lane = threadIdx.x & 31;
     int before = 0;  // blocks of the sequences before these 32
     for (int base = 0; base < s.seqs; base += 32) {
         const int i = base + lane;
-        int q0 = 0, n = 0, T = 0;
+        int q0 = 0, n = 0, len = 0;
         if (i < s.seqs) {
             q0 = row_begin(s, i);
             n = max(row_begin(s, i + 1) - q0, 0);
-            T = held_tokens(s, i);
+            len = length_of(s, i);
         }
         const int nb = (int)(((long long)n * G + RB - 1) / RB);
         int sum = nb;
@@ -127,7 +130,10 @@ __device__ __forceinline__ bool find_block(const PagedSeqs& s, int G, int RB, in
             b.seq = base + l;
             b.q0 = __shfl_sync(0xffffffffu, q0, l);
             b.n = __shfl_sync(0xffffffffu, n, l);
-            b.T = __shfl_sync(0xffffffffu, T, l);
+            len = __shfl_sync(0xffffffffu, len, l);
+            b.p0 = len - b.n;
+            b.T = held_tokens(s, len);
+            if (len > b.T && lane == 0) flag(s.status, kPgBadPage);
             b.blk = z - before - __shfl_sync(0xffffffffu, sum - nb, l);
             return true;
         }

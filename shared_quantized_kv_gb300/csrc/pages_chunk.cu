@@ -199,7 +199,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const int i = pages::div_group(p, j_begin + row);
         tok = b.q0 + i_begin + i;
         head = g * p.G + j_begin + row - i * p.G;
-        pos = T - b.n + i_begin + i;
+        pos = b.p0 + i_begin + i;
         see = pages::row_seen<SCORED>(p, b.seq, tok, pos, T);
     }
     // Q on its way to registers: 16-byte pieces, consecutive lanes on consecutive
@@ -246,7 +246,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     auto seen_end = [&](int slot) {
         if constexpr (SCORED) return rng[2 * slot + 1];
         const int last = two && slot == 0 ? kTile - 1 : nr - 1;
-        return max(0, min(T, T - b.n + i_begin + pages::div_group(p, j_begin + last) + 1));
+        return max(0, min(T, b.p0 + i_begin + pages::div_group(p, j_begin + last) + 1));
     };
     // this CTA's key tiles [ta, ta + n), counted without the gap: the cluster's
     // share of the tiles that any row sees; a slot takes those that its rows see

@@ -106,8 +106,11 @@ pages_rows_kernel(const PagedAttend p) {
         b.blk = 0;
         b.q0 = pages::row_begin(s, b.seq);
         b.n = max(pages::row_begin(s, b.seq + 1) - b.q0, 0);
-        b.T = pages::held_tokens(s, b.seq);
+        const int len = pages::length_of(s, b.seq);
+        b.p0 = len - b.n;
+        b.T = pages::held_tokens(s, len);
         if (b.n == 0) return;  // the whole cluster's
+        if (len > b.T && tid == 0) pages::flag(s.status, kPgBadPage);
     } else {
         if (!pages::find_block(s, p.G, kRows, blockIdx.x / S, b)) return;
     }
@@ -129,7 +132,7 @@ pages_rows_kernel(const PagedAttend p) {
             const int i = (r_begin + r) / p.G;
             tok[h] = b.q0 + i;
             head[h] = g * p.G + (r_begin + r) - i * p.G;
-            pos[h] = T - b.n + i;
+            pos[h] = b.p0 + i;
             see[h] = pages::row_seen<SCORED>(p, b.seq, tok[h], pos[h], T);
             slope2[h] = SCORED && p.slopes ? __ldg(p.slopes + head[h]) * 1.4426950408889634f : 0.0f;
         }
@@ -318,9 +321,9 @@ pages_rows_kernel(const PagedAttend p) {
             for (int r = 0; r < nr; ++r) {
                 if (!((odds >> ((r & 7) * 4)) & 0xFu)) continue;
                 const int i = (r_begin + r) / p.G, hd = g * p.G + (r_begin + r) - i * p.G;
-                const Seen se = pages::row_seen<SCORED>(p, b.seq, b.q0 + i, T - b.n + i, T);
+                const Seen se = pages::row_seen<SCORED>(p, b.seq, b.q0 + i, b.p0 + i, T);
                 float mm, ll, acc[D / 32];
-                pages::careful_row<D, SCORED>(p, b.seq, b.q0 + i, hd, T - b.n + i, se, gap, 4, ua + warp,
+                pages::careful_row<D, SCORED>(p, b.seq, b.q0 + i, hd, b.p0 + i, se, gap, 4, ua + warp,
                                               ub, kWarps, mm, ll, acc);
                 float* dst = rows + r * RS;
                 __syncwarp();

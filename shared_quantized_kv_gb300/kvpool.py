@@ -407,7 +407,8 @@ def pages_append(K_pages, V_pages, layer, K, V, table, kv_len, q_start, status=N
     [seqs, pages of a sequence], kv_len int32 [seqs] (the new tokens included),
     q_start int32 [seqs + 1]: sequence s's new tokens are rows q_start[s] ...
     q_start[s + 1] - 1. status: None or an int32 [1] word that records page
-    numbers out of range. All on the current device."""
+    numbers out of range and sequences longer than their table has room for,
+    whose tokens are dropped. All on the current device."""
     dev = _here()
     pg = _pages(K_pages, V_pages, status, dev)
     n = K.shape[0]
