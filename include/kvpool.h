@@ -536,7 +536,8 @@ int kvpool_pages_attend(const kvpool_pages_t* pages, int layer, const kvpool_seq
  * of at least kvpool_attend_pages_ws_bytes bytes, 16-byte aligned, scratch;
  * calls that overlap on the GPU must not share one. The pool's max_rows bounds
  * one token's rows here, not the call's: more tokens than max_rows / (q_heads
- * / kv_heads) read the pool again for every such slice. Errors as
+ * / kv_heads), or than fill the GPU once with row groups of every KV head, read
+ * the pool again for every such slice. Errors as
  * kvpool_attend_ws and kvpool_pages_attend. Source: as kvpool_attend (PolyKV
  * summary, section 2.A; CoMixKV article, recent states). */
 int kvpool_attend_pages(kvpool_t* pool, int pool_layer, const kvpool_pages_t* pages, int page_layer,

@@ -646,14 +646,16 @@ int kvpool_attend_ws(kvpool_t* p, int layer, const void* Q, int agents, int q_he
 namespace {
 
 // kvpool_attend_pages takes the tokens in slices whose rows fit the pool's
-// row limit; its workspace holds the pages' (m, l) of all rows, then what
-// kvpool_attend_ws needs for a slice.
+// row limit and whose row groups (times the KV heads) fit one wave of CTAs; its
+// workspace holds the pages' (m, l) of all rows, then what kvpool_attend_ws
+// needs for a slice.
 struct PagesWs {
     int slice;  // tokens per slice
     size_t ml_bytes, bytes;
 };
 PagesWs pages_ws(const kvpool* p, long long tokens, int group) {
-    PagesWs w{(int)std::min<long long>(tokens, p->max_rows / group), 0, 0};
+    const long long wave = (long long)(p->sm_count / p->kv_heads) * (128 / group);  // groups of <= 128 rows, whole tokens
+    PagesWs w{(int)std::min({tokens, (long long)(p->max_rows / group), wave}), 0, 0};
     if (w.slice < 1) return w;
     const WsLayout l = ws_layout(p, (long long)w.slice * group, group);
     if (l.bytes == 0) return w;
@@ -688,7 +690,7 @@ int kvpool_attend_pages(kvpool_t* p, int pool_layer, const kvpool_pages_t* pages
     if (group > p->max_rows) return KVPOOL_ERR_INVALID_ARG;
     if (!p->compressed[pool_layer]) return KVPOOL_ERR_STATE;
     const PagesWs w = pages_ws(p, tokens, group);
-    if (w.bytes == 0) return KVPOOL_ERR_UNSUPPORTED;  // more row groups than one wave of CTAs
+    if (w.bytes == 0) return KVPOOL_ERR_UNSUPPORTED;  // a token's row groups are more than one wave of CTAs
     if (!workspace || !aligned16(workspace) || workspace_bytes < w.bytes) return KVPOOL_ERR_INVALID_ARG;
     // The pages' states of all rows: accumulators into out, (m, l) into the
     // workspace (0 for rows of no sequence); then slice by slice the pool's

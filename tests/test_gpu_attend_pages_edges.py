@@ -47,6 +47,32 @@ def test_rows_of_no_sequence_and_a_pool_far_below_0(kp, d, level):
     assert pool.status() == 0
     close(got, reference(encs[0], b.Q, b.K, b.V, 0, b.table, b.kv_len, b.q_start))
     pool.close()
+@pytest.mark.parametrize("hk,hq,max_rows,tokens", [(40, 40, 0, 400), (32, 32, 1024, 700), (20, 40, 1024, 513)])
+def test_more_rows_than_one_wave_of_the_pool(kp, hk, hq, max_rows, tokens):
+    """max_rows admits more rows at once than the pool's attention has CTAs for."""
+    w = wl.custom("wave", 1, hk, hq, 64, 130, 1, "lognormal", bits=(3,))
+    pool, encs = filled(kp, w, max_rows=max_rows)
+    b = Batch(hk, hq, 64, 64, [tokens - 3, 1, 2], [tokens - 3, 50, 70], seed=hk)
+    c = OneCache(b)
+    got = pool.attend_pages(0, c.Q, c, c)
+    assert pool.status() == 0 and int(c.status_word.cpu()[0]) == 0
+    ref = reference(encs[0], b.Q[-40:], b.K, b.V, 0, b.table, b.kv_len, np.array([0, 37, 38, 40]))
+    close(got[-40:], ref)
+    few = Batch(hk, hq, 64, 64, [40], [40], seed=hk)  # the first rows, alone
+    few.K, few.V, few.table, few.Q = b.K, b.V, b.table[:1], b.Q[:40]
+    close(got[:40], reference(encs[0], few.Q, few.K, few.V, 0, few.table, few.kv_len, few.q_start))
+    pool.close()
+
+
+def test_more_kv_heads_than_the_gpu_has_sms_is_refused(kp):
+    import torch
+
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    pool = kp.KVPool(1, sms + 1, 64, 130, [3])
+    assert pool.attend_pages_ws_bytes(5, sms + 1) == 0 and pool.attend_ws_bytes(5, sms + 1) == 0
+    pool.close()
+
+
 def test_one_workspace_for_calls_in_turn_and_a_graph(kp):
     """Two layers' calls share a workspace on a stream of their own, then in a
     graph whose replays see other lengths."""
