@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -332,7 +333,8 @@ class Pager:
 
 
 def _i32(x, name):
-    """x, which ctypes would cut to 32 bits without a word."""
+    """The whole number x, which ctypes would cut to 32 bits without a word."""
+    x = operator.index(x)
     if not -(1 << 31) <= x < 1 << 31:
         raise ValueError(f"{name} must fit 32 bits, not {x}")
     return x
@@ -531,9 +533,12 @@ class PagedCache:
     def grow(self, seqs, counts, stream=None):
         """Room for counts[i] new tokens at the end of seqs[i]: the batch that
         append and attend take, rows in this order. Fewer free pages than it
-        takes: KVPoolError (OOM), and no sequence has grown."""
+        takes: KVPoolError (OOM). Whatever it raises, no sequence has grown."""
         if len(seqs) != len(counts) or not len(seqs) or len(set(seqs)) != len(seqs):
             raise ValueError("one count per sequence, each sequence once")
+        counts = [_i32(n, "counts") for n in counts]
+        dev = _here()  # (another device's cache or stream is refused before anything changes)
+        _pages(self.K, self.V, self.status_word, dev), _raw_stream(stream, dev)
         before = [self.pager.length(s) for s in seqs]
         src, dst = [], []
         try:
@@ -542,15 +547,15 @@ class PagedCache:
                 if pair:
                     src.append(pair[0])
                     dst.append(pair[1])
-        except KVPoolError:
-            # (a page of its own that a sequence got already is copied below and kept)
+            pages_copy(self.K, self.V, src, dst, stream)
+            return PagedBatch(self, seqs, counts, stream)
+        except BaseException:
+            # (a page of its own that a sequence got already is copied and kept)
             for s, n in zip(seqs, before):
                 self.pager.truncate(s, n)
             live = [(a, b) for a, b in zip(src, dst) if self.pager.owners(b)]
             pages_copy(self.K, self.V, [a for a, _ in live], [b for _, b in live], stream)
             raise
-        pages_copy(self.K, self.V, src, dst, stream)
-        return PagedBatch(self, seqs, counts, stream)
 
     def append(self, layer, K, V, batch, stream=None):
         """Write the batch's new tokens: K, V bf16 [tokens, kv_heads, d]."""

@@ -1,9 +1,6 @@
 """PagedCache.grow when it cannot grow, on a machine without a GPU (the page
 copies and the batch's upload are recorded, not made): no sequence has grown,
-and every page that a sequence got of its own meanwhile is copied. And numbers
-that do not fit the calls' 32 bits."""
-
-import ctypes
+and every page that a sequence got of its own meanwhile is copied."""
 
 import pytest
 
@@ -26,7 +23,9 @@ class Recorded:
 
         monkeypatch.setattr(kp, "pages_copy", copy)
         monkeypatch.setattr(kp, "PagedBatch", batch)
+        monkeypatch.setattr(kp, "_here", lambda: 0)
         monkeypatch.setattr(kp, "_pages", lambda *a, **k: None)
+        monkeypatch.setattr(kp, "_raw_stream", lambda *a, **k: None)
 
 
 @pytest.fixture
@@ -89,3 +88,18 @@ def test_a_batch_that_cannot_be_uploaded(kp, monkeypatch):
         r.cache.grow([a, b], [1, 20])
         assert r.cache.pager.length(a) == 21 and r.cache.pager.length(b) == 40
         r.cache.close()
+
+
+@pytest.mark.parametrize("what", ["_here", "_pages", "_raw_stream"])
+def test_another_device(kp, monkeypatch, what):
+    r, a, b = forked(kp, monkeypatch)
+
+    def refuse(*args, **kwargs):
+        raise ValueError("another device")
+
+    monkeypatch.setattr(kp, what, refuse)
+    with pytest.raises(ValueError):
+        r.cache.grow([a, b], [1, 20])
+    check_nobody_has_grown(r, a, b)
+    assert not r.copied
+    r.cache.close()
