@@ -261,7 +261,8 @@ class Pager:
 
     def __init__(self, pages, page_tokens):
         h = ctypes.c_void_p()
-        _check(_lib().kvpool_pager_create(ctypes.byref(h), pages, page_tokens), "kvpool_pager_create")
+        _check(_lib().kvpool_pager_create(ctypes.byref(h), _i32(pages, "pages"), _i32(page_tokens, "page_tokens")),
+               "kvpool_pager_create")
         self._h, self.pages, self.page_tokens = h, pages, page_tokens
 
     @property
@@ -293,20 +294,21 @@ class Pager:
         """Room for n more tokens: None, or the (shared page, own page) pair
         that has to be copied before they are written."""
         pair = (ctypes.c_int32 * 2)()
-        due = self._count(_lib().kvpool_pager_extend(self._h, seq, _i32(n, "n"), pair), "kvpool_pager_extend")
+        due = self._count(_lib().kvpool_pager_extend(self._h, _i32(seq, "seq"), _i32(n, "n"), pair),
+                          "kvpool_pager_extend")
         return (pair[0], pair[1]) if due else None
 
     def truncate(self, seq, length):
         """Cut a sequence to its first `length` tokens."""
-        _check(_lib().kvpool_pager_truncate(self._h, seq, _i32(length, "length")), "kvpool_pager_truncate")
+        _check(_lib().kvpool_pager_truncate(self._h, _i32(seq, "seq"), _i32(length, "length")), "kvpool_pager_truncate")
 
     def fork(self, seq) -> int:
         """A new sequence that shares all pages of seq."""
-        return self._count(_lib().kvpool_pager_fork(self._h, seq), "kvpool_pager_fork")
+        return self._count(_lib().kvpool_pager_fork(self._h, _i32(seq, "seq")), "kvpool_pager_fork")
 
     def free(self, seq):
         """End a sequence."""
-        _check(_lib().kvpool_pager_free(self._h, seq), "kvpool_pager_free")
+        _check(_lib().kvpool_pager_free(self._h, _i32(seq, "seq")), "kvpool_pager_free")
 
     def compact(self):
         """Owned pages become the lowest numbers: lists (src, dst) of the page copies due."""
@@ -315,10 +317,11 @@ class Pager:
         return list(src[:n]), list(dst[:n])
 
     def length(self, seq) -> int:
-        return self._count(_lib().kvpool_pager_len(self._h, seq), "kvpool_pager_len")
+        return self._count(_lib().kvpool_pager_len(self._h, _i32(seq, "seq")), "kvpool_pager_len")
 
     def table(self, seq):
         """The sequence's pages in order (list of int)."""
+        seq = _i32(seq, "seq")
         n = self._count(_lib().kvpool_pager_table(self._h, seq, None, 0), "kvpool_pager_table")
         buf = (ctypes.c_int32 * max(n, 1))()
         self._count(_lib().kvpool_pager_table(self._h, seq, buf, n), "kvpool_pager_table")
@@ -329,7 +332,7 @@ class Pager:
 
     def owners(self, page) -> int:
         """Sequences that own the page (0: free)."""
-        return self._count(_lib().kvpool_pager_owners(self._h, page), "kvpool_pager_owners")
+        return self._count(_lib().kvpool_pager_owners(self._h, _i32(page, "page")), "kvpool_pager_owners")
 
 
 def _i32(x, name):
@@ -411,6 +414,7 @@ def pages_append(K_pages, V_pages, layer, K, V, table, kv_len, q_start, status=N
     q_start[s + 1] - 1. status: None or an int32 [1] word that records page
     numbers out of range and sequences longer than their table has room for,
     whose tokens are dropped. All on the current device."""
+    layer = _i32(layer, "layer")
     dev = _here()
     pg = _pages(K_pages, V_pages, status, dev)
     n = K.shape[0]
@@ -453,6 +457,7 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
     gets 0 and -inf; rows behind the last sequence are left as they are."""
     import torch
 
+    layer = _i32(layer, "layer")
     dev = _here()
     pg = _pages(K_pages, V_pages, status, dev)
     if Q.dim() != 3:
@@ -727,7 +732,8 @@ class KVPool:
 
     def attend_pages_ws_bytes(self, tokens, q_heads) -> int:
         """Workspace bytes kvpool_attend_pages needs for this many tokens."""
-        return int(_lib().kvpool_attend_pages_ws_bytes(self._h, int(tokens), int(q_heads)))
+        return int(_lib().kvpool_attend_pages_ws_bytes(self._h, _i32(int(tokens), "tokens"),
+                                                       _i32(int(q_heads), "q_heads")))
 
     def attend_pages(self, layer, Q, cache, batch, page_layer=None, workspace=None, out=None, softmax_scale=0.0,
                      stream=None):
@@ -736,6 +742,8 @@ class KVPool:
         number). Q: bf16 [tokens, q_heads, d]. Returns out: float32, like Q."""
         import torch
 
+        layer = _i32(layer, "layer")
+        page_layer = layer if page_layer is None else _i32(page_layer, "page_layer")
         n, hq, d = Q.shape
         dev = _here()
         pg = _pages(cache.K, cache.V, cache.status_word, dev)
@@ -751,7 +759,7 @@ class KVPool:
                 out = torch.empty((n, hq, d), dtype=torch.float32, device=Q.device)
             if workspace is None:
                 workspace = torch.empty(max(self.attend_pages_ws_bytes(n, hq), 16), dtype=torch.uint8, device=Q.device)
-        _check(_lib().kvpool_attend_pages(self._h, layer, ctypes.byref(pg), layer if page_layer is None else page_layer,
+        _check(_lib().kvpool_attend_pages(self._h, layer, ctypes.byref(pg), page_layer,
                                           ctypes.byref(sq), qp, hq, _need(out, torch.float32, "out", dev),
                                           softmax_scale, _need(workspace, workspace.dtype, "workspace", dev),
                                           workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
