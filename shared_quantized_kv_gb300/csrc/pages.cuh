@@ -213,29 +213,31 @@ __device__ __forceinline__ float2* state_ml(const PagedAttend& a, int t, int hd)
 // which the cap turns into cap * 2^-22 of a score that is at least 0.6 cap (the
 // reciprocal of an overflowed e^(2z) is 0, as it should be). 32 keys take the
 // polynomial where all of a warp's are near (no exponential and no reciprocal
-// per key), else the other form, whose error is the same part of the cap.
+// per key), else the other form, whose error is the same part of the cap: 2^-16
+// nats at most for caps up to 64. With wider ones (WIDE) each key takes its own.
+constexpr float kWideCap2 = 64.0f * 1.4426950408889634f;
 __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float capped(const PagedAttend& a, float s) {
+    const float z = s * a.cap_z, u = z * z;
+    float q = fmaf(u, a.cap_q[4], a.cap_q[3]);
+    q = fmaf(u, q, a.cap_q[2]), q = fmaf(u, q, a.cap_q[1]), q = fmaf(u, q, a.cap_q[0]);
+    const float far = fmaf(-2.0f * a.cap2, rcp(ptx::ex2(s * a.cap_in) + 1.0f), a.cap2);
+    return fabsf(s) <= a.cap_near ? s * fmaf(u, q, a.scale_log2) : far;
+}
 template <bool SCORED>
 __device__ __forceinline__ float score(const PagedAttend& a, float s, float slope2, int pos, int j) {
-    if (!SCORED || !(a.cap2 > 0.0f)) {
-        s *= a.scale_log2;
-    } else {
-        const float z = s * a.cap_z, u = z * z;
-        float q = fmaf(u, a.cap_q[4], a.cap_q[3]);
-        q = fmaf(u, q, a.cap_q[2]), q = fmaf(u, q, a.cap_q[1]), q = fmaf(u, q, a.cap_q[0]);
-        const float far = fmaf(-2.0f * a.cap2, rcp(ptx::ex2(s * a.cap_in) + 1.0f), a.cap2);
-        s = fabsf(s) <= a.cap_near ? s * fmaf(u, q, a.scale_log2) : far;
-    }
+    s = !SCORED || !(a.cap2 > 0.0f) ? s * a.scale_log2 : capped(a, s);
     if (SCORED && a.slopes) s = fmaf(-slope2, fabsf((float)(pos - j)), s);
     return s;
 }
 // The scores of 32 keys. behind: no key lies behind the row's position, so the
 // distance to key j0 joins the constant and each key costs one more step. live:
 // the row is one (which form a warp's tanh takes is for its rows to say).
+template <bool WIDE>
 __device__ __forceinline__ void scores32(const PagedAttend& a, float (&x)[32], float slope2, int pos, int j0,
                                          bool behind, bool live) {
     const float far = (float)(pos - j0), base = a.slopes && behind ? -slope2 * far : 0.0f;
@@ -265,6 +267,9 @@ __device__ __forceinline__ void scores32(const PagedAttend& a, float (&x)[32], f
             const float2 y = __ffma2_rn(s, __ffma2_rn(u, q, f), c);
             x[k] = y.x, x[k + 1] = y.y;
         }
+    } else if constexpr (WIDE) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = capped(a, x[k]) + base;
     } else {
         const float2 in = make_float2(a.cap_in, a.cap_in), one = make_float2(1.0f, 1.0f);
         const float2 f = make_float2(-2.0f * a.cap2, -2.0f * a.cap2), c = make_float2(a.cap2 + base, a.cap2 + base);

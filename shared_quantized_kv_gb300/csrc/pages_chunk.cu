@@ -124,8 +124,9 @@ __device__ __forceinline__ uint32_t span_bits(int a, int b, int c) {
 
 // KIND: the causal mask alone; other masks too; scores that a cap or a bias by
 // distance changes (their costs are apart: 2,432 tokens over 16K keys take
-// 343 us, 417 with a window, 795 with a cap, 618 with a bias and 830 with both).
-enum { kPlain, kMasks, kScores };
+// 343 us, 417 with a window, 795 with a cap, 618 with a bias and 830 with both);
+// the same with a cap so wide that each key takes a form of its own.
+enum { kPlain, kMasks, kScores, kWideScores };
 // STATE: the rows' states for a merge instead of the output; the weights then
 // go through the product with V as bf16 hi and lo (16 bits; lo in the half of
 // S's columns that hi leaves), as the merged output is float32.
@@ -135,7 +136,8 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                    const PagedAttend p) {
     using L = Lay<D>;
     constexpr bool SCORED = KIND != kPlain;
-    constexpr float kLazy = KIND == kScores ? kLazyScores : kLazyMax;
+    constexpr bool CHANGED = KIND == kScores || KIND == kWideScores;
+    constexpr float kLazy = CHANGED ? kLazyScores : kLazyMax;
     constexpr uint32_t kColS = 0, kColO = 256;  // slot w: 128 w columns on
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(
@@ -264,10 +266,10 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int n = max(0, min(t_hi, ta + per) - ta);
     // Modified scores take the tiles from the last to the first: with a bias by
     // distance the first then holds the maxima, and the reference hardly moves.
-    auto tile_at = [&](int i) { return gap.number(KIND == kScores ? ta + n - 1 - i : ta + i); };
+    auto tile_at = [&](int i) { return gap.number(CHANGED ? ta + n - 1 - i : ta + i); };
     auto tiles_of = [&](int slot) {
         if (!two) return (n - slot + 1) / 2;
-        if (KIND == kScores) return n;  // (of the tiles that the other slot alone sees, the halves are passed over)
+        if (CHANGED) return n;  // (of the tiles that the other slot alone sees, the halves are passed over)
         return max(0, min(n, gap.count((seen_end(slot) + kTile - 1) / kTile) - ta));
     };
     if (rank >= S) {  // not a split block's: nothing to do, and nobody waits for this CTA
@@ -375,7 +377,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         ptx::mma_f16_ta_elect(tO, tP, dv + ks * (2048 >> 4), idO, (it > 0 || ks > 0) ? 1u : 0u);
                         if constexpr (STATE) ptx::mma_f16_ta_elect(tO, tP + 16, dv + ks * (2048 >> 4), idO, 1u);
                     }
-                    if (KIND == kScores && h == 0) ptx::mma_commit_elect(u_o);  // (it takes over 100 cycles)
+                    if (CHANGED && h == 0) ptx::mma_commit_elect(u_o);  // (it takes over 100 cycles)
                 }
             };
             // The slots take turns: P V and the next Q K^T of one, then of the other, so
@@ -552,14 +554,14 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             ptx::bar_sync(b_pair, 64);  // P of either part overwrites what both have read
         }
         float top = -CUDART_INF_F;  // the part's maximum in the tile before
-        const float scale = KIND == kScores ? 1.0f : p.scale_log2;  // of scores in units of log2 already, or not
+        const float scale = CHANGED ? 1.0f : p.scale_log2;  // of scores in units of log2 already, or not
         // the scores of the part's 32 keys from k0 on, -inf where the row sees none
         auto in_log2 = [&](int k0, bool whole, uint32_t (&u)[32]) {
-            if constexpr (KIND == kScores) {
+            if constexpr (CHANGED) {
                 const bool behind = p.slopes && __all_sync(0xffffffffu, !live || pos >= k0 + 31);
                 // (what an unseen place holds has no say in the form that a cap takes)
                 if (!whole && p.cap2 > 0.0f) mask(k0, u, 0.0f);
-                pages::scores32(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0, behind, live);
+                pages::scores32<KIND == kWideScores>(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0, behind, live);
             }
             if (!whole) mask(k0, u, -CUDART_INF_F);
         };
@@ -567,11 +569,11 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const int i = two ? it : 2 * it + w;  // tile of this CTA
             const int t0 = tile_at(i) * kTile;
             // A maximum that passes the reference by 2^8 moves it: where scores cost much
-            // to form or may rise fast (kScores) at once, else before the next tile (until
+            // to form or may rise fast (CHANGED) at once, else before the next tile (until
             // then the weights are that much larger, which float32 has room for up to 2^128;
             // rows beyond it come out infinite and are done again). The two threads of a row
             // ask one another while S is on its way.
-            const bool moves = KIND != kScores && it > 0 && some && ptx::bar_or(b_pair, 64, top > m + kLazy);
+            const bool moves = !CHANGED && it > 0 && some && ptx::bar_or(b_pair, 64, top > m + kLazy);
             warp_wait(b_s + 8 * w, it & 1, bad);
             ptx::tc_fence_after();
             // keys behind the sequence's end: whatever their V holds becomes 0 (a
@@ -630,7 +632,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     ptx::tmem_wait_ld(u);
                     in_log2(k0, whole, u);
                     const float x = max_of(u) * scale;
-                    if constexpr (KIND == kScores) {
+                    if constexpr (CHANGED) {
                         if (ptx::bar_or(b_pair, 64, x > m + kLazy || (m == -CUDART_INF_F && x > m))) {
                             if (h) {  // (S came after every P V but the first half's)
                                 warp_wait(b_o + 8 * w, it & 1, bad);
@@ -682,7 +684,7 @@ pages_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             se.b2 = __shfl_sync(0xffffffffu, see.b2, of);
             pages::careful_row<D, SCORED>(p, b.seq, __shfl_sync(0xffffffffu, tok, of),
                                           __shfl_sync(0xffffffffu, head, of), __shfl_sync(0xffffffffu, pos, of), se,
-                                          gap, 7, two || all ? ta : ta + (KIND == kScores ? (n - 1 - w) & 1 : w), ta + n,
+                                          gap, 7, two || all ? ta : ta + (CHANGED ? (n - 1 - w) & 1 : w), ta + n,
                                           two || all ? 1 : 2, cm, cl, acc);
         };
         l = joined(l, true);
@@ -987,10 +989,14 @@ cudaError_t launch(const PagedAttend& a, int max_q, int max_kv, cudaStream_t st)
 }  // namespace
 
 cudaError_t launch_pages_chunk(const PagedAttend& a, int head_dim, int max_q, int max_kv, cudaStream_t st) {
-    const int kind = a.cap2 > 0.0f || a.slopes ? kScores : paged_scored(a) ? kMasks : kPlain;
+    const int kind = a.cap2 > pages::kWideCap2        ? kWideScores
+                     : a.cap2 > 0.0f || a.slopes ? kScores
+                     : paged_scored(a)           ? kMasks
+                                                 : kPlain;
 #define KVP_PG_CHUNK(KK, SS) \
     (head_dim == 64 ? launch<64, KK, SS>(a, max_q, max_kv, st) : launch<128, KK, SS>(a, max_q, max_kv, st))
     if (a.st_acc) return KVP_PG_CHUNK(kPlain, true);
+    if (kind == kWideScores) return KVP_PG_CHUNK(kWideScores, false);
     if (kind == kScores) return KVP_PG_CHUNK(kScores, false);
     return kind == kMasks ? KVP_PG_CHUNK(kMasks, false) : KVP_PG_CHUNK(kPlain, false);
 #undef KVP_PG_CHUNK
