@@ -528,9 +528,16 @@ class PagedCache:
         """Cut a sequence to its first `length` tokens."""
         self.pager.truncate(seq, length)
 
+    def _usable(self, stream):
+        """Another device's cache or stream is refused, before the pager has changed anything."""
+        dev = _here()
+        _pages(self.K, self.V, self.status_word, dev)
+        _raw_stream(stream, dev)
+
     def compact(self, stream=None):
         """Move owned pages into the lowest numbers; how many moved. Batches
         made before are void."""
+        self._usable(stream)
         src, dst = self.pager.compact()
         pages_copy(self.K, self.V, src, dst, stream)
         return len(src)
@@ -542,8 +549,7 @@ class PagedCache:
         if len(seqs) != len(counts) or not len(seqs) or len(set(seqs)) != len(seqs):
             raise ValueError("one count per sequence, each sequence once")
         counts = [_i32(n, "counts") for n in counts]
-        dev = _here()  # (another device's cache or stream is refused before anything changes)
-        _pages(self.K, self.V, self.status_word, dev), _raw_stream(stream, dev)
+        self._usable(stream)
         before = [self.pager.length(s) for s in seqs]
         src, dst = [], []
         try:
