@@ -405,6 +405,12 @@ def _token_rows(t, name, heads, d, dev):
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * d
 
 
+def _check_rows(rows, batch):
+    """Fewer rows than the batch has would be taken for the last tokens of their sequence."""
+    if rows.shape[0] < batch.tokens:
+        raise ValueError(f"a batch of {batch.tokens} tokens takes as many rows at least, not {rows.shape[0]}")
+
+
 def pages_append(K_pages, V_pages, layer, K, V, table, kv_len, q_start, status=None, stream=None):
     """Write new tokens into their pages (kvpool_pages_append). K_pages,
     V_pages: bf16 [layers, pages, kv_heads, page_tokens, d]; K, V: bf16
@@ -569,11 +575,13 @@ class PagedCache:
             raise
 
     def append(self, layer, K, V, batch, stream=None):
-        """Write the batch's new tokens: K, V bf16 [tokens, kv_heads, d]."""
+        """Write the batch's new tokens: K, V bf16 [tokens, kv_heads, d] (rows behind the batch's are padding)."""
+        _check_rows(K, batch)
         pages_append(self.K, self.V, layer, K, V, batch.table, batch.kv_len, batch.q_start, self.status_word, stream)
 
     def attend(self, layer, Q, batch, **options):
-        """pages_attend of the batch's new tokens over their sequences."""
+        """pages_attend of the batch's new tokens over their sequences (rows behind the batch's are padding)."""
+        _check_rows(Q, batch)
         return pages_attend(self.K, self.V, layer, Q, batch.table, batch.kv_len, batch.q_start, batch.max_q,
                             batch.max_kv, status=self.status_word, **options)
 
@@ -750,6 +758,7 @@ class KVPool:
 
         layer = _i32(layer, "layer")
         page_layer = layer if page_layer is None else _i32(page_layer, "page_layer")
+        _check_rows(Q, batch)
         n, hq, d = Q.shape
         dev = _here()
         pg = _pages(cache.K, cache.V, cache.status_word, dev)
