@@ -482,9 +482,10 @@ typedef struct {
  * <q, k_j>; cap > 0: x = cap * tanh(x / cap); slopes: x -= slopes[h] * |p - j|.
  * The row sees j when 0 <= j < kv_len[s], j >= first[row] (document mask: the
  * first token of the row's document) and (p - window < j <= p, or j <
- * prefix[s]: a prefix every row of the sequence sees, whole). Keys it does not
- * see may hold anything, infinities and NaN included. Zeroed: the causal mask
- * alone. */
+ * prefix[s]: a prefix that the sequence's rows see from both sides and past
+ * their windows). first holds for the prefix too: a row whose document begins
+ * behind the prefix sees none of it. Keys a row does not see may hold anything,
+ * infinities and NaN included. Zeroed: the causal mask alone. */
 typedef struct {
     float cap;             /* >= 0; 0: none; 3 softmax_scale / cap has to be finite */
     int window;            /* >= 0; 0: none; else the last `window` keys, the row's own among them */

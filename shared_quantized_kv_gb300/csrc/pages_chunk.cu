@@ -28,17 +28,17 @@
 // the CTA runs to its end without waiting again.
 //
 // Measured on 2,432 new tokens over 16K keys, 32 query heads on 8 KV heads of
-// 128 (two full waves of CTAs): 343 us, 1750 TFLOP/s. What got it there: one
+// 128 (two full waves of CTAs): 333 us, 1815 TFLOP/s. What got it there: one
 // issuer per slot, taking turns (a single one's waits and commits left the
 // tensor cores idle: 466 us; two without turns fell into step: 592 us);
 // operands of the MMAs in uniform registers (509 us before; not all of them
 // known to be uniform and no elected lane: 413 us); two threads per row (402 us
 // with one and the same issue, its P too late for its turn); P formed under the
 // reference as it is, the maxima looked at after it, and handed over in halves;
-// hardly a register spilled (the roles' registers shifted between the
-// warpgroups). Pages of 16 tokens are 32 boxes per pair of tiles: one loader
-// issues them in 1.4 times as long as the rest takes (470 us against 340 on
-// 2,048 tokens over 16K), two keep up.
+// no register spilled (the roles' registers shifted between the warpgroups; 128
+// bytes of spill loads cost 3 %). Pages of 16 tokens are 32 boxes per pair of tiles:
+// one loader issues them in 1.4 times as long as the rest takes (470 us against
+// 340 on 2,048 tokens over 16K when two were tried; now 325), two keep up.
 #include <algorithm>
 #include <mutex>
 
@@ -124,7 +124,7 @@ __device__ __forceinline__ uint32_t span_bits(int a, int b, int c) {
 
 // KIND: the causal mask alone; other masks too; scores that a cap or a bias by
 // distance changes (their costs are apart: 2,432 tokens over 16K keys take
-// 343 us, 417 with a window, 795 with a cap, 618 with a bias and 830 with both);
+// 333 us, 382 with a window, 793 with a cap, 610 with a bias and 827 with both);
 // the same with a cap so wide that each key takes a form of its own.
 enum { kPlain, kMasks, kScores, kWideScores };
 // STATE: the rows' states for a merge instead of the output; the weights then

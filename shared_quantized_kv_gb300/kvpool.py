@@ -457,7 +457,8 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
     a sequence where the caller knows them (they choose kernels, not results).
     Scores: cap (x = cap tanh(x / cap)), slopes float32 [q_heads] (minus slope
     times distance), window (the last keys up to the row's own), first int32
-    [tokens] (document mask), prefix int32 [seqs] (keys every row sees).
+    [tokens] (document mask: no key before it is seen, of a prefix neither),
+    prefix int32 [seqs] (keys that every row sees from first on).
     Returns out bf16 [tokens, q_heads, d], or (out, lse float32 [tokens,
     q_heads]) with return_lse or an lse to write to. A row that sees no key
     gets 0 and -inf; rows behind the last sequence are left as they are."""
