@@ -214,14 +214,13 @@ def _power_of_two(e):
 
 def _coded(x):
     """Codes and scales of vectors [..., d], step by step in 32 bits: the largest value brought into [1/2, 1), so that squares
-    stay in range; the butterflies of the transform; the squares summed in halves."""
+    stay in range; the butterflies of the transform; the squares summed in neighbouring pairs."""
     d = x.shape[-1]
     e = torch.frexp(x.abs().amax(-1, keepdim=True))[1].clamp_(-126, 126)
     y = x * _power_of_two(-e)
     sq = y * y
     while sq.shape[-1] > 1:
-        a, b = sq.chunk(2, -1)
-        sq = a + b
+        sq = sq[..., 0::2] + sq[..., 1::2]
     step = torch.tensor(STEP, dtype=torch.float32, device=x.device) * sq.sqrt()
     h = 1
     while h < d:
