@@ -451,8 +451,8 @@ typedef struct {
     int page_tokens;  /* 16, 32, 64 or 128 */
     int head_dim;     /* 64 or 128 */
     int32_t* status;  /* device word that the kernels OR error bits into (zeroed by the caller), or NULL:
-                         1 a page number out of range, or none for a token; 2 a bounded wait expired; see
-                         kvpool_pages_status */
+                         1 a page number out of range, or none for a token; 2 a bounded wait expired; 4 a
+                         position outside the rotation's tables; see kvpool_pages_status */
 } kvpool_pages_t;
 
 /* The sequences of one call. Sequence s holds kv_len[s] tokens, this call's
@@ -550,10 +550,98 @@ int kvpool_attend_pages(kvpool_t* pool, int pool_layer, const kvpool_pages_t* pa
 size_t kvpool_attend_pages_ws_bytes(const kvpool_t* pool, int tokens, int q_heads);
 
 /* Synchronise `stream`, then return and clear *pages->status: KVPOOL_OK,
- * KVPOOL_ERR_INVALID_ARG (a page number was out of range, or a sequence longer
- * than its table has room for) or KVPOOL_ERR_TIMEOUT. KVPOOL_ERR_INVALID_ARG
+ * KVPOOL_ERR_INVALID_ARG (a page number was out of range, a sequence longer
+ * than its table has room for, or a position outside the rotation's tables) or
+ * KVPOOL_ERR_TIMEOUT. KVPOOL_ERR_INVALID_ARG
  * too when status is NULL. */
 int kvpool_pages_status(const kvpool_pages_t* pages, void* stream);
+
+/* The rotation of Q and K by position. Of each head's channels the first dim
+ * turn in pairs: (i, i + dim / 2), or (2 i, 2 i + 1) where interleaved. Pair i
+ * (a, b) of a token becomes (a c - b s, b c + a s) with c and s its row's i-th
+ * cosine and sine, in float32. The token's row of the tables is at[its row of
+ * the call] where `at` is given, else offset + its position in its sequence (a
+ * sequence behind a shared context of that many tokens). */
+typedef struct {
+    const float* cos;  /* device [positions][dim / 2], 16-byte aligned */
+    const float* sin;
+    int positions;     /* >= 1 */
+    int dim;           /* a multiple of 16, at most head_dim */
+    int interleaved;
+    int offset;
+    const int32_t* at; /* device int32 [tokens], or NULL */
+} kvpool_rotary_t;
+
+/* kvpool_pages_append with the rotation on the way: K is turned, rounded to
+ * bf16 once and written, V written as it is. Q (or NULL, with Q_out NULL and
+ * q_heads 0): bf16 [tokens][q_heads][head_dim], q_stride elements from one
+ * token to the next, is turned into Q_out (q_out_stride; the same conditions);
+ * Q_out may be Q itself, with the same stride, and may overlap nothing else. A
+ * token whose row lies outside the tables is recorded in *status and nothing is
+ * written for it, its Q neither; a token that the page table has no page for is
+ * recorded, its Q is turned. Nothing is written for positions before 0 and for
+ * rows from q_start[seqs] on. */
+int kvpool_pages_append_rotary(const kvpool_pages_t* pages, int layer, const kvpool_seqs_t* seqs,
+                               const kvpool_rotary_t* rotary, const void* K, long long k_stride, const void* V,
+                               long long v_stride, const void* Q, long long q_stride, int q_heads, void* Q_out,
+                               long long q_out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged private caches in 4 bits: the same pages, sequences, pager and score
+ * modifiers, with K and V held at (head_dim / 2 + 4) bytes per head-vector
+ * instead of 2 head_dim. A head-vector x (K after its rotation) of d channels
+ * becomes y = H x, H the Walsh-Hadamard matrix in Sylvester's order, whose
+ * coordinates come near N(0, |x|^2). With step = 0.3352 |x| (the best uniform
+ * quantiser of 16 levels for a normal variable: J. Max, 1960) its codes are u_i
+ * = clamp(floor(y_i / step) + 8, 0, 15) and its scale t = step / d, and it
+ * stands for t H (u - 7.5). As V of the shared pool it is rotated so that large
+ * channels spread over all; here K is too. The codes' order of float32
+ * operations: x is scaled by the power of two that brings its largest value
+ * into [1/2, 1) (exponents clamped to +-126); squares are added in neighbouring
+ * pairs; y by the stages h = 1, 2, 4, ... (x_i + x_{i+h}, x_i - x_{i+h}); u from
+ * y_i * (1 / step). A vector that holds an infinity or NaN stands for NaN.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void* K;          /* uint8 [layers][pages][kv_heads][page_tokens][head_dim / 2], device, 16-byte aligned: 32-bit
+                         words of 8 channels, channel 2 k of them in bits 4 k ... 4 k + 3, channel 2 k + 1 sixteen
+                         bits above */
+    void* V;
+    float* K_scale;   /* float [layers][pages][kv_heads][page_tokens], device, 16-byte aligned */
+    float* V_scale;
+    int layers, pages, kv_heads;
+    int page_tokens;  /* 16, 32, 64 or 128 */
+    int head_dim;     /* 64 or 128 */
+    int32_t* status;  /* as kvpool_pages_t's */
+} kvpool_pages4_t;
+
+/* kvpool_pages_append_rotary into 4 bits; rotary NULL (then Q too): K as it is.
+ * K goes from float32 to its codes without a rounding to bf16 between. */
+int kvpool_pages4_append(const kvpool_pages4_t* pages, int layer, const kvpool_seqs_t* seqs,
+                         const kvpool_rotary_t* rotary, const void* K, long long k_stride, const void* V,
+                         long long v_stride, const void* Q, long long q_stride, int q_heads, void* Q_out,
+                         long long q_out_stride, void* stream);
+
+/* The sequences' last n tokens (n = q_start[s + 1] - q_start[s]; n = kv_len[s]:
+ * all) as the values they stand for: rows q_start[s] ... of K and V, bf16
+ * [tokens][kv_heads][head_dim], device, 16-byte aligned (t times the exact sum,
+ * rounded to float32 and then to bf16). Tokens without a page read as zeros and
+ * are recorded; rows of positions before 0 and rows from q_start[seqs] on are
+ * left as they are. */
+int kvpool_pages4_read(const kvpool_pages4_t* pages, int layer, const kvpool_seqs_t* seqs, void* K, void* V,
+                       void* stream);
+
+/* kvpool_pages_copy of codes and scales. */
+int kvpool_pages4_copy(const kvpool_pages4_t* pages, const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* kvpool_pages_attend over what the codes stand for (the same Q, bf16 and after
+ * its rotation, the same modifiers, outputs and errors): no dequantised copy is
+ * made, no workspace needed, nothing allocated. */
+int kvpool_pages4_attend(const kvpool_pages4_t* pages, int layer, const kvpool_seqs_t* seqs, const void* Q,
+                         long long q_stride, int q_heads, const kvpool_score_t* score, void* out, float* lse,
+                         float softmax_scale, void* stream);
+
+/* kvpool_pages_status of a 4-bit cache's word. */
+int kvpool_pages4_status(const kvpool_pages4_t* pages, void* stream);
 
 /* The pager: which pages each sequence owns. Host only, no device work: its
  * calls say which pages the caller has to copy (kvpool_pages_copy, on the

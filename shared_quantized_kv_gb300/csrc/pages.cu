@@ -7,7 +7,7 @@
 #include <new>
 #include <vector>
 
-#include "pages.cuh"
+#include "pages4.cuh"
 
 namespace kvp {
 namespace {
@@ -105,16 +105,28 @@ pages_copy_kernel(uint4* __restrict__ K, uint4* __restrict__ V, long long layer_
 }
 
 template <int NP>
-cudaError_t copy_some(const kvpool_pages_t& pg, const int32_t* src, const int32_t* dst, int n, cudaStream_t st) {
+cudaError_t copy_some(void* K, void* V, int layers, int pages, int pieces, const int32_t* src, const int32_t* dst, int n,
+                      cudaStream_t st) {
     CopyPairs<NP> pr;
     for (int i = 0; i < n; ++i) pr.src[i] = src[i], pr.dst[i] = dst[i];
-    const int pieces = pg.kv_heads * pg.page_tokens * pg.head_dim / 8;
-    pages_copy_kernel<NP><<<dim3((pieces + kCopyPiece - 1) / kCopyPiece, n, 2 * pg.layers), kCopyThreads, 0, st>>>(
-        static_cast<uint4*>(pg.K), static_cast<uint4*>(pg.V), (long long)pg.pages * pieces, pieces, pr);
+    pages_copy_kernel<NP><<<dim3((pieces + kCopyPiece - 1) / kCopyPiece, n, 2 * layers), kCopyThreads, 0, st>>>(
+        static_cast<uint4*>(K), static_cast<uint4*>(V), (long long)pages * pieces, pieces, pr);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t copy_pages(void* K, void* V, int layers, int pages, int pieces, const int32_t* src, const int32_t* dst, int n,
+                       cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < n && e == cudaSuccess;) {
+        const int m = std::min(n - i, n <= kCopyFew ? kCopyFew : kCopyMany);
+        e = m <= kCopyFew ? copy_some<kCopyFew>(K, V, layers, pages, pieces, src + i, dst + i, m, st)
+                          : copy_some<kCopyMany>(K, V, layers, pages, pieces, src + i, dst + i, m, st);
+        i += m;
+    }
+    return e;
+}
 
 cudaError_t launch_pages_append(const PagedSeqs& s, int head_dim, uint16_t* Kp, uint16_t* Vp, const void* K,
                                 long long k_stride, const void* V, long long v_stride, cudaStream_t st) {
@@ -194,6 +206,50 @@ kvp::PagedSeqs seqs_view(const kvpool_pages_t* pg, const kvpool_seqs_t* s) {
 }
 
 }  // namespace
+
+int kvp::check_pages_args(const kvpool_pages_t* pg, int layer) { return check_pages(pg, layer); }
+int kvp::check_seqs_args(const kvpool_seqs_t* s) { return check_seqs(s); }
+int kvp::check_sm103(int& sms) { return check_device(sms); }
+kvp::PagedSeqs kvp::paged_seqs_view(const kvpool_pages_t* pg, const kvpool_seqs_t* s) { return seqs_view(pg, s); }
+
+int kvp::check_copy_args(const kvpool_pages_t* pg, const int32_t* src, const int32_t* dst, int n) {
+    if (n < 0 || n > pg->pages || (n > 0 && (!src || !dst))) return KVPOOL_ERR_INVALID_ARG;
+    // every page at most once a destination, and then no source. Few pairs are
+    // compared with one another (the decode path: a fork or two); many are
+    // marked in a table of the pages.
+    for (int i = 0; i < n; ++i)
+        if (src[i] < 0 || src[i] >= pg->pages || dst[i] < 0 || dst[i] >= pg->pages) return KVPOOL_ERR_INVALID_ARG;
+    if (n <= 64) {
+        for (int i = 0; i < n; ++i)
+            for (int j = 0; j < n; ++j)
+                if (dst[i] == src[j] || (i != j && dst[i] == dst[j])) return KVPOOL_ERR_INVALID_ARG;
+    } else {
+        try {
+            std::vector<bool> is_dst(pg->pages, false);
+            for (int i = 0; i < n; ++i) {
+                if (is_dst[dst[i]]) return KVPOOL_ERR_INVALID_ARG;
+                is_dst[dst[i]] = true;
+            }
+            for (int i = 0; i < n; ++i)
+                if (is_dst[src[i]]) return KVPOOL_ERR_INVALID_ARG;
+        } catch (...) {
+            return KVPOOL_ERR_OOM;
+        }
+    }
+    return KVPOOL_OK;
+}
+
+int kvp::pages_status(int32_t* status, void* stream) {
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int32_t bits = 0;
+    cudaError_t e = cudaMemcpyAsync(&bits, status, sizeof(bits), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, sizeof(bits), st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
+    if (bits & kPgTimeout) return KVPOOL_ERR_TIMEOUT;
+    if (bits & (kPgBadPage | kPgBadPosition)) return KVPOOL_ERR_INVALID_ARG;
+    return KVPOOL_OK;
+}
 
 int kvp::paged_attend_args(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t* seqs, const void* Q,
                            long long q_stride, int q_heads, const kvpool_score_t* score, float softmax_scale,
@@ -282,45 +338,37 @@ int kvpool_pages_append(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t
                                              static_cast<cudaStream_t>(stream)));
 }
 
+int kvpool_pages_append_rotary(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t* seqs,
+                               const kvpool_rotary_t* rotary, const void* K, long long k_stride, const void* V,
+                               long long v_stride, const void* Q, long long q_stride, int q_heads, void* Q_out,
+                               long long q_out_stride, void* stream) {
+    int rc = check_pages(pg, layer);
+    if (rc) return rc;
+    kvp::AppendArgs a{};
+    rc = kvp::append_args(pg, seqs, rotary, K, k_stride, V, v_stride, Q, q_stride, q_heads, Q_out, q_out_stride, a);
+    if (rc) return rc;
+    if (!rotary) return KVPOOL_ERR_INVALID_ARG;
+    int sms = 0;
+    rc = check_device(sms);
+    if (rc) return rc;
+    const long long at = layer * layer_elems(pg);
+    a.Kp = static_cast<uint16_t*>(pg->K) + at;
+    a.Vp = static_cast<uint16_t*>(pg->V) + at;
+    return map_cuda(kvp::launch_append(a, pg->head_dim, false, static_cast<cudaStream_t>(stream)));
+}
+
 int kvpool_pages_copy(const kvpool_pages_t* pg, const int32_t* src, const int32_t* dst, int n, void* stream) {
     int rc = check_pages(pg, 0);
     if (rc) return rc;
-    if (n < 0 || n > pg->pages || (n > 0 && (!src || !dst))) return KVPOOL_ERR_INVALID_ARG;
-    // every page at most once a destination, and then no source. Few pairs are
-    // compared with one another (the decode path: a fork or two); many are
-    // marked in a table of the pages.
-    for (int i = 0; i < n; ++i)
-        if (src[i] < 0 || src[i] >= pg->pages || dst[i] < 0 || dst[i] >= pg->pages) return KVPOOL_ERR_INVALID_ARG;
-    if (n <= 64) {
-        for (int i = 0; i < n; ++i)
-            for (int j = 0; j < n; ++j)
-                if (dst[i] == src[j] || (i != j && dst[i] == dst[j])) return KVPOOL_ERR_INVALID_ARG;
-    } else {
-        try {
-            std::vector<bool> is_dst(pg->pages, false);
-            for (int i = 0; i < n; ++i) {
-                if (is_dst[dst[i]]) return KVPOOL_ERR_INVALID_ARG;
-                is_dst[dst[i]] = true;
-            }
-            for (int i = 0; i < n; ++i)
-                if (is_dst[src[i]]) return KVPOOL_ERR_INVALID_ARG;
-        } catch (...) {
-            return KVPOOL_ERR_OOM;
-        }
-    }
+    rc = kvp::check_copy_args(pg, src, dst, n);
+    if (rc) return rc;
     if (n == 0) return KVPOOL_OK;
     int sms = 0;
     rc = check_device(sms);
     if (rc) return rc;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; i < n && e == cudaSuccess;) {
-        const int m = std::min(n - i, n <= kvp::kCopyFew ? kvp::kCopyFew : kvp::kCopyMany);
-        e = m <= kvp::kCopyFew ? kvp::copy_some<kvp::kCopyFew>(*pg, src + i, dst + i, m, st)
-                               : kvp::copy_some<kvp::kCopyMany>(*pg, src + i, dst + i, m, st);
-        i += m;
-    }
-    return map_cuda(e);
+    return map_cuda(kvp::copy_pages(pg->K, pg->V, pg->layers, pg->pages,
+                                    pg->kv_heads * pg->page_tokens * pg->head_dim / 8, src, dst, n,
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 int kvpool_pages_attend(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t* seqs, const void* Q,
@@ -341,15 +389,7 @@ int kvpool_pages_attend(const kvpool_pages_t* pg, int layer, const kvpool_seqs_t
 
 int kvpool_pages_status(const kvpool_pages_t* pg, void* stream) {
     if (!pg || !pg->status || !aligned(pg->status, 4)) return KVPOOL_ERR_INVALID_ARG;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int32_t bits = 0;
-    cudaError_t e = cudaMemcpyAsync(&bits, pg->status, sizeof(bits), cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(pg->status, 0, sizeof(bits), st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return KVPOOL_ERR_CUDA;
-    if (bits & kvp::kPgTimeout) return KVPOOL_ERR_TIMEOUT;
-    if (bits & kvp::kPgBadPage) return KVPOOL_ERR_INVALID_ARG;
-    return KVPOOL_OK;
+    return kvp::pages_status(pg->status, stream);
 }
 
 }  // extern "C"

@@ -15,7 +15,7 @@ namespace kvp {
 constexpr int kPagedDevices = 64;  // devices of a process that the paged calls may run on
 
 // Bits of kvpool_pages_t.status.
-enum : int { kPgBadPage = 1, kPgTimeout = 2 };
+enum : int { kPgBadPage = 1, kPgTimeout = 2, kPgBadPosition = 4 };
 
 // The pages of one layer and the sequences of one call.
 struct PagedSeqs {

@@ -1,0 +1,608 @@
+// Attention of few query rows per sequence over its pages in 4 bits: decode
+// steps, draft tokens.
+//
+// Mathematics: a key stands for t H c with c = u - 7.5 of its codes, so that
+// <q, k> = t <H q, c>, and a row's sum of weighted values is H (sum p t' c'): the
+// rows are transformed once at the start, the sums once at the end, and between
+// them the matrix products see codes alone. One pass over the keys with a
+// running reference m per row, p = 2^(x - m), O and l rescaled when a score
+// passes m by more than 2^8. The weights p t' are rounded to bf16 (off by at
+// most 2^-8 of each, as the output's own rounding is of it), H q to fp16 after a
+// power of two has brought the row's largest value into [1/2, 1): off by at most 2^-11 of
+// each coordinate. Codes enter the products exactly: of Q K^T as fp16 1024 + u
+// or 1024 + 16 u (one mask and one constant; the constants' share is the
+// product's first summand, the sixteenth is in that channel's H q), of P V as
+// bf16 u - 8, the other half of a step times the sum of the weights, which one
+// more matrix row of ones adds up.
+//
+// Bound: memory, as a step reads D + 8 bytes per key and KV head; close behind
+// it the instructions that make operands of codes, so the layout serves these.
+// The keys are the matrix product's 16 rows and the query rows its 8 columns:
+// each code is taken apart once for up to 8 NR query rows, a lane's 16 bytes of
+// a key are its operands of all steps over the channels (they are summed, so
+// any order does), and the weights turn into the second product's operand by a
+// transpose of 8 x 8 registers. A CTA has up to 8 NR rows (new tokens x heads of
+// a group) of one sequence and KV head; its 4 warps take units of 32 keys in
+// turn, each through a ring of its own in shared memory, filled by 16-byte
+// asynchronous copies that nothing but the warp itself waits for. The warps'
+// states meet in shared memory at the end, those of a cluster's CTAs, which
+// split the keys, in distributed shared memory: no workspace, no second launch.
+#include <algorithm>
+#include <mutex>
+
+#include "pages4.cuh"
+
+namespace kvp {
+namespace {
+
+using pages::Seen;
+
+constexpr int kWarps = 4;
+constexpr int kUnit = 32;   // keys per unit
+constexpr int kStages = 3;  // units in a warp's ring
+constexpr float kLazyMax = 8.0f;
+constexpr int kMaxSplit = 16;
+// CTAs per SM, by their registers: 8, 16 and 32 rows
+constexpr int ctas_per_sm(int NR) { return NR == 1 ? 4 : NR == 2 ? 3 : 2; }
+
+template <int D, int NR>
+struct Lay {
+    static constexpr int codes = kUnit * D / 2;              // bytes of a unit's K or V
+    static constexpr int stage = 2 * codes + 2 * kUnit * 4;  // K, V, their scales
+    static constexpr int ring = kWarps * kStages * stage;
+    static constexpr int rs = D + 4;                         // floats of a merge row: O, m, l
+    static constexpr int rows = 8 * NR;
+    // the merge reuses the rings: per warp `rows` rows, then the CTA's merged ones
+    static constexpr int merge = (kWarps + 1) * rows * rs * 4;
+    static constexpr int q = rows * (D * 2 + 16);            // H q, at the start; then 2 floats per row
+    static constexpr int total = (ring > merge ? ring : merge) > q ? (ring > merge ? ring : merge) : q;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// c += A (16 keys x 16 channels) B (16 channels x 8 rows)
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the 8 x 8 matrix of 16-bit values that the warp's registers hold, transposed
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// (x & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t mask_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+    return y;
+}
+// codes in bits 0-3 of both halves -> bf16 u - 8, exactly
+__device__ __forceinline__ uint32_t centred(uint32_t x) {
+    const uint32_t y = mask_or(x, 0x000F000Fu, 0x43004300u);  // 128 + u
+    uint32_t z;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0xC308C308u));  // - 136
+    return z;
+}
+
+// Butterflies of the transform over a row that lies in 4 consecutive channels
+// per lane, D / 4 lanes.
+template <int D>
+__device__ __forceinline__ void transform4(float4& a) {
+    const float s = a.x + a.y, d = a.x - a.y, u = a.z + a.w, v = a.z - a.w;
+    a = make_float4(s + u, d + v, s - u, d - v);
+#pragma unroll
+    for (int o = 1; o < D / 4; o <<= 1) {
+        const float g = threadIdx.x & o ? -1.0f : 1.0f;
+        a.x = fmaf(g, a.x, __shfl_xor_sync(0xffffffffu, a.x, o));
+        a.y = fmaf(g, a.y, __shfl_xor_sync(0xffffffffu, a.y, o));
+        a.z = fmaf(g, a.z, __shfl_xor_sync(0xffffffffu, a.z, o));
+        a.w = fmaf(g, a.w, __shfl_xor_sync(0xffffffffu, a.w, o));
+    }
+}
+
+// NR: blocks of 8 query rows. SCORED: score modifiers apply. DIRECT: every
+// sequence has one block (no search; if it has more, the CTA takes them in
+// turn). Grid: blocks x the CTAs of a cluster, KV heads.
+template <int D, int NR, bool SCORED, bool DIRECT>
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NR))
+pages4_rows_kernel(const PagedAttend4 p4) {
+    using L = Lay<D, NR>;
+    constexpr int kRows = L::rows;
+    constexpr int KS = D / 16;   // steps of Q K^T over the channels
+    constexpr int MB = D / 16;   // blocks of 16 channels of P V
+    constexpr int W = D / 32;    // words of a key per lane in Q K^T
+    constexpr int RS = L::rs;
+    const PagedAttend& p = p4.a;
+    extern __shared__ __align__(128) unsigned char sm[];
+    const PagedSeqs& s = p.s;
+    const int S = (int)ptx::cluster_size(), rank = (int)ptx::cluster_rank();
+    const int g = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+    const int quad = lane >> 2, qi = lane & 3;
+
+    pages::RowBlock b;
+    if constexpr (DIRECT) {
+        b.seq = blockIdx.x / S;
+        b.blk = 0;
+        b.q0 = pages::row_begin(s, b.seq);
+        b.n = max(pages::row_begin(s, b.seq + 1) - b.q0, 0);
+        const int len = pages::length_of(s, b.seq);
+        b.p0 = len - b.n;
+        b.T = pages::held_tokens(s, len);
+        if (b.n == 0) return;  // the whole cluster's
+        if (len > b.T && tid == 0) pages::flag(s.status, kPgBadPage);
+    } else {
+        if (!pages::find_block(s, p.G, kRows, blockIdx.x / S, b)) return;
+    }
+    const int T = b.T;
+    const int32_t* table = s.table + (long long)b.seq * s.tstride;
+
+    for (;; ++b.blk) {
+        const int r_begin = b.blk * kRows;
+        const int nr = min(kRows, b.n * p.G - r_begin);
+        auto token_of = [&](int r) { return (r_begin + r) / p.G; };
+        auto head_of = [&](int r) { return g * p.G + (r_begin + r) % p.G; };
+
+        // H q of the block's rows in fp16 (rows past it repeat its last), the constants' share and the power of two
+        unsigned char* qs = sm;
+        constexpr int kQRow = D * 2 + 16;
+        for (int r = warp; r < kRows; r += kWarps) {
+            const int rr = min(r, nr - 1);
+            const uint16_t* src = p.Q + (long long)(b.q0 + token_of(rr)) * p.q_stride + (long long)head_of(rr) * D;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane < D / 4) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+                x = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                                __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+            }
+            uint32_t top = max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
+                               max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w))));
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int e = min(max((int)(top >> 23) - 126, -126), 126);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            x.x *= down, x.y *= down, x.z *= down, x.w *= down;
+            transform4<D>(x);
+            // channels 4 l + 2 and + 3 meet 16 u
+            const __half2 lo = __floats2half2_rn(x.x, x.y), hi = __floats2half2_rn(x.z * 0.0625f, x.w * 0.0625f);
+            const float2 fl = __half22float2(lo), fh = __half22float2(hi);
+            float off = lane < D / 4 ? fmaf(fl.x + fl.y, 1031.5f, (fh.x + fh.y) * 1144.0f) : 0.0f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) off += __shfl_xor_sync(0xffffffffu, off, o);
+            if (lane < D / 4)
+                *reinterpret_cast<uint2*>(qs + r * kQRow + lane * 8) = make_uint2(
+                    *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            if (lane == 0)
+                *reinterpret_cast<float2*>(qs + r * kQRow + D * 2) =
+                    make_float2(off, __uint_as_float((uint32_t)(127 + e) << 23));
+        }
+        __syncthreads();
+        // operands: row 8 n + quad, channels 32 qi ... (D = 64: 16 qi ...), two registers per step
+        uint32_t qf[NR][KS][2];
+        float off[NR][2], mul[NR][2];  // of this lane's rows 8 n + 2 qi + h
+        Seen see[NR][2];
+        int pos[NR][2];
+        float slope2[NR][2];
+        int lo = INT_MAX, hi = 0, pre_end = 0, win_lo = INT_MAX;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const uint2* src = reinterpret_cast<const uint2*>(qs + (8 * n + quad) * kQRow + qi * (D / 2));
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const uint2 v = src[k];
+                qf[n][k][0] = v.x, qf[n][k][1] = v.y;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 8 * n + 2 * qi + h, rr = min(r, nr - 1);
+                const float2 c = *reinterpret_cast<const float2*>(qs + r * kQRow + D * 2);
+                off[n][h] = -c.x;
+                mul[n][h] = c.y * (SCORED ? 1.0f : p.scale_log2);
+                const int i = token_of(rr);
+                pos[n][h] = b.p0 + i;
+                see[n][h] = pages::row_seen<SCORED>(p, b.seq, b.q0 + i, pos[n][h], T);
+                slope2[n][h] = SCORED && p.slopes ? __ldg(p.slopes + head_of(rr)) * 1.4426950408889634f : 0.0f;
+                lo = min(lo, see[n][h].lo());
+                hi = max(hi, see[n][h].hi());
+                pre_end = max(pre_end, see[n][h].prefix_end());
+                win_lo = min(win_lo, see[n][h].window_lo());
+            }
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        pages::Gap gap;
+        if (SCORED && p.prefix && p.window > 0)
+            gap = pages::Gap(__reduce_max_sync(0xffffffffu, pre_end), __reduce_min_sync(0xffffffffu, win_lo), kUnit);
+        __syncthreads();  // every warp has its operands: the rings may be filled
+
+        // keys that any row of the block sees, in units; the cluster's CTAs take
+        // consecutive shares of them, the warps of a CTA every fourth unit
+        const int u_lo = hi > 0 ? lo / kUnit : 0, u_hi = gap.count((hi + kUnit - 1) / kUnit);
+        const int per = (u_hi - u_lo + S - 1) / S;
+        const int ua = u_lo + rank * per, ub = min(u_hi, ua + per);
+        const int nu = ub - ua > warp ? (ub - ua - warp + kWarps - 1) / kWarps : 0;  // this warp's units
+
+        const uint32_t ring = ptx::smem_u32(sm) + warp * (kStages * L::stage);
+        // the pages of this warp's next 16 units, one per lane for 16 keys each
+        auto pages_at = [&](int k) {
+            const int i = k + (lane >> 1), t = gap.number(ua + warp + i * kWarps) * kUnit + 16 * (lane & 1);
+            return i < nu && t < T ? __ldg(table + (t >> s.pshift)) : 0;
+        };
+        int pg_now = pages_at(0), pg_next = 0;
+        // where this lane's 16-byte pieces go: within a 128-byte line, pieces are
+        // exchanged by the line's number, so that neither product's reads collide
+        constexpr int kLineRows = 256 / D;  // keys per line
+        auto swizzled = [](int line) { return D == 128 ? 2 * (line & 3) : 2 * (line & 1); };
+        auto load_unit = [&](int k) {
+            if ((k & 15) == 0) {
+                if (k > 0) pg_now = pg_next;
+                pg_next = pages_at(k + 16);
+            }
+            if (k < nu) {
+                const int t0 = gap.number(ua + warp + k * kWarps) * kUnit;
+                const uint32_t dst = ring + (k % kStages) * L::stage;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int page = __shfl_sync(0xffffffffu, pg_now, (k & 15) * 2 + h), t = t0 + 16 * h;
+                    const bool ok = page >= 0 && page < s.pages;
+                    if (!ok && lane == 0) pages::flag(s.status, kPgBadPage);
+                    const long long vec =
+                        ((((long long)(ok ? page : 0) * s.Hk + g) << s.pshift) + (t & ((1 << s.pshift) - 1)));
+                    const unsigned char* kc = reinterpret_cast<const unsigned char*>(p.K) + vec * (D / 2);
+                    const unsigned char* vc = reinterpret_cast<const unsigned char*>(p.V) + vec * (D / 2);
+                    constexpr int kPieces = 16 * D / 32;  // of 16 keys
+#pragma unroll
+                    for (int it = 0; it < kPieces / 32; ++it) {
+                        const int i = it * 32 + lane, line = h * (kPieces / 8) + i / 8;
+                        const bool real = ok && t + i / (D / 32) < T;
+                        const uint32_t to = dst + line * 128 + (((i & 7) ^ swizzled(line)) << 4);
+                        cp_async16(to, kc + i * 16, real ? 16 : 0);
+                        cp_async16(to + L::codes, vc + i * 16, real ? 16 : 0);
+                    }
+                    // scales: four keys to a piece
+                    if (lane < 8) {
+                        const int i = lane & 3;
+                        const float* from = (lane < 4 ? p4.Kt : p4.Vt) + vec + 4 * i;
+                        const uint32_t to = dst + 2 * L::codes + (lane >> 2) * (kUnit * 4) + h * 64 + i * 16;
+                        cp_async16(to, from, ok ? min(max(T - t - 4 * i, 0), 4) * 4 : 0);
+                    }
+                }
+            }
+            cp_commit();  // an empty group past the last unit keeps the count
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) load_unit(k);
+
+        float O[NR][MB][4], sumw[NR][4];
+        float m[NR][2], l[NR][2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sumw[n][e] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < MB; ++k) O[n][k][e] = 0.0f;
+            }
+            m[n][0] = m[n][1] = -CUDART_INF_F;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+
+        for (int k = 0; k < nu; ++k) {
+            load_unit(k + kStages - 1);
+            cp_wait<kStages - 1>();
+            __syncwarp();
+            const unsigned char* st = sm + warp * (kStages * L::stage) + (k % kStages) * L::stage;
+            const int t0 = gap.number(ua + warp + k * kWarps) * kUnit;
+            const float* kt = reinterpret_cast<const float*>(st + 2 * L::codes);
+            const float* vt = kt + kUnit;
+            // ---- scores: c[n][i][e]: key t0 + 16 i + quad (+ 8 for e >= 2), row 8 n + 2 qi + (e & 1)
+            float c[NR][2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[n][i][e] = off[n][e & 1];
+                uint32_t w[2][W];  // keys quad and quad + 8
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 16 * i + 8 * h + quad, line = row / kLineRows;
+                    const int piece = (row % kLineRows) * (D / 32) + (D == 128 ? qi : qi >> 1);
+                    const unsigned char* at = st + line * 128 + ((piece ^ swizzled(line)) << 4);
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(at);
+                        w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(at + (qi & 1) * 8);
+                        w[h][0] = v.x, w[h][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const uint32_t x = w[0][j], y = w[1][j], x8 = x >> 8, y8 = y >> 8;
+                    const uint32_t xa = mask_or(x, 0x000F000Fu, 0x64006400u), xb = mask_or(x, 0x00F000F0u, 0x64006400u);
+                    const uint32_t ya = mask_or(y, 0x000F000Fu, 0x64006400u), yb = mask_or(y, 0x00F000F0u, 0x64006400u);
+                    const uint32_t xc = mask_or(x8, 0x000F000Fu, 0x64006400u), xd = mask_or(x8, 0x00F000F0u, 0x64006400u);
+                    const uint32_t yc = mask_or(y8, 0x000F000Fu, 0x64006400u), yd = mask_or(y8, 0x00F000F0u, 0x64006400u);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        mma_f16(c[n][i], xa, ya, xb, yb, qf[n][2 * j][0], qf[n][2 * j][1]);
+                        mma_f16(c[n][i], xc, yc, xd, yd, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
+                    }
+                }
+            }
+            // ---- weights
+            float tk[4], tv[4];  // keys t0 + quad + 8 i
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tk[i] = kt[quad + 8 * i], tv[i] = vt[quad + 8 * i];
+            bool all = true;
+#pragma unroll
+            for (int n = 0; n < NR; ++n) all = all && see[n][0].all(t0, t0 + kUnit) && see[n][1].all(t0, t0 + kUnit);
+            const bool whole = __all_sync(0xffffffffu, all);
+            bool move = false;
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int h = e & 1, kk = 2 * i + (e >> 1), j = t0 + quad + 8 * kk;
+                        float x = c[n][i][e] * mul[n][h] * tk[kk];
+                        if constexpr (SCORED) x = pages::score<SCORED>(p, x, slope2[n][h], pos[n][h], j);
+                        if (!whole && !see[n][h].has(j)) x = -CUDART_INF_F;
+                        c[n][i][e] = x;
+                        mx[h] = fmaxf(mx[h], x);
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    move = move || mx[h] > m[n][h] + kLazyMax || (m[n][h] == -CUDART_INF_F && mx[h] > m[n][h]);
+            }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float mx = fmaxf(fmaxf(fmaxf(c[n][0][h], c[n][0][2 + h]), fmaxf(c[n][1][h], c[n][1][2 + h])), m[n][h]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        // (nothing summed yet: sums of 0, or NaN, which stays)
+                        const float al = m[n][h] == -CUDART_INF_F ? 1.0f : ptx::ex2(m[n][h] - mx);
+                        l[n][h] *= al;
+                        sumw[n][h] *= al, sumw[n][2 + h] *= al;
+#pragma unroll
+                        for (int q = 0; q < MB; ++q) O[n][q][h] *= al, O[n][q][2 + h] *= al;
+                        m[n][h] = mx;
+                    }
+            }
+            uint32_t pb[NR][2][2];  // operands of P V: keys of 16 i, in two eights
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const float ref[2] = {m[n][0] == -CUDART_INF_F ? 0.0f : m[n][0], m[n][1] == -CUDART_INF_F ? 0.0f : m[n][1]};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float t = tv[2 * i + (e >> 1)];
+                        const float w0 = ptx::ex2(c[n][i][e] - ref[0]), w1 = ptx::ex2(c[n][i][e + 1] - ref[1]);
+                        l[n][0] += w0, l[n][1] += w1;
+                        float v0 = w0 * t, v1 = w1 * t;
+                        if (!whole) {  // what a masked place's scale holds has no say
+                            v0 = w0 == 0.0f ? 0.0f : v0;
+                            v1 = w1 == 0.0f ? 0.0f : v1;
+                        }
+                        pb[n][i][e >> 1] = transposed(pack_bf2(v0, v1));
+                    }
+            }
+            // ---- O += P V; lane: channels of the D / 8 from quad on, keys 2 qi, 2 qi + 1 of each eight
+            const unsigned char* sv = st + L::codes;
+            constexpr int VW = D / 64;  // words of a key per lane
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t w[4][VW];  // keys 2 qi, 2 qi + 1, 8 more, one more
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int row = 16 * i + 2 * qi + (y & 1) + 8 * (y >> 1), line = row / kLineRows;
+                    const int piece = (row % kLineRows) * (D / 32) + (D == 128 ? quad >> 1 : quad >> 2);
+                    const unsigned char* at = sv + line * 128 + ((piece ^ swizzled(line)) << 4);
+                    if constexpr (D == 128) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(at + (quad & 1) * 8);
+                        w[y][0] = v.x, w[y][1] = v.y;
+                    } else {
+                        w[y][0] = *reinterpret_cast<const uint32_t*>(at + (quad & 3) * 4);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mma_bf16(sumw[n], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, pb[n][i][0], pb[n][i][1]);
+#pragma unroll
+                for (int j = 0; j < VW; ++j) {
+                    // even channels of both keys, odd ones; of the first eight keys, of the second
+                    uint32_t ev0 = ptx::prmt(w[0][j], w[1][j], 0x5410), od0 = ptx::prmt(w[0][j], w[1][j], 0x7632);
+                    uint32_t ev1 = ptx::prmt(w[2][j], w[3][j], 0x5410), od1 = ptx::prmt(w[2][j], w[3][j], 0x7632);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t a0 = centred(ev0), a1 = centred(od0), a2 = centred(ev1), a3 = centred(od1);
+                        ev0 >>= 4, od0 >>= 4, ev1 >>= 4, od1 >>= 4;
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma_bf16(O[n][4 * j + q], a0, a1, a2, a3, pb[n][i][0], pb[n][i][1]);
+                    }
+                }
+            }
+            __syncwarp();  // every lane has read the stage
+        }
+        cp_wait<0>();
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[n][h] += __shfl_xor_sync(0xffffffffu, l[n][h], o);
+        __syncthreads();  // every warp is done with its ring
+
+        // the warps' rows: O, then (m, l) with m = -inf where nothing was summed
+        float* rows = reinterpret_cast<float*>(sm) + warp * (kRows * RS);
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float* dst = rows + (8 * n + 2 * qi + h) * RS;
+                const float half = 0.5f * sumw[n][h];
+#pragma unroll
+                for (int q = 0; q < MB; ++q)
+                    *reinterpret_cast<float2*>(dst + quad * (D / 8) + 2 * q) = make_float2(O[n][q][h] + half, O[n][q][2 + h] + half);
+                if (quad == 0) {
+                    dst[D] = l[n][h] == 0.0f ? -CUDART_INF_F : (m[n][h] == -CUDART_INF_F ? 0.0f : m[n][h]);
+                    dst[D + 1] = l[n][h];
+                }
+            }
+        __syncthreads();
+
+        // merge: 4 channels per item, whole warps (the transform crosses lanes)
+        constexpr int C4 = D / 4;
+        auto finish = [&](bool live, int r, int c4, float M, float Lt, float4 a) {
+            transform4<D>(a);
+            if (!live) return;
+            const long long row = (long long)(b.q0 + token_of(r)) * p.Hq + head_of(r);
+            const float inv = Lt == 0.0f ? 0.0f : 1.0f / Lt;
+            *reinterpret_cast<uint2*>(p.out + row * D + c4 * 4) =
+                Lt == 0.0f ? make_uint2(0u, 0u)
+                           : make_uint2(pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv));
+            if (c4 == 0 && p.lse) p.lse[row] = Lt == 0.0f ? -CUDART_INF_F : (M + log2f(Lt)) * 0.6931471805599453f;
+        };
+        float* merged = reinterpret_cast<float*>(sm) + kWarps * (kRows * RS);
+        for (int it0 = 0; it0 < nr * C4; it0 += kWarps * 32) {
+            const int it = it0 + tid, r = min(it / C4, nr - 1), c4 = it % C4;
+            const bool live = it < nr * C4;
+            const float* src = reinterpret_cast<const float*>(sm) + r * RS;
+            float M = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, src[w * (kRows * RS) + D]);
+            float Lt = 0.0f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float* x = src + w * (kRows * RS);
+                const float lw = x[D + 1];
+                const float f = lw == 0.0f ? 0.0f : ptx::ex2(x[D] - M);
+                const float4 v = *reinterpret_cast<const float4*>(x + c4 * 4);
+                Lt = fmaf(f, lw, Lt);
+                a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+            }
+            if (S == 1) {
+                finish(live, r, c4, M, Lt, a);
+            } else if (live) {
+                *reinterpret_cast<float4*>(merged + r * RS + c4 * 4) = a;
+                if (c4 == 0) merged[r * RS + D] = M, merged[r * RS + D + 1] = Lt;
+            }
+        }
+        if (S > 1) {
+            ptx::cluster_arrive();
+            ptx::cluster_wait();
+            for (int it0 = rank * (kWarps * 32); it0 < nr * C4; it0 += S * kWarps * 32) {
+                const int it = it0 + tid, r = min(it / C4, nr - 1), c4 = it % C4;
+                float M = -CUDART_INF_F;
+                for (int k = 0; k < S; ++k) M = fmaxf(M, ptx::ld_dsmem(ptx::dsmem_addr(merged + r * RS + D, k)));
+                float Lt = 0.0f;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < S; ++k) {
+                    const float2 ml = ptx::ld_dsmem2(ptx::dsmem_addr(merged + r * RS + D, k));
+                    const float4 v = ptx::ld_dsmem4(ptx::dsmem_addr(merged + r * RS + c4 * 4, k));
+                    const float f = ml.y == 0.0f ? 0.0f : ptx::ex2(ml.x - M);
+                    Lt = fmaf(f, ml.y, Lt);
+                    a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+                }
+                finish(it < nr * C4, r, c4, M, Lt, a);
+            }
+            // no CTA goes on (or away) while another reads its rows
+            ptx::cluster_arrive();
+            ptx::cluster_wait();
+        }
+        if (!DIRECT || (b.blk + 1) * kRows >= b.n * p.G) break;
+        __syncthreads();
+    }
+}
+
+template <int D, int NR, bool SCORED, bool DIRECT>
+cudaError_t launch(const PagedAttend4& a, int split, long long blocks, cudaStream_t st) {
+    auto kern = pages4_rows_kernel<D, NR, SCORED, DIRECT>;
+    constexpr int smem = Lay<D, NR>::total;
+    // opted in once per instance and device
+    static std::once_flag once[kPagedDevices];
+    static cudaError_t opt[kPagedDevices];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device >= kPagedDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[device], [&] {
+        opt[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (opt[device] == cudaSuccess)
+            opt[device] = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (opt[device] != cudaSuccess) return opt[device];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(split * blocks), a.a.s.Hk, 1);
+    cfg.blockDim = dim3(kWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int D, int NR>
+cudaError_t launch_rows(const PagedAttend4& p, int max_q, int max_kv, int sm_count, cudaStream_t st) {
+    const PagedAttend& a = p.a;
+    constexpr int kRows = 8 * NR;
+    const bool direct = (long long)max_q * a.G <= kRows;
+    const long long blocks = direct ? a.s.seqs : (long long)a.s.tokens * a.G / kRows + a.s.seqs;
+    // keys split over a cluster as far as all CTAs still run at once and every warp keeps two units
+    const long long jobs = std::min(blocks, a.s.seqs * (((long long)max_q * a.G + kRows - 1) / kRows)) * a.s.Hk;
+    long long split = std::min<long long>((long long)ctas_per_sm(NR) * sm_count / std::max(1LL, jobs),
+                                          max_kv / (2 * kWarps * kUnit));
+    split = std::max<long long>(1, std::min<long long>(split, kMaxSplit));
+    if (split * blocks > INT_MAX) return cudaErrorInvalidValue;
+    if (paged_scored(a))
+        return direct ? launch<D, NR, true, true>(p, (int)split, blocks, st)
+                      : launch<D, NR, true, false>(p, (int)split, blocks, st);
+    return direct ? launch<D, NR, false, true>(p, (int)split, blocks, st)
+                  : launch<D, NR, false, false>(p, (int)split, blocks, st);
+}
+
+}  // namespace
+
+cudaError_t launch_pages4_rows(const PagedAttend4& a, int head_dim, int max_q, int max_kv, int sm_count,
+                               cudaStream_t st) {
+    const long long rows = (long long)max_q * a.a.G;
+#define KVP_PG4_ROWS(DD)                                                         \
+    (rows <= 8    ? launch_rows<DD, 1>(a, max_q, max_kv, sm_count, st)  \
+     : rows <= 16 ? launch_rows<DD, 2>(a, max_q, max_kv, sm_count, st)  \
+                  : launch_rows<DD, 4>(a, max_q, max_kv, sm_count, st))
+    return head_dim == 64 ? KVP_PG4_ROWS(64) : KVP_PG4_ROWS(128);
+#undef KVP_PG4_ROWS
+}
+
+}  // namespace kvp

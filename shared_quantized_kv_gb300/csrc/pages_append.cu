@@ -1,0 +1,360 @@
+// New tokens on their way into the pages: K and Q turned by their positions,
+// and K and V written as bf16 or in 4 bits; and the way back, tokens of the
+// 4-bit pages as bf16.
+//
+// Mathematics. Rotation: a pair (a, b) of channels becomes (a c - b s, b c + a s),
+// two float32 products and their sum, each rounded once (no FMA: the same
+// numbers whoever adds them up), then one rounding to bf16 or none before the
+// codes. Codes: y = H x, step = 0.3352 |x|, u = clamp(floor(y / step) + 8, 0, 15),
+// t = step / D; x is first scaled by a power of two that brings its largest
+// value into [1/2, 1), so that neither squares nor sums overflow.
+//
+// Bound: memory, each byte once. A block takes one token; D / 16 lanes take a
+// head-vector, each lane two pieces of 8 channels that lie D / 2 apart: the
+// pairs (i, i + D / 2) are then in one lane, a lane's angles serve all heads, and
+// of the transform's log2 D stages four stay in registers.
+#include "pages4.cuh"
+
+namespace kvp {
+namespace {
+
+constexpr int kAppThreads = 128;
+
+// How a call's rotation meets a lane's channels: none; pairs (i, i + D / 2), both
+// in the lane; pairs elsewhere or fewer channels.
+enum { kNoTurn, kWhole, kPart };
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    auto two = [](float lo, float hi) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    };
+    return make_uint4(two(x[0], x[1]), two(x[2], x[3]), two(x[4], x[5]), two(x[6], x[7]));
+}
+// a c - b s and b c + a s
+__device__ __forceinline__ float turn_a(float a, float b, float c, float s) {
+    return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+}
+__device__ __forceinline__ float turn_b(float a, float b, float c, float s) {
+    return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+}
+
+// The angles of one piece of 8 channels, p-th of its head: eight for pairs of
+// which the piece has one end (the other `reach` pieces on, or back), four for
+// neighbouring pairs.
+struct Angles {
+    float c[8], s[8];
+    int reach;  // 0: the piece does not turn, or pairs are neighbours
+    bool turns;
+    __device__ __forceinline__ void load(const Rotary& r, int at, int p) {
+        turns = 8 * p < 2 * r.half;
+        reach = 0;
+        if (!turns) return;
+        const long long row = (long long)at * r.half;
+        int i = 4 * p;
+        if (!r.interleaved) {
+            const int n = r.half / 8;
+            reach = p < n ? n : -n;
+            i = 8 * (p < n ? p : p - n);
+        }
+        const float4 *c4 = reinterpret_cast<const float4*>(r.cos + row + i), *s4 = reinterpret_cast<const float4*>(r.sin + row + i);
+        *reinterpret_cast<float4*>(c) = __ldg(c4);
+        *reinterpret_cast<float4*>(s) = __ldg(s4);
+        if (!r.interleaved) {
+            *reinterpret_cast<float4*>(c + 4) = __ldg(c4 + 1);
+            *reinterpret_cast<float4*>(s + 4) = __ldg(s4 + 1);
+        }
+    }
+    // src: the piece in memory
+    __device__ __forceinline__ void turn(float (&x)[8], const uint4* src) const {
+        if (!turns) return;
+        if (reach == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = turn_a(a, b, c[i], s[i]);
+                x[2 * i + 1] = turn_b(a, b, c[i], s[i]);
+            }
+        } else {
+            float y[8];
+            unpack8(src[reach], y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = reach > 0 ? turn_a(x[i], y[i], c[i], s[i]) : turn_b(y[i], x[i], c[i], s[i]);
+        }
+    }
+};
+
+// Codes of a head-vector spread over its L lanes, which all come here with all
+// lanes of the warp: words j and j + L, and the scale.
+template <int L>
+__device__ __forceinline__ void encode(float (&x0)[8], float (&x1)[8], uint32_t& w0, uint32_t& w1, float& t) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, max(__float_as_uint(fabsf(x0[i])), __float_as_uint(fabsf(x1[i]))));
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+    const int e = min(max((int)(top >> 23) - 126, -126), 126);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    float q0[8], q1[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x0[i] = __fmul_rn(x0[i], down), x1[i] = __fmul_rn(x1[i], down);
+        q0[i] = __fmul_rn(x0[i], x0[i]), q1[i] = __fmul_rn(x1[i], x1[i]);
+    }
+    // squares in neighbouring pairs: within the pieces, over the lanes, over the halves
+#pragma unroll
+    for (int n = 4; n; n >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; ++i) q0[i] = __fadd_rn(q0[2 * i], q0[2 * i + 1]), q1[i] = __fadd_rn(q1[2 * i], q1[2 * i + 1]);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+        q0[0] = __fadd_rn(q0[0], __shfl_xor_sync(kAll, q0[0], o));
+        q1[0] = __fadd_rn(q1[0], __shfl_xor_sync(kAll, q1[0], o));
+    }
+    const float step = __fmul_rn(kStep4, __fsqrt_rn(__fadd_rn(q0[0], q1[0])));
+    // the transform: stages 1, 2, 4 in the pieces, then over the lanes, then over the halves
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & h)) {
+                float a = x0[i], b = x0[i + h];
+                x0[i] = __fadd_rn(a, b), x0[i + h] = __fsub_rn(a, b);
+                a = x1[i], b = x1[i + h];
+                x1[i] = __fadd_rn(a, b), x1[i + h] = __fsub_rn(a, b);
+            }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = __shfl_xor_sync(kAll, x0[i], o), b = __shfl_xor_sync(kAll, x1[i], o);
+            x0[i] = upper ? __fsub_rn(a, x0[i]) : __fadd_rn(a, x0[i]);
+            x1[i] = upper ? __fsub_rn(b, x1[i]) : __fadd_rn(b, x1[i]);
+        }
+    }
+    const float inv = __fdiv_rn(1.0f, step);
+    w0 = w1 = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = __fadd_rn(x0[i], x1[i]), b = __fsub_rn(x0[i], x1[i]);
+        const int u0 = min(max(__float2int_rd(__fmul_rn(a, inv)), -8), 7) + 8;
+        const int u1 = min(max(__float2int_rd(__fmul_rn(b, inv)), -8), 7) + 8;
+        w0 |= (uint32_t)u0 << (2 * (i & 6) + 16 * (i & 1));
+        w1 |= (uint32_t)u1 << (2 * (i & 6) + 16 * (i & 1));
+    }
+    if (!(step > 0.0f)) w0 = w1 = 0x88888888u;
+    // a vector that holds an infinity or NaN stands for NaN
+    t = top >= 0x7F800000u ? CUDART_NAN_F
+                           : __fmul_rn(__fmul_rn(step, __uint_as_float((uint32_t)(127 + e) << 23)), 1.0f / (16 * L));
+}
+
+// The token row `tok`: its sequence, position and, where the table has a page
+// for it, the index of its first head's vector in the layer (-1 where not).
+// False: a row behind the last sequence, or a position before 0.
+__device__ __forceinline__ bool place_of(const PagedSeqs& s, int tok, int& pos, long long& vec) {
+    pages::RowBlock b;
+    if (!pages::find_block(s, 1, 1, tok, b)) return false;
+    // blocks of one row each are numbered over the sequences' rows alone; rows that belong to
+    // nobody lie behind them, so the block's row is the token (q_start ascending from 0, as documented)
+    pos = b.p0 + b.blk;
+    if (pos < 0 || b.q0 + b.blk != tok) return false;
+    vec = -1;
+    if (pos >= b.T) return true;  // no room in the table (recorded by find_block)
+    const int page = __ldg(s.table + (long long)b.seq * s.tstride + (pos >> s.pshift));
+    if (page < 0 || page >= s.pages) {
+        if ((threadIdx.x & 31) == 0) pages::flag(s.status, kPgBadPage);
+        return true;
+    }
+    vec = (((long long)page * s.Hk) << s.pshift) + (pos & ((1 << s.pshift) - 1));
+    return true;
+}
+
+template <int D, bool FOUR, int TURN>
+__global__ void __launch_bounds__(kAppThreads)
+append_kernel(const AppendArgs a) {
+    constexpr int L = D / 16, kSlots = kAppThreads / L;
+    const PagedSeqs& s = a.s;
+    const int tok = blockIdx.x, slot = threadIdx.x / L, j = threadIdx.x % L;
+    // head-vector v of the token: K's heads, then V's
+    auto kv = [&](int v) {
+        const bool k = v < s.Hk;
+        return reinterpret_cast<const uint4*>((k ? a.K + tok * a.k_stride + (long long)v * D
+                                                 : a.V + tok * a.v_stride + (long long)(v - s.Hk) * D)) + j;
+    };
+    auto qh = [&](int h) { return reinterpret_cast<const uint4*>(a.Q + tok * a.q_stride + (long long)h * D) + j; };
+    // the first vectors are asked for before the lookups that say where they go have come back
+    uint4 p0 = {}, p1 = {}, r0 = {}, r1 = {};
+    if (slot < 2 * s.Hk) p0 = kv(slot)[0], p1 = kv(slot)[L];
+    const int hq = TURN != kNoTurn && a.Q ? a.Hq : 0;
+    if (slot < hq) r0 = qh(slot)[0], r1 = qh(slot)[L];
+    int pos;
+    long long vec;
+    if (!place_of(s, tok, pos, vec)) return;
+    Angles a0, a1;
+    if constexpr (TURN != kNoTurn) {
+        const long long at = a.r.at ? __ldg(a.r.at + tok) : (long long)a.r.offset + pos;
+        if (at < 0 || at >= a.r.positions) {  // nothing is written for it
+            if (threadIdx.x == 0) pages::flag(s.status, kPgBadPosition);
+            return;
+        }
+        a0.load(a.r, (int)at, j);
+        if constexpr (TURN == kPart) a1.load(a.r, (int)at, j + L);
+    }
+    auto turned = [&](float (&x0)[8], float (&x1)[8], const uint4* src) {
+        if constexpr (TURN == kWhole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = x0[i], q = x1[i];
+                x0[i] = turn_a(p, q, a0.c[i], a0.s[i]);
+                x1[i] = turn_b(p, q, a0.c[i], a0.s[i]);
+            }
+        } else if constexpr (TURN == kPart) {
+            a0.turn(x0, src);
+            a1.turn(x1, src + L);
+        }
+    };
+    // (the loops' bounds are the same for all lanes: encode takes whole warps)
+    if (vec >= 0) {
+        for (int v0 = 0; v0 < 2 * s.Hk; v0 += kSlots) {
+            const int v = v0 + slot;
+            const bool mine = v < 2 * s.Hk;
+            if (v0 > 0 && mine) p0 = kv(v)[0], p1 = kv(v)[L];
+            const bool k = v < s.Hk;
+            const long long at = vec + ((long long)(k ? v : v - s.Hk) << s.pshift);
+            if constexpr (FOUR) {
+                float x0[8], x1[8];
+                unpack8(p0, x0);
+                unpack8(p1, x1);
+                if (mine && k) turned(x0, x1, kv(v));
+                uint32_t w0, w1;
+                float t;
+                encode<L>(x0, x1, w0, w1, t);
+                if (mine) {
+                    uint32_t* to = (k ? a.Kc : a.Vc) + at * (D / 8) + j;
+                    to[0] = w0, to[L] = w1;
+                    if (j == 0) (k ? a.Kt : a.Vt)[at] = t;
+                }
+            } else if (mine) {
+                if (k) {
+                    float x0[8], x1[8];
+                    unpack8(p0, x0);
+                    unpack8(p1, x1);
+                    turned(x0, x1, kv(v));
+                    p0 = pack8(x0), p1 = pack8(x1);
+                }
+                uint4* to = reinterpret_cast<uint4*>((k ? a.Kp : a.Vp) + at * D) + j;
+                to[0] = p0, to[L] = p1;
+            }
+        }
+    }
+    if constexpr (TURN != kNoTurn) {
+        for (int h0 = 0; h0 < hq; h0 += kSlots) {
+            const int h = h0 + slot;
+            const bool mine = h < hq;
+            if (h0 > 0 && mine) r0 = qh(h)[0], r1 = qh(h)[L];
+            float x0[8], x1[8];
+            unpack8(r0, x0);
+            unpack8(r1, x1);
+            if (mine) turned(x0, x1, qh(h));
+            if constexpr (TURN == kPart) __syncwarp();  // Q_out may be Q: its pieces are read before any is written
+            if (mine) {
+                uint4* to = reinterpret_cast<uint4*>(a.Q_out + tok * a.q_out_stride + (long long)h * D) + j;
+                to[0] = pack8(x0), to[L] = pack8(x1);
+            }
+        }
+    }
+}
+
+// Tokens of the 4-bit pages as bf16 rows: t H (u - 7.5). The sums are of halves
+// of whole numbers, exact in float32 in any order.
+template <int D>
+__global__ void __launch_bounds__(kAppThreads)
+read_kernel(const PagedSeqs s, const uint32_t* __restrict__ Kc, const uint32_t* __restrict__ Vc,
+            const float* __restrict__ Kt, const float* __restrict__ Vt, uint16_t* __restrict__ K,
+            uint16_t* __restrict__ V) {
+    constexpr int L = D / 16, kSlots = kAppThreads / L;
+    const int tok = blockIdx.x, slot = threadIdx.x / L, j = threadIdx.x % L, lane = threadIdx.x & 31;
+    int pos;
+    long long vec;
+    if (!place_of(s, tok, pos, vec)) return;
+    for (int v0 = 0; v0 < 2 * s.Hk; v0 += kSlots) {
+        const int v = v0 + slot;
+        const bool mine = v < 2 * s.Hk, k = v < s.Hk;
+        const int h = k ? v : v - s.Hk;
+        uint32_t w0 = 0, w1 = 0;
+        float t = 0.0f;
+        if (mine && vec >= 0) {
+            const long long at = vec + ((long long)h << s.pshift);
+            const uint32_t* from = (k ? Kc : Vc) + at * (D / 8) + j;
+            w0 = __ldg(from), w1 = __ldg(from + L), t = __ldg((k ? Kt : Vt) + at);
+        }
+        float x0[8], x1[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int sh = 2 * (i & 6) + 16 * (i & 1);
+            const float a = (float)(w0 >> sh & 15) - 7.5f, b = (float)(w1 >> sh & 15) - 7.5f;
+            x0[i] = a + b, x1[i] = a - b;  // the halves' stage
+        }
+#pragma unroll
+        for (int n = 1; n < 8; n <<= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!(i & n)) {
+                    float a = x0[i], b = x0[i + n];
+                    x0[i] = a + b, x0[i + n] = a - b;
+                    a = x1[i], b = x1[i + n];
+                    x1[i] = a + b, x1[i + n] = a - b;
+                }
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) {
+            const float sign = lane & o ? -1.0f : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x0[i] = fmaf(sign, x0[i], __shfl_xor_sync(0xffffffffu, x0[i], o));
+                x1[i] = fmaf(sign, x1[i], __shfl_xor_sync(0xffffffffu, x1[i], o));
+            }
+        }
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x0[i] = vec < 0 ? 0.0f : x0[i] * t, x1[i] = vec < 0 ? 0.0f : x1[i] * t;
+            uint4* to = reinterpret_cast<uint4*>((k ? K : V) + ((long long)tok * s.Hk + h) * D) + j;
+            to[0] = pack8(x0), to[L] = pack8(x1);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs& a, int head_dim, bool four, cudaStream_t st) {
+    const int turn = !a.r.cos ? kNoTurn : !a.r.interleaved && 2 * a.r.half == head_dim ? kWhole : kPart;
+#define KVP_APPEND(DD, FF, TT) append_kernel<DD, FF, TT><<<a.s.tokens, kAppThreads, 0, st>>>(a)
+#define KVP_APPEND_D(FF, TT) (head_dim == 64 ? KVP_APPEND(64, FF, TT) : KVP_APPEND(128, FF, TT))
+    if (four) {
+        if (turn == kNoTurn) KVP_APPEND_D(true, kNoTurn);
+        else if (turn == kWhole) KVP_APPEND_D(true, kWhole);
+        else KVP_APPEND_D(true, kPart);
+    } else {
+        if (turn == kWhole) KVP_APPEND_D(false, kWhole);
+        else KVP_APPEND_D(false, kPart);
+    }
+#undef KVP_APPEND_D
+#undef KVP_APPEND
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages4_read(const PagedSeqs& s, int head_dim, const uint32_t* Kc, const uint32_t* Vc, const float* Kt,
+                               const float* Vt, uint16_t* K, uint16_t* V, cudaStream_t st) {
+    if (head_dim == 64) read_kernel<64><<<s.tokens, kAppThreads, 0, st>>>(s, Kc, Vc, Kt, Vt, K, V);
+    else read_kernel<128><<<s.tokens, kAppThreads, 0, st>>>(s, Kc, Vc, Kt, Vt, K, V);
+    return cudaGetLastError();
+}
+
+}  // namespace kvp

@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 import operator
 import os
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkvpool.so")
@@ -49,6 +50,18 @@ class Seqs(ctypes.Structure):
 class Score(ctypes.Structure):
     _fields_ = [("cap", ctypes.c_float), ("window", ctypes.c_int), ("slopes", ctypes.c_void_p),
                 ("first", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
+class Pages4Arg(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("K_scale", ctypes.c_void_p),
+                ("V_scale", ctypes.c_void_p), ("layers", ctypes.c_int), ("pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("page_tokens", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("status", ctypes.c_void_p)]
+
+
+class RotaryArg(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_int), ("dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("offset", ctypes.c_int), ("at", ctypes.c_void_p)]
 
 
 class LayerView(ctypes.Structure):
@@ -119,6 +132,21 @@ _SIGS = {
     "kvpool_pages_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_longlong, ctypes.c_void_p, ctypes.c_longlong,
                                            ctypes.c_void_p]),
+    "kvpool_pages_append_rotary": (
+        ctypes.c_int,
+        [ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 3 + [ctypes.c_longlong, ctypes.c_void_p, ctypes.c_longlong,
+         ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_void_p]),
+    "kvpool_pages4_append": (
+        ctypes.c_int,
+        [ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 3 + [ctypes.c_longlong, ctypes.c_void_p, ctypes.c_longlong,
+         ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_void_p]),
+    "kvpool_pages4_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 4),
+    "kvpool_pages4_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                          ctypes.c_void_p]),
+    "kvpool_pages4_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p]),
+    "kvpool_pages4_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "kvpool_pages_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                          ctypes.c_void_p]),
     "kvpool_pages_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
@@ -433,19 +461,204 @@ def pages_append(K_pages, V_pages, layer, K, V, table, kv_len, q_start, status=N
                                       _raw_stream(stream, dev)), "kvpool_pages_append")
 
 
-def pages_copy(K_pages, V_pages, src, dst, stream=None):
-    """Page dst[i] of every layer becomes page src[i] (kvpool_pages_copy);
-    src, dst: lists of int. No page twice a destination, or both."""
+class Rotary(NamedTuple):
+    """The rotation of Q and K by position (kvpool_rotary_t): cos and sin
+    float32 [positions, dim / 2] on the device (rotary_tables makes them).
+    Channels i and i + dim / 2 of a head turn together, or 2 i and 2 i + 1 where
+    interleaved. A token at position p of its sequence takes row offset + p (an
+    agent behind a shared context: its length)."""
+
+    cos: object
+    sin: object
+    interleaved: bool = False
+    offset: int = 0
+
+
+def rotary_tables(positions, dim, base=10000.0, device="cuda"):
+    """Cosines and sines of the angles p * base^(-2 i / dim), float32
+    [positions, dim / 2] each, from angles in 64 bits."""
+    import torch
+
+    if dim < 2 or dim % 2 or positions < 1:
+        raise ValueError("positions must be at least 1, dim even and at least 2")
+    turn = base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * turn
+    return angle.cos().float(), angle.sin().float()
+
+
+def _rotary(rotary, at, tokens, dev):
+    import torch
+
+    cos, sin = rotary[0], rotary[1]
+    shape = cos.shape
+    if len(shape) != 2 or sin.shape != shape:
+        raise ValueError("cos and sin must be [positions, dim / 2]")
+    f32 = torch.float32
+    if at is not None:
+        if tuple(at.shape) != (tokens,):
+            raise ValueError(f"positions must have shape {(tokens,)}")
+        at = _need(at, torch.int32, "positions", dev)
+    return RotaryArg(_need(cos, f32, "cos", dev), _need(sin, f32, "sin", dev), _i32(shape[0], "positions"), 2 * shape[1],
+                     1 if rotary[2] else 0, _i32(rotary[3], "offset"), at)
+
+
+def _append_turned(call, pages, layer, K, V, table, kv_len, q_start, rotary, Q, Q_out, positions, stream):
+    """Append into the cache that pages(device) describes, with K and Q turned."""
+    import torch
+
+    layer = _i32(layer, "layer")
+    dev = _here()
+    pg = pages(dev)
+    n = K.shape[0]
+    if V.shape[0] != n:
+        raise ValueError("K and V must have the same shape")
+    kp, ks = _token_rows(K, "K", pg.kv_heads, pg.head_dim, dev)
+    vp, vs = _token_rows(V, "V", pg.kv_heads, pg.head_dim, dev)
+    sq = _seqs(table, kv_len, q_start, n, 0, 0, dev)
+    if rotary is None:
+        if Q is not None or Q_out is not None or positions is not None:
+            raise ValueError("Q, Q_out and positions go with a rotary")
+        turn = None
+    else:
+        turn = ctypes.byref(_rotary(rotary, positions, n, dev))
+    raw = _raw_stream(stream, dev)
+    qp = qs = op = os_ = None
+    hq = 0
+    if Q is not None:
+        if Q.dim() != 3 or Q.shape[0] != n:
+            raise ValueError(f"Q must be [{n}, q_heads, head_dim]")
+        hq = Q.shape[1]
+        qp, qs = _token_rows(Q, "Q", hq, pg.head_dim, dev)
+        if Q_out is None:
+            # on the stream that writes it, so that the allocator knows it
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                Q_out = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
+        elif Q_out.shape != Q.shape:
+            raise ValueError("Q_out must have Q's shape")
+        op, os_ = _token_rows(Q_out, "Q_out", hq, pg.head_dim, dev)
+    elif Q_out is not None:
+        raise ValueError("Q_out goes with Q")
+    _check(getattr(_lib(), call)(ctypes.byref(pg), layer, ctypes.byref(sq), turn, kp, ks, vp, vs, qp, qs or 0, hq, op,
+                                 os_ or 0, raw), call)
+    return Q_out
+
+
+def pages_append_rotary(K_pages, V_pages, layer, K, V, table, kv_len, q_start, rotary, Q=None, Q_out=None, positions=None,
+                        status=None, stream=None):
+    """pages_append with the rotation by position on the way
+    (kvpool_pages_append_rotary): K is turned, rounded to bf16 once and written,
+    V written as it is; the new tokens' Q (bf16 [tokens, q_heads, d], rows of a
+    fused projection as they are) is turned into Q_out, which may be Q itself.
+    rotary: a Rotary; positions: None or int32 [tokens], the tables' row of each
+    token, instead of offset + its position. Returns Q_out, or None without Q. A
+    position outside the tables is recorded in status and nothing is written for
+    its token."""
+    if rotary is None:
+        raise ValueError("rotary is needed: pages_append writes K as it is")
+    return _append_turned("kvpool_pages_append_rotary", lambda dev: _pages(K_pages, V_pages, status, dev), layer, K, V,
+                          table, kv_len, q_start, rotary, Q, Q_out, positions, stream)
+
+
+def _copy_args(src, dst):
     n = len(src)
     if len(dst) != n:
         raise ValueError("src and dst must have the same length")
     for x in (src, dst) if n else ():
         _i32(min(x), "page"), _i32(max(x), "page")
-    dev = _here()
     arr = ctypes.c_int32 * max(n, 1)
+    return arr(*src), arr(*dst), n
+
+
+def pages_copy(K_pages, V_pages, src, dst, stream=None):
+    """Page dst[i] of every layer becomes page src[i] (kvpool_pages_copy);
+    src, dst: lists of int. No page twice a destination, or both."""
+    args = _copy_args(src, dst)
+    dev = _here()
     pg = _pages(K_pages, V_pages, None, dev)
-    _check(_lib().kvpool_pages_copy(ctypes.byref(pg), arr(*src), arr(*dst), n, _raw_stream(stream, dev)),
-           "kvpool_pages_copy")
+    _check(_lib().kvpool_pages_copy(ctypes.byref(pg), *args, _raw_stream(stream, dev)), "kvpool_pages_copy")
+
+
+class Pages4(NamedTuple):
+    """Pages in 4 bits (kvpool_pages4_t): codes uint8 [layers, pages, kv_heads,
+    page_tokens, head_dim / 2], scales float32 [layers, pages, kv_heads,
+    page_tokens], on the current device."""
+
+    K: object
+    V: object
+    K_scale: object
+    V_scale: object
+
+
+def pages4_empty(layers, pages, kv_heads, page_tokens, head_dim):
+    """Uninitialised Pages4 on the current CUDA device."""
+    import torch
+
+    shape = (layers, pages, kv_heads, page_tokens)
+    codes = [torch.empty(shape + (head_dim // 2,), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    return Pages4(*codes, *(torch.empty(shape, dtype=torch.float32, device="cuda") for _ in range(2)))
+
+
+def _pages4(pages, status=None, dev=None):
+    import torch
+
+    dev = _here() if dev is None else dev
+    K, V, ks, vs = pages
+    shape = K.shape
+    if len(shape) != 5 or V.shape != shape or ks.shape != shape[:4] or vs.shape != shape[:4]:
+        raise ValueError("codes must be [layers, pages, kv_heads, page_tokens, head_dim / 2], scales [layers, pages, "
+                         "kv_heads, page_tokens]")
+    u8, f32 = torch.uint8, torch.float32
+    return Pages4Arg(_need(K, u8, "K", dev), _need(V, u8, "V", dev), _need(ks, f32, "K_scale", dev),
+                     _need(vs, f32, "V_scale", dev), *shape[:4], 2 * shape[4],
+                     None if status is None else _need(status, torch.int32, "status", dev))
+
+
+def pages4_append(pages, layer, K, V, table, kv_len, q_start, rotary=None, Q=None, Q_out=None, positions=None,
+                  status=None, stream=None):
+    """Write new tokens into pages of 4 bits (kvpool_pages4_append): pages a
+    Pages4, the rest as pages_append, and pages_append_rotary where a rotary is
+    given (K goes from its rotation to codes without a rounding to bf16)."""
+    return _append_turned("kvpool_pages4_append", lambda dev: _pages4(pages, status, dev), layer, K, V, table, kv_len,
+                          q_start, rotary, Q, Q_out, positions, stream)
+
+
+def pages4_read(pages, layer, table, kv_len, q_start, tokens, K=None, V=None, status=None, stream=None):
+    """What the codes of the sequences' last tokens stand for
+    (kvpool_pages4_read): K, V bf16 [tokens, kv_heads, d], sequence s's last
+    q_start[s + 1] - q_start[s] tokens in rows q_start[s] and on."""
+    import torch
+
+    layer, tokens = _i32(layer, "layer"), _i32(tokens, "tokens")
+    dev = _here()
+    pg = _pages4(pages, status, dev)
+    sq = _seqs(table, kv_len, q_start, tokens, 0, 0, dev)
+    shape = (tokens, pg.kv_heads, pg.head_dim)
+    raw = _raw_stream(stream, dev)
+    for t, name in ((K, "K"), (V, "V")):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}")
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        K, V = (torch.empty(shape, dtype=torch.bfloat16, device=pages[0].device) if t is None else t for t in (K, V))
+    _check(_lib().kvpool_pages4_read(ctypes.byref(pg), layer, ctypes.byref(sq), _need(K, torch.bfloat16, "K", dev),
+                                     _need(V, torch.bfloat16, "V", dev), raw), "kvpool_pages4_read")
+    return K, V
+
+
+def pages4_copy(pages, src, dst, stream=None):
+    """pages_copy of pages in 4 bits, codes and scales (kvpool_pages4_copy)."""
+    args = _copy_args(src, dst)
+    dev = _here()
+    pg = _pages4(pages, None, dev)
+    _check(_lib().kvpool_pages4_copy(ctypes.byref(pg), *args, _raw_stream(stream, dev)), "kvpool_pages4_copy")
+
+
+def pages4_attend(pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=None, cap=0.0, slopes=None, window=0,
+                  first=None, prefix=None, out=None, lse=None, return_lse=False, softmax_scale=0.0, status=None,
+                  stream=None):
+    """pages_attend over pages of 4 bits (kvpool_pages4_attend): pages a Pages4,
+    the rest and the results as pages_attend's."""
+    return _attend("kvpool_pages4_attend", lambda dev: _pages4(pages, status, dev), layer, Q, table, kv_len, q_start,
+                   max_q, max_kv, cap, slopes, window, first, prefix, out, lse, return_lse, softmax_scale, stream)
 
 
 def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=None, cap=0.0, slopes=None,
@@ -462,11 +675,18 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
     Returns out bf16 [tokens, q_heads, d], or (out, lse float32 [tokens,
     q_heads]) with return_lse or an lse to write to. A row that sees no key
     gets 0 and -inf; rows behind the last sequence are left as they are."""
+    return _attend("kvpool_pages_attend", lambda dev: _pages(K_pages, V_pages, status, dev), layer, Q, table, kv_len,
+                   q_start, max_q, max_kv, cap, slopes, window, first, prefix, out, lse, return_lse, softmax_scale, stream)
+
+
+def _attend(call, pages, layer, Q, table, kv_len, q_start, max_q, max_kv, cap, slopes, window, first, prefix, out, lse,
+            return_lse, softmax_scale, stream):
+    """Attention over the cache that pages(device) describes."""
     import torch
 
     layer = _i32(layer, "layer")
     dev = _here()
-    pg = _pages(K_pages, V_pages, status, dev)
+    pg = pages(dev)
     if Q.dim() != 3:
         raise ValueError("Q must be [tokens, q_heads, head_dim]")
     n, hq, d = Q.shape
@@ -495,24 +715,33 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
             if return_lse and lp is None:
                 lse = torch.empty((n, hq), dtype=torch.float32, device=Q.device)
                 lp = lse.data_ptr()
-    _check(_lib().kvpool_pages_attend(ctypes.byref(pg), layer, ctypes.byref(sq), qp, qs, hq, sc, op, lp, softmax_scale,
-                                      raw), "kvpool_pages_attend")
+    _check(getattr(_lib(), call)(ctypes.byref(pg), layer, ctypes.byref(sq), qp, qs, hq, sc, op, lp, softmax_scale, raw),
+           call)
     return out if lse is None else (out, lse)
 
 
 class PagedCache:
-    """The agents' private caches: bf16 pages of every layer (K, V tensors
-    [layers, pages, kv_heads, page_tokens, head_dim]) on the current CUDA
-    device, and the pager that says whose they are. Page copies that a fork or
-    a compaction makes due are enqueued before the call returns."""
+    """The agents' private caches: pages of every layer on the current CUDA
+    device, and the pager that says whose they are. bits 16: bf16 (K, V tensors
+    [layers, pages, kv_heads, page_tokens, head_dim]); bits 4: codes and scales
+    (pages4, a Pages4; K and V are its codes). Page copies that a fork or a
+    compaction makes due are enqueued before the call returns."""
 
-    def __init__(self, layers, kv_heads, head_dim, pages, page_tokens=64):
+    pages4 = None
+
+    def __init__(self, layers, kv_heads, head_dim, pages, page_tokens=64, bits=16):
         import torch
 
+        if bits not in (4, 16):
+            raise ValueError(f"bits must be 4 or 16, not {bits}")
         self.pager = Pager(pages, page_tokens)
-        shape = (layers, pages, kv_heads, page_tokens, head_dim)
-        self.K = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
-        self.V = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        if bits == 4:
+            self.pages4 = pages4_empty(layers, pages, kv_heads, page_tokens, head_dim)
+            self.K, self.V = self.pages4[:2]
+        else:
+            shape = (layers, pages, kv_heads, page_tokens, head_dim)
+            self.K = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+            self.V = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
         self.status_word = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.page_tokens = page_tokens
 
@@ -538,15 +767,26 @@ class PagedCache:
     def _usable(self, stream):
         """Another device's cache or stream is refused, before the pager has changed anything."""
         dev = _here()
-        _pages(self.K, self.V, self.status_word, dev)
+        self._arg(dev)
         _raw_stream(stream, dev)
+
+    def _arg(self, dev=None):
+        if self.pages4 is not None:
+            return _pages4(self.pages4, self.status_word, dev)
+        return _pages(self.K, self.V, self.status_word, dev)
+
+    def _copy(self, src, dst, stream):
+        if self.pages4 is not None:
+            pages4_copy(self.pages4, src, dst, stream)
+        else:
+            pages_copy(self.K, self.V, src, dst, stream)
 
     def compact(self, stream=None):
         """Move owned pages into the lowest numbers; how many moved. Batches
         made before are void."""
         self._usable(stream)
         src, dst = self.pager.compact()
-        pages_copy(self.K, self.V, src, dst, stream)
+        self._copy(src, dst, stream)
         return len(src)
 
     def grow(self, seqs, counts, stream=None):
@@ -565,31 +805,61 @@ class PagedCache:
                 if pair:
                     src.append(pair[0])
                     dst.append(pair[1])
-            pages_copy(self.K, self.V, src, dst, stream)
+            self._copy(src, dst, stream)
             return PagedBatch(self, seqs, counts, stream)
         except BaseException:
             # (a page of its own that a sequence got already is copied and kept)
             for s, n in zip(seqs, before):
                 self.pager.truncate(s, n)
             live = [(a, b) for a, b in zip(src, dst) if self.pager.owners(b)]
-            pages_copy(self.K, self.V, [a for a, _ in live], [b for _, b in live], stream)
+            self._copy([a for a, _ in live], [b for _, b in live], stream)
             raise
 
-    def append(self, layer, K, V, batch, stream=None):
-        """Write the batch's new tokens: K, V bf16 [tokens, kv_heads, d] (rows behind the batch's are padding)."""
+    def append(self, layer, K, V, batch, stream=None, rotary=None, Q=None, Q_out=None, positions=None):
+        """Write the batch's new tokens: K, V bf16 [tokens, kv_heads, d] (rows
+        behind the batch's are padding). With a rotary (a Rotary) K is turned by
+        position on the way and Q too, as pages_append_rotary does: returns the
+        turned Q, or None without Q."""
         _check_rows(K, batch)
-        pages_append(self.K, self.V, layer, K, V, batch.table, batch.kv_len, batch.q_start, self.status_word, stream)
+        where = batch.table, batch.kv_len, batch.q_start
+        if self.pages4 is not None:
+            return pages4_append(self.pages4, layer, K, V, *where, rotary, Q, Q_out, positions, self.status_word, stream)
+        if rotary is not None:
+            return pages_append_rotary(self.K, self.V, layer, K, V, *where, rotary, Q, Q_out, positions,
+                                       self.status_word, stream)
+        if Q is not None or Q_out is not None or positions is not None:
+            raise ValueError("Q, Q_out and positions go with a rotary")
+        pages_append(self.K, self.V, layer, K, V, *where, self.status_word, stream)
 
     def attend(self, layer, Q, batch, **options):
         """pages_attend of the batch's new tokens over their sequences (rows behind the batch's are padding)."""
         _check_rows(Q, batch)
-        return pages_attend(self.K, self.V, layer, Q, batch.table, batch.kv_len, batch.q_start, batch.max_q,
-                            batch.max_kv, status=self.status_word, **options)
+        where = batch.table, batch.kv_len, batch.q_start, batch.max_q, batch.max_kv
+        if self.pages4 is not None:
+            return pages4_attend(self.pages4, layer, Q, *where, status=self.status_word, **options)
+        return pages_attend(self.K, self.V, layer, Q, *where, status=self.status_word, **options)
+
+    def read(self, layer, seqs, stream=None):
+        """Whole sequences of a 4-bit cache as the values they stand for: per
+        sequence (K, V), bf16 [tokens, kv_heads, d] each."""
+        if self.pages4 is None:
+            raise ValueError("a cache of 16 bits holds its values: K and V")
+        self._usable(stream)
+        counts = [self.pager.length(s) for s in seqs]
+        if not sum(counts):
+            import torch
+
+            none = torch.empty((0, self.K.shape[2], 2 * self.K.shape[4]), dtype=torch.bfloat16, device=self.K.device)
+            return [(none, none) for _ in seqs]
+        b = PagedBatch(self, seqs, counts, stream)
+        K, V = pages4_read(self.pages4, layer, b.table, b.kv_len, b.q_start, b.tokens, status=self.status_word, stream=stream)
+        return list(zip(K.split(counts), V.split(counts)))
 
     def status(self, stream=None) -> int:
         """Synchronise and return (and clear) the device status code of the pages' calls."""
-        pg = _pages(self.K, self.V, self.status_word)
-        return int(_lib().kvpool_pages_status(ctypes.byref(pg), _stream_ptr(stream)))
+        pg = self._arg()
+        call = _lib().kvpool_pages_status if self.pages4 is None else _lib().kvpool_pages4_status
+        return int(call(ctypes.byref(pg), _stream_ptr(stream)))
 
 
 class PagedBatch:
@@ -762,6 +1032,8 @@ class KVPool:
         _check_rows(Q, batch)
         n, hq, d = Q.shape
         dev = _here()
+        if getattr(cache, "pages4", None) is not None:
+            raise ValueError("the joint softmax with the pool takes a cache of 16 bits")
         pg = _pages(cache.K, cache.V, cache.status_word, dev)
         if d != pg.head_dim:
             raise ValueError("Q must be [tokens, q_heads, head_dim]")
