@@ -7,13 +7,12 @@
 // them the matrix products see codes alone. One pass over the keys with a
 // running reference m per row, p = 2^(x - m), O and l rescaled when a score
 // passes m by more than 2^8. The weights p t' are rounded to bf16 (off by at
-// most 2^-8 of each, as the output's own rounding is of it), H q to fp16 after a
-// power of two has brought the row's largest value into [1/2, 1): off by at most 2^-11 of
-// each coordinate. Codes enter the products exactly: of Q K^T as fp16 1024 + u
-// or 1024 + 16 u (one mask and one constant; the constants' share is the
-// product's first summand, the sixteenth is in that channel's H q), of P V as
-// bf16 u - 8, the other half of a step times the sum of the weights, which one
-// more matrix row of ones adds up.
+// most 2^-8 of each, as the output's own rounding is of it), H q to two fp16
+// parts (a power of two has brought the row's largest value into [1/2, 1)), as
+// one part alone, off by 2^-11, is seen in the log of the sum. Codes enter the
+// products exactly: of Q K^T as fp16 u - 8 or 16 (u - 8) (one mask and one
+// addition; the sixteenth is in that channel's H q, the other half of a step is
+// the product's first summand), of P V as bf16 u - 7.5.
 //
 // Bound: memory, as a step reads D + 8 bytes per key and KV head; close behind
 // it the instructions that make operands of codes, so the layout serves these.
@@ -54,8 +53,10 @@ struct Lay {
     static constexpr int rows = 8 * NR;
     // the merge reuses the rings: per warp `rows` rows, then the CTA's merged ones
     static constexpr int merge = (kWarps + 1) * rows * rs * 4;
-    static constexpr int q = rows * (D * 2 + 16);            // H q, at the start; then 2 floats per row
-    static constexpr int total = (ring > merge ? ring : merge) > q ? (ring > merge ? ring : merge) : q;
+    // H q as the lanes' operands of every step, 16 bytes each: high and low parts; then 2 floats per row
+    static constexpr int q = ring > merge ? ring : merge, steps = D / 16;
+    static constexpr int info = q + NR * steps * 512;
+    static constexpr int total = info + rows * 8;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -96,28 +97,20 @@ __device__ __forceinline__ uint32_t mask_or(uint32_t x, uint32_t mask, uint32_t 
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
     return y;
 }
-// codes in bits 0-3 of both halves -> bf16 u - 8, exactly
+// codes in bits 1-4 of both halves -> bf16 u - 7.5, exactly
 __device__ __forceinline__ uint32_t centred(uint32_t x) {
-    const uint32_t y = mask_or(x, 0x000F000Fu, 0x43004300u);  // 128 + u
+    const uint32_t y = mask_or(x, 0x001E001Eu, 0x42804280u);  // 64 + u
     uint32_t z;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0xC308C308u));  // - 136
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(0xC28FC28Fu));  // - 71.5
     return z;
 }
 
-// Butterflies of the transform over a row that lies in 4 consecutive channels
-// per lane, D / 4 lanes.
-template <int D>
-__device__ __forceinline__ void transform4(float4& a) {
-    const float s = a.x + a.y, d = a.x - a.y, u = a.z + a.w, v = a.z - a.w;
-    a = make_float4(s + u, d + v, s - u, d - v);
-#pragma unroll
-    for (int o = 1; o < D / 4; o <<= 1) {
-        const float g = threadIdx.x & o ? -1.0f : 1.0f;
-        a.x = fmaf(g, a.x, __shfl_xor_sync(0xffffffffu, a.x, o));
-        a.y = fmaf(g, a.y, __shfl_xor_sync(0xffffffffu, a.y, o));
-        a.z = fmaf(g, a.z, __shfl_xor_sync(0xffffffffu, a.z, o));
-        a.w = fmaf(g, a.w, __shfl_xor_sync(0xffffffffu, a.w, o));
-    }
+// codes under the mask -> fp16 1024 + u (or 1024 + 16 u) less 1032 (1152), exactly
+__device__ __forceinline__ uint32_t half_centred(uint32_t x, uint32_t mask, uint32_t less) {
+    const uint32_t y = mask_or(x, mask, 0x64006400u);
+    uint32_t z;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(z) : "r"(y), "r"(less));
+    return z;
 }
 
 // NR: blocks of 8 query rows. SCORED: score modifiers apply. DIRECT: every
@@ -132,6 +125,7 @@ pages4_rows_kernel(const PagedAttend4 p4) {
     constexpr int MB = D / 16;   // blocks of 16 channels of P V
     constexpr int W = D / 32;    // words of a key per lane in Q K^T
     constexpr int RS = L::rs;
+    constexpr bool kApart = NR == 1;
     const PagedAttend& p = p4.a;
     extern __shared__ __align__(128) unsigned char sm[];
     const PagedSeqs& s = p.s;
@@ -163,9 +157,7 @@ pages4_rows_kernel(const PagedAttend4 p4) {
         auto token_of = [&](int r) { return (r_begin + r) / p.G; };
         auto head_of = [&](int r) { return g * p.G + (r_begin + r) % p.G; };
 
-        // H q of the block's rows in fp16 (rows past it repeat its last), the constants' share and the power of two
-        unsigned char* qs = sm;
-        constexpr int kQRow = D * 2 + 16;
+        // H q of the block's rows in two fp16 parts (rows past it repeat its last), half a step's share and the power of two
         for (int r = warp; r < kRows; r += kWarps) {
             const int rr = min(r, nr - 1);
             const uint16_t* src = p.Q + (long long)(b.q0 + token_of(rr)) * p.q_stride + (long long)head_of(rr) * D;
@@ -181,23 +173,24 @@ pages4_rows_kernel(const PagedAttend4 p4) {
             const int e = min(max((int)(top >> 23) - 126, -126), 126);
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
             x.x *= down, x.y *= down, x.z *= down, x.w *= down;
-            transform4<D>(x);
-            // channels 4 l + 2 and + 3 meet 16 u
-            const __half2 lo = __floats2half2_rn(x.x, x.y), hi = __floats2half2_rn(x.z * 0.0625f, x.w * 0.0625f);
-            const float2 fl = __half22float2(lo), fh = __half22float2(hi);
-            float off = lane < D / 4 ? fmaf(fl.x + fl.y, 1031.5f, (fh.x + fh.y) * 1144.0f) : 0.0f;
+            pages::transform4<D>(x);
+            float sum = (x.x + x.y) + (x.z + x.w);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) off += __shfl_xor_sync(0xffffffffu, off, o);
-            if (lane < D / 4)
-                *reinterpret_cast<uint2*>(qs + r * kQRow + lane * 8) = make_uint2(
-                    *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            for (int o = D / 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            // channels 4 l + 2 and + 3 meet 16 (u - 8)
+            x.z *= 0.0625f, x.w *= 0.0625f;
+            const __half2 h0 = __floats2half2_rn(x.x, x.y), h1 = __floats2half2_rn(x.z, x.w);
+            const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+            const __half2 l0 = __floats2half2_rn(x.x - f0.x, x.y - f0.y), l1 = __floats2half2_rn(x.z - f1.x, x.w - f1.y);
+            auto bits = [](const __half2& h) { return *reinterpret_cast<const uint32_t*>(&h); };
+            if (lane < D / 4)  // step lane % KS of the quarter-row lane / KS
+                *reinterpret_cast<uint4*>(sm + L::q + (((r >> 3) * KS + lane % KS) * 32 + (r & 7) * 4 + lane / KS) * 16) =
+                    make_uint4(bits(h0), bits(h1), bits(l0), bits(l1));
             if (lane == 0)
-                *reinterpret_cast<float2*>(qs + r * kQRow + D * 2) =
-                    make_float2(off, __uint_as_float((uint32_t)(127 + e) << 23));
+                *reinterpret_cast<float2*>(sm + L::info + r * 8) =
+                    make_float2(0.5f * sum, __uint_as_float((uint32_t)(127 + e) << 23));
         }
         __syncthreads();
-        // operands: row 8 n + quad, channels 32 qi ... (D = 64: 16 qi ...), two registers per step
-        uint32_t qf[NR][KS][2];
         float off[NR][2], mul[NR][2];  // of this lane's rows 8 n + 2 qi + h
         Seen see[NR][2];
         int pos[NR][2];
@@ -205,17 +198,11 @@ pages4_rows_kernel(const PagedAttend4 p4) {
         int lo = INT_MAX, hi = 0, pre_end = 0, win_lo = INT_MAX;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const uint2* src = reinterpret_cast<const uint2*>(qs + (8 * n + quad) * kQRow + qi * (D / 2));
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const uint2 v = src[k];
-                qf[n][k][0] = v.x, qf[n][k][1] = v.y;
-            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = 8 * n + 2 * qi + h, rr = min(r, nr - 1);
-                const float2 c = *reinterpret_cast<const float2*>(qs + r * kQRow + D * 2);
-                off[n][h] = -c.x;
+                const float2 c = *reinterpret_cast<const float2*>(sm + L::info + r * 8);
+                off[n][h] = c.x;
                 mul[n][h] = c.y * (SCORED ? 1.0f : p.scale_log2);
                 const int i = token_of(rr);
                 pos[n][h] = b.p0 + i;
@@ -232,7 +219,6 @@ pages4_rows_kernel(const PagedAttend4 p4) {
         pages::Gap gap;
         if (SCORED && p.prefix && p.window > 0)
             gap = pages::Gap(__reduce_max_sync(0xffffffffu, pre_end), __reduce_min_sync(0xffffffffu, win_lo), kUnit);
-        __syncthreads();  // every warp has its operands: the rings may be filled
 
         // keys that any row of the block sees, in units; the cluster's CTAs take
         // consecutive shares of them, the warps of a CTA every fourth unit
@@ -241,6 +227,7 @@ pages4_rows_kernel(const PagedAttend4 p4) {
         const int ua = u_lo + rank * per, ub = min(u_hi, ua + per);
         const int nu = ub - ua > warp ? (ub - ua - warp + kWarps - 1) / kWarps : 0;  // this warp's units
 
+        const uint4* qs = reinterpret_cast<const uint4*>(sm + L::q) + lane;
         const uint32_t ring = ptx::smem_u32(sm) + warp * (kStages * L::stage);
         // the pages of this warp's next 16 units, one per lane for 16 keys each
         auto pages_at = [&](int k) {
@@ -248,10 +235,23 @@ pages4_rows_kernel(const PagedAttend4 p4) {
             return i < nu && t < T ? __ldg(table + (t >> s.pshift)) : 0;
         };
         int pg_now = pages_at(0), pg_next = 0;
-        // where this lane's 16-byte pieces go: within a 128-byte line, pieces are
+        // Where this lane's 16-byte pieces go: within a 128-byte line, pieces are
         // exchanged by the line's number, so that neither product's reads collide
+        // (the exchange repeats after 512 bytes, or 256 with D = 64: further rows of
+        // the lane lie at fixed distances).
         constexpr int kLineRows = 256 / D;  // keys per line
         auto swizzled = [](int line) { return D == 128 ? 2 * (line & 3) : 2 * (line & 1); };
+        auto place = [&](int row, int piece) {  // of the row
+            const int line = row / kLineRows;
+            return line * 128 + ((((row % kLineRows) * (D / 32) + piece) ^ swizzled(line)) << 4);
+        };
+        constexpr int kHalf = 16 * D / 2;  // bytes of 16 keys
+        const uint32_t to_codes = place(lane / (D / 32), lane % (D / 32));
+        const uint32_t to_scales = 2 * L::codes + ((lane >> 2) & 1) * (kUnit * 4) + (lane & 3) * 16;
+        const unsigned char* kc = reinterpret_cast<const unsigned char*>(p.K) + lane * 16;
+        const unsigned char* vc = reinterpret_cast<const unsigned char*>(p.V) + lane * 16;
+        const float* scales = (lane & 4 ? p4.Vt : p4.Kt) + 4 * (lane & 3);
+        uint32_t fill = ring;  // the stage that is filled next
         auto load_unit = [&](int k) {
             if ((k & 15) == 0) {
                 if (k > 0) pg_now = pg_next;
@@ -259,94 +259,110 @@ pages4_rows_kernel(const PagedAttend4 p4) {
             }
             if (k < nu) {
                 const int t0 = gap.number(ua + warp + k * kWarps) * kUnit;
-                const uint32_t dst = ring + (k % kStages) * L::stage;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int page = __shfl_sync(0xffffffffu, pg_now, (k & 15) * 2 + h), t = t0 + 16 * h;
                     const bool ok = page >= 0 && page < s.pages;
-                    if (!ok && lane == 0) pages::flag(s.status, kPgBadPage);
                     const long long vec =
                         ((((long long)(ok ? page : 0) * s.Hk + g) << s.pshift) + (t & ((1 << s.pshift) - 1)));
-                    const unsigned char* kc = reinterpret_cast<const unsigned char*>(p.K) + vec * (D / 2);
-                    const unsigned char* vc = reinterpret_cast<const unsigned char*>(p.V) + vec * (D / 2);
-                    constexpr int kPieces = 16 * D / 32;  // of 16 keys
+                    const uint32_t to = fill + to_codes + h * kHalf;
+                    if (ok && t + 16 <= T) {
 #pragma unroll
-                    for (int it = 0; it < kPieces / 32; ++it) {
-                        const int i = it * 32 + lane, line = h * (kPieces / 8) + i / 8;
-                        const bool real = ok && t + i / (D / 32) < T;
-                        const uint32_t to = dst + line * 128 + (((i & 7) ^ swizzled(line)) << 4);
-                        cp_async16(to, kc + i * 16, real ? 16 : 0);
-                        cp_async16(to + L::codes, vc + i * 16, real ? 16 : 0);
-                    }
-                    // scales: four keys to a piece
-                    if (lane < 8) {
-                        const int i = lane & 3;
-                        const float* from = (lane < 4 ? p4.Kt : p4.Vt) + vec + 4 * i;
-                        const uint32_t to = dst + 2 * L::codes + (lane >> 2) * (kUnit * 4) + h * 64 + i * 16;
-                        cp_async16(to, from, ok ? min(max(T - t - 4 * i, 0), 4) * 4 : 0);
+                        for (int it = 0; it < D / 64; ++it) {
+                            cp_async16(to + it * 512, kc + vec * (D / 2) + it * 512, 16);
+                            cp_async16(to + L::codes + it * 512, vc + vec * (D / 2) + it * 512, 16);
+                        }
+                        if (lane < 8) cp_async16(fill + to_scales + h * 64, scales + vec, 16);
+                    } else {
+                        if (!ok && lane == 0) pages::flag(s.status, kPgBadPage);
+#pragma unroll
+                        for (int it = 0; it < D / 64; ++it) {
+                            const int real = ok && t + (it * 32 + lane) / (D / 32) < T ? 16 : 0;
+                            cp_async16(to + it * 512, kc + vec * (D / 2) + it * 512, real);
+                            cp_async16(to + L::codes + it * 512, vc + vec * (D / 2) + it * 512, real);
+                        }
+                        // (scales: four keys to a piece)
+                        if (lane < 8)
+                            cp_async16(fill + to_scales + h * 64, scales + vec,
+                                       ok ? min(max(T - t - 4 * (lane & 3), 0), 4) * 4 : 0);
                     }
                 }
             }
             cp_commit();  // an empty group past the last unit keeps the count
+            fill = fill == ring + (kStages - 1) * L::stage ? ring : fill + L::stage;
         };
 #pragma unroll
         for (int k = 0; k < kStages - 1; ++k) load_unit(k);
 
-        float O[NR][MB][4], sumw[NR][4];
+        float O[NR][MB][4];
         float m[NR][2], l[NR][2];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sumw[n][e] = 0.0f;
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int k = 0; k < MB; ++k) O[n][k][e] = 0.0f;
-            }
             m[n][0] = m[n][1] = -CUDART_INF_F;
             l[n][0] = l[n][1] = 0.0f;
         }
 
+        // this lane's reads: K of key quad (its piece, or half of one), V of keys 2 qi and 2 qi + 1
+        const int k_at = D == 128 ? place(quad, qi) : place(quad, qi >> 1) + (qi & 1) * 8;
+        const int v_in = D == 128 ? (quad & 1) * 8 : (quad & 3) * 4;
+        const int v_at[2] = {place(2 * qi, D == 128 ? quad >> 1 : quad >> 2) + v_in,
+                             place(2 * qi + 1, D == 128 ? quad >> 1 : quad >> 2) + v_in};
+        constexpr int kEight = 8 * D / 2;  // bytes of 8 keys
+        int sees_all = INT_MAX;  // with the causal mask alone: the keys that every row sees
+        if constexpr (!SCORED) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) sees_all = min(sees_all, min(see[n][0].b1, see[n][1].b1));
+            sees_all = __reduce_min_sync(0xffffffffu, sees_all);
+        }
+        const unsigned char* st = sm + warp * (kStages * L::stage);
         for (int k = 0; k < nu; ++k) {
             load_unit(k + kStages - 1);
             cp_wait<kStages - 1>();
             __syncwarp();
-            const unsigned char* st = sm + warp * (kStages * L::stage) + (k % kStages) * L::stage;
             const int t0 = gap.number(ua + warp + k * kWarps) * kUnit;
             const float* kt = reinterpret_cast<const float*>(st + 2 * L::codes);
             const float* vt = kt + kUnit;
             // ---- scores: c[n][i][e]: key t0 + 16 i + quad (+ 8 for e >= 2), row 8 n + 2 qi + (e & 1)
             float c[NR][2][4];
+            float cl[kApart ? NR : 1][2][4];  // of the low parts (shorter chains, where there are registers)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int n = 0; n < NR; ++n)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) c[n][i][e] = off[n][e & 1];
-                uint32_t w[2][W];  // keys quad and quad + 8
+                    for (int e = 0; e < 4; ++e) c[n][i][e] = off[n][e & 1], cl[kApart ? n : 0][i][e] = 0.0f;
+            uint32_t w[4][W];  // keys quad + 8 y
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = 16 * i + 8 * h + quad, line = row / kLineRows;
-                    const int piece = (row % kLineRows) * (D / 32) + (D == 128 ? qi : qi >> 1);
-                    const unsigned char* at = st + line * 128 + ((piece ^ swizzled(line)) << 4);
-                    if constexpr (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(at);
-                        w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(at + (qi & 1) * 8);
-                        w[h][0] = v.x, w[h][1] = v.y;
-                    }
+            for (int y = 0; y < 4; ++y) {
+                const unsigned char* at = st + k_at + y * kEight;
+                if constexpr (D == 128) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(at);
+                    w[y][0] = v.x, w[y][1] = v.y, w[y][2] = v.z, w[y][3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(at);
+                    w[y][0] = v.x, w[y][1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2 * W; ++j) {  // a step: four channels of each lane, half a word
+                uint32_t a[4], a16[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    if (j & 1) w[y][j / 2] >>= 8;
+                    a[y] = half_centred(w[y][j / 2], 0x000F000Fu, 0xE408E408u);    // u - 8
+                    a16[y] = half_centred(w[y][j / 2], 0x00F000F0u, 0xE480E480u);  // 16 (u - 8)
                 }
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const uint32_t x = w[0][j], y = w[1][j], x8 = x >> 8, y8 = y >> 8;
-                    const uint32_t xa = mask_or(x, 0x000F000Fu, 0x64006400u), xb = mask_or(x, 0x00F000F0u, 0x64006400u);
-                    const uint32_t ya = mask_or(y, 0x000F000Fu, 0x64006400u), yb = mask_or(y, 0x00F000F0u, 0x64006400u);
-                    const uint32_t xc = mask_or(x8, 0x000F000Fu, 0x64006400u), xd = mask_or(x8, 0x00F000F0u, 0x64006400u);
-                    const uint32_t yc = mask_or(y8, 0x000F000Fu, 0x64006400u), yd = mask_or(y8, 0x00F000F0u, 0x64006400u);
+                for (int n = 0; n < NR; ++n) {
+                    const uint4 q = qs[(n * KS + j) * 32];
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        mma_f16(c[n][i], xa, ya, xb, yb, qf[n][2 * j][0], qf[n][2 * j][1]);
-                        mma_f16(c[n][i], xc, yc, xd, yd, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
+                    for (int i = 0; i < 2; ++i) {
+                        mma_f16(c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.x, q.y);
+                        mma_f16(kApart ? cl[kApart ? n : 0][i] : c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.z, q.w);
                     }
                 }
             }
@@ -354,28 +370,31 @@ pages4_rows_kernel(const PagedAttend4 p4) {
             float tk[4], tv[4];  // keys t0 + quad + 8 i
 #pragma unroll
             for (int i = 0; i < 4; ++i) tk[i] = kt[quad + 8 * i], tv[i] = vt[quad + 8 * i];
-            bool all = true;
+            bool whole = t0 + kUnit <= sees_all;
+            if constexpr (SCORED) {
+                bool all = true;
 #pragma unroll
-            for (int n = 0; n < NR; ++n) all = all && see[n][0].all(t0, t0 + kUnit) && see[n][1].all(t0, t0 + kUnit);
-            const bool whole = __all_sync(0xffffffffu, all);
+                for (int n = 0; n < NR; ++n) all = all && see[n][0].all(t0, t0 + kUnit) && see[n][1].all(t0, t0 + kUnit);
+                whole = __all_sync(0xffffffffu, all);
+            }
             bool move = false;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int h = e & 1, kk = 2 * i + (e >> 1), j = t0 + quad + 8 * kk;
-                        float x = c[n][i][e] * mul[n][h] * tk[kk];
+                        float x = (kApart ? c[n][i][e] + cl[kApart ? n : 0][i][e] : c[n][i][e]) * mul[n][h] * tk[kk];
                         if constexpr (SCORED) x = pages::score<SCORED>(p, x, slope2[n][h], pos[n][h], j);
                         if (!whole && !see[n][h].has(j)) x = -CUDART_INF_F;
                         c[n][i][e] = x;
-                        mx[h] = fmaxf(mx[h], x);
                     }
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    move = move || mx[h] > m[n][h] + kLazyMax || (m[n][h] == -CUDART_INF_F && mx[h] > m[n][h]);
+                for (int h = 0; h < 2; ++h) {
+                    const float mx = fmaxf(ptx::max3(c[n][0][h], c[n][0][2 + h], c[n][1][h]), c[n][1][2 + h]);
+                    move = move || mx > m[n][h] + kLazyMax;  // (any score above a reference of -inf)
+                }
             }
             if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -388,7 +407,6 @@ pages4_rows_kernel(const PagedAttend4 p4) {
                         // (nothing summed yet: sums of 0, or NaN, which stays)
                         const float al = m[n][h] == -CUDART_INF_F ? 1.0f : ptx::ex2(m[n][h] - mx);
                         l[n][h] *= al;
-                        sumw[n][h] *= al, sumw[n][2 + h] *= al;
 #pragma unroll
                         for (int q = 0; q < MB; ++q) O[n][q][h] *= al, O[n][q][2 + h] *= al;
                         m[n][h] = mx;
@@ -421,33 +439,30 @@ pages4_rows_kernel(const PagedAttend4 p4) {
                 uint32_t w[4][VW];  // keys 2 qi, 2 qi + 1, 8 more, one more
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const int row = 16 * i + 2 * qi + (y & 1) + 8 * (y >> 1), line = row / kLineRows;
-                    const int piece = (row % kLineRows) * (D / 32) + (D == 128 ? quad >> 1 : quad >> 2);
-                    const unsigned char* at = sv + line * 128 + ((piece ^ swizzled(line)) << 4);
+                    const unsigned char* at = sv + v_at[y & 1] + (2 * i + (y >> 1)) * kEight;
                     if constexpr (D == 128) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(at + (quad & 1) * 8);
+                        const uint2 v = *reinterpret_cast<const uint2*>(at);
                         w[y][0] = v.x, w[y][1] = v.y;
                     } else {
-                        w[y][0] = *reinterpret_cast<const uint32_t*>(at + (quad & 3) * 4);
+                        w[y][0] = *reinterpret_cast<const uint32_t*>(at);
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NR; ++n) mma_bf16(sumw[n], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, pb[n][i][0], pb[n][i][1]);
-#pragma unroll
                 for (int j = 0; j < VW; ++j) {
                     // even channels of both keys, odd ones; of the first eight keys, of the second
-                    uint32_t ev0 = ptx::prmt(w[0][j], w[1][j], 0x5410), od0 = ptx::prmt(w[0][j], w[1][j], 0x7632);
-                    uint32_t ev1 = ptx::prmt(w[2][j], w[3][j], 0x5410), od1 = ptx::prmt(w[2][j], w[3][j], 0x7632);
+                    const uint32_t ev0 = ptx::prmt(w[0][j], w[1][j], 0x5410), od0 = ptx::prmt(w[0][j], w[1][j], 0x7632);
+                    const uint32_t ev1 = ptx::prmt(w[2][j], w[3][j], 0x5410), od1 = ptx::prmt(w[2][j], w[3][j], 0x7632);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t a0 = centred(ev0), a1 = centred(od0), a2 = centred(ev1), a3 = centred(od1);
-                        ev0 >>= 4, od0 >>= 4, ev1 >>= 4, od1 >>= 4;
+                        auto nibble = [&](uint32_t x) { return centred(q ? x >> (4 * q - 1) : x << 1); };
+                        const uint32_t a0 = nibble(ev0), a1 = nibble(od0), a2 = nibble(ev1), a3 = nibble(od1);
 #pragma unroll
                         for (int n = 0; n < NR; ++n) mma_bf16(O[n][4 * j + q], a0, a1, a2, a3, pb[n][i][0], pb[n][i][1]);
                     }
                 }
             }
             __syncwarp();  // every lane has read the stage
+            st = st == sm + warp * (kStages * L::stage) + (kStages - 1) * L::stage ? sm + warp * (kStages * L::stage) : st + L::stage;
         }
         cp_wait<0>();
 #pragma unroll
@@ -465,10 +480,9 @@ pages4_rows_kernel(const PagedAttend4 p4) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float* dst = rows + (8 * n + 2 * qi + h) * RS;
-                const float half = 0.5f * sumw[n][h];
 #pragma unroll
                 for (int q = 0; q < MB; ++q)
-                    *reinterpret_cast<float2*>(dst + quad * (D / 8) + 2 * q) = make_float2(O[n][q][h] + half, O[n][q][2 + h] + half);
+                    *reinterpret_cast<float2*>(dst + quad * (D / 8) + 2 * q) = make_float2(O[n][q][h], O[n][q][2 + h]);
                 if (quad == 0) {
                     dst[D] = l[n][h] == 0.0f ? -CUDART_INF_F : (m[n][h] == -CUDART_INF_F ? 0.0f : m[n][h]);
                     dst[D + 1] = l[n][h];
@@ -479,7 +493,7 @@ pages4_rows_kernel(const PagedAttend4 p4) {
         // merge: 4 channels per item, whole warps (the transform crosses lanes)
         constexpr int C4 = D / 4;
         auto finish = [&](bool live, int r, int c4, float M, float Lt, float4 a) {
-            transform4<D>(a);
+            pages::transform4<D>(a);
             if (!live) return;
             const long long row = (long long)(b.q0 + token_of(r)) * p.Hq + head_of(r);
             const float inv = Lt == 0.0f ? 0.0f : 1.0f / Lt;
