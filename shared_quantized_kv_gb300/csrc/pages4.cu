@@ -25,7 +25,7 @@ int check_pages4(const kvpool_pages4_t* pg, int layer, kvpool_pages_t& v) {
     return KVPOOL_OK;
 }
 
-constexpr double kRowsReads = 1 << 17;
+constexpr double kRowsReads = 5 << 18;
 
 long long layer_vectors(const kvpool_pages4_t* pg) { return (long long)pg->pages * pg->kv_heads * pg->page_tokens; }
 
@@ -145,10 +145,10 @@ int kvpool_pages4_attend(const kvpool_pages4_t* pg, int layer, const kvpool_seqs
     a.Vt = pg->V_scale + at;
     a.a.out = static_cast<uint16_t*>(out);
     a.a.lse = lse;
-    // one block of rows per sequence, or few enough of them: the kernel for few rows
-    const long long blocks = (long long)seqs->seqs * (((long long)max_q * a.a.G + 31) / 32);
+    // blocks of 8 rows, each through all its keys: the kernel for few rows while these are few
+    const long long blocks = (long long)seqs->seqs * (((long long)max_q * a.a.G + 7) / 8);
     const double reads = (double)blocks * pg->kv_heads * max_kv;
-    if ((long long)max_q * a.a.G <= 32 || reads < kRowsReads)
+    if ((long long)max_q * a.a.G <= 16 || reads < kRowsReads)
         return map_cuda(
             kvp::launch_pages4_rows(a, pg->head_dim, max_q, max_kv, sms, static_cast<cudaStream_t>(stream)));
     return map_cuda(kvp::launch_pages4_chunk(a, pg->head_dim, max_q, max_kv, static_cast<cudaStream_t>(stream)));

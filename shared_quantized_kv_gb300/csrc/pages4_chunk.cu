@@ -1,15 +1,18 @@
 // Attention of many query rows per sequence over its pages in 4 bits: chunks of
 // new tokens, whole prompts (sm_103a, tcgen05).
 //
-// Mathematics as in pages4_rows.cu: <q, k> = t <H q, c> and O = H (sum p t' c'), c
-// = u - 7.5 of the codes, one pass with a running reference maximum. Here H q is
-// one fp16 number per channel (off by 2^-11 of each at most; the row's factor is
-// then chosen so that the rounded row's product with the row itself is exact,
-// which takes the part that the softmax's own tilt of the keys would sum up out
-// of the log of the sum), and a key's operand is fp16 c t / T with T a power of
-// two common to 32 keys (off by 2^-11 twice; where the 32 scales are further
-// apart than 2^10 the operand is c and the scale joins the score). V's operand is
-// bf16 c, exactly; the weights p t' are rounded to bf16 once.
+// Mathematics as in pages4_rows.cu for the values: O = H (sum p t' c'), c = u -
+// 7.5 of the codes, one pass with a running reference maximum; V's operand is bf16
+// c, exactly, and the weights p t' are rounded to bf16 once (off by 2^-8 of each at
+// most). The scores are taken the other way round: <q, k> = t <q, H c>, as H c = H
+// (u - 8) + (D / 2) e_0 is a vector of whole numbers up to 8 D + D / 2, which fp16
+// holds exactly, and so is q (bf16) once a power of two has brought the row's
+// largest value into [8, 16) (what lies 2^18 and more below it loses bits that are
+// 2^-29 of it). So the products are exact, with one MMA per operand pair;
+// transformed queries would need two fp16 parts (one alone is off by 2^-11, which
+// the log of the sum of a row with few keys shows), for which shared memory has no
+// room. The transform is H16 x H8 (H4 with D = 64): the first by small matrix
+// products, the second by additions.
 //
 // Bound: the tensor cores, 4 D FLOP per (row, key), with the instructions that
 // make operands of codes and weights of scores close behind. The frame is that
@@ -59,8 +62,8 @@ constexpr int kRegsIssue = 64, kRegsMany = 88, kRegsExpand = 64;
 // What the softmax needs to know of a tile's scales, beside the ring: a slot per tile
 struct TileScales {
     float v[kTile];     // V's
-    float k[kTile];     // K's over their common factor, where a group's operand is without them; else 1
-    uint32_t odd[4];    // of 32 keys: 1: K's scales are to join the scores, 2: V's are not all finite
+    float k[kTile];     // K's
+    uint32_t odd[4];    // of 32 keys: V's are not all finite
 };
 
 template <int D>
@@ -74,8 +77,7 @@ struct Lay {
     static constexpr int codes = 32 * D / 2;     // of an expander's share of a tile
     static constexpr int raw = ring + nst * stage;
     static constexpr int scales = raw + kExpanders * kRaw * codes;
-    static constexpr int common = scales + slots * (int)sizeof(TileScales);  // the factor of each group of 32 keys
-    static constexpr int rowf = common + 16;
+    static constexpr int rowf = scales + slots * (int)sizeof(TileScales);
     static constexpr int bars = rowf + kRows * 4;
     // barriers: full, empty per ring stage; per slot S, P (of each half), P V of the first, all done
     static constexpr int bar_s = bars + 2 * nst * 8, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_fin = bar_o + 16;
@@ -141,21 +143,21 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
 }
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     uint32_t y;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
 }
-// a word's eight channels as fp16 (u - 7.5) t, rounded once; t twice in a register
-__device__ __forceinline__ uint4 k_operand(uint32_t w, uint32_t t) {
-    const uint32_t w8 = w >> 8, half_t = hfma2(t, 0x38003800u, 0u);
-    auto even = [&](uint32_t x) {  // 1024 + u - 1032
-        return hfma2(hadd2(mask_or(x, 0x000F000Fu, 0x64006400u), 0xE408E408u), t, half_t);
-    };
-    auto odd = [&](uint32_t x) {  // (1024 + 16 u) / 16 - 72
-        return hfma2(hfma2(mask_or(x, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u), t, half_t);
-    };
-    return make_uint4(even(w), odd(w), even(w8), odd(w8));
+// codes in bits 0-3 of both halves -> fp16 u - 8
+__device__ __forceinline__ uint32_t k_pair(uint32_t x) {
+    return hadd2(mask_or(x, 0x000F000Fu, 0x64006400u), 0xE408E408u);
+}
+// d = A (16 keys x 16 channels) B (16 x 8) in fp16: whole numbers, exactly
+__device__ __forceinline__ void mma_half(uint32_t& d0, uint32_t& d1, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f16.f16.f16.f16 {%0,%1}, {%2,%3,%4,%5}, {%6,%7}, {%8,%8};"
+        : "=r"(d0), "=r"(d1)
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0u));
 }
 // a word's eight channels as bf16 u - 7.5, exactly: 64 + u - 71.5
 __device__ __forceinline__ uint4 v_operand(uint32_t w) {
@@ -166,19 +168,6 @@ __device__ __forceinline__ uint4 v_operand(uint32_t w) {
         return z;
     };
     return make_uint4(one(w << 1), one(w >> 3), one(w >> 7), one(w >> 11));
-}
-
-// Scores of a warp's rows in tensor memory, of 32 keys and of the 32 that come 64 later, times factors of the keys.
-__device__ __noinline__ void scale_scores(uint32_t at, const float* f) {
-    for (int h = 0; h < 2; ++h) {
-        uint32_t u[32];
-        ptx::tmem_ld32(at + 64 * h, u);
-        ptx::tmem_wait_ld(u);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) u[k] = asu(asf(u[k]) * f[64 * h + k]);
-        ptx::tmem_st32x(at + 64 * h, u);
-    }
-    ptx::tmem_wait_st();
 }
 
 // KIND: the causal mask alone; other masks too; scores that a cap or a bias by
@@ -449,8 +438,10 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
         // ---------------------------------------------------------- expanders
         // 32 keys of every tile each, in two halves of 16 (a page holds at least as
         // many). Codes come by asynchronous copies into the warp's own small ring, two
-        // entries ahead; D / 8 lanes then take a key, a word each, which becomes 16
-        // bytes of its row in the tile.
+        // entries ahead. V: D / 8 lanes take a key, a word each, which becomes 16 bytes of
+        // its row in the tile. K: 16 keys at a time are a matrix operand (u - 8) whose 16
+        // channels of a group the product with H16 transforms; the groups' results then
+        // go through the last stages in registers.
         constexpr int kLanes = D / 8, kKeys = 32 / kLanes;  // lanes of a key, keys at a time
         const int key0 = (warp - 20) * 32, in_row = lane % kLanes, in_key = lane / kLanes;
         const int32_t* table = s.table + (long long)b.seq * s.tstride;
@@ -493,13 +484,23 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             cp_commit();  // an empty group past the last entry keeps the count
         };
         float tk = 0.0f, tv = 0.0f;
-        uint32_t ex = 127;
         auto ask_scales = [&](int i) {  // lane: key key0 + lane
             const int at = vector_of(i, lane >> 4);
             const bool held = at >= 0 && i < n && tile_at(i) * kTile + key0 + lane < T;
             tk = held ? __ldg(p4.Kt + at + (lane & 15)) : 0.0f;
             tv = held ? __ldg(p4.Vt + at + (lane & 15)) : 0.0f;
         };
+        // H16's columns as operands: entry (k, n) is -1 to the ones that k and n share
+        const int quad = lane >> 2, qi = lane & 3;
+        uint32_t h16[2][2];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                auto sign = [&](int k) { return __popc(k & (quad + 8 * nb)) & 1 ? 0xBC00u : 0x3C00u; };
+                h16[nb][y] = sign(2 * qi + 8 * y) | sign(2 * qi + 8 * y + 1) << 16;
+            }
+        const uint32_t half_sum = qi == 0 ? (D == 128 ? 0x5400u : 0x5000u) : 0u;  // D / 2 to channel 0
         // where this lane's 16 bytes of a key go; (key & 7) changes by kKeys at a time
         const uint32_t to = (in_row / 8) * (kTile * 128) + (key0 + in_key) * 128;
         const uint32_t piece = (in_row % 8) ^ (in_key & 7);
@@ -517,30 +518,60 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             unsigned char* stage = sm + L::ring + (e % L::nst) * L::stage;
             if (is_k(e)) {
                 const int i = (e + 1) / 2;
-                // The scales' common factor 2^(ex - 127) is the power of two of the largest
-                // finite one of the first tile; where a later one is more than 2^10 below or
-                // 2^11 above it, the group's operands stay without scales.
-                const uint32_t bits = asu(fabsf(tk));
-                const bool fine = bits < 0x7F800000u;
-                if (e == 0) {
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, fine ? bits : 0u);
-                    ex = top == 0 ? 127u : min(max(top >> 23, 12u), 240u);
-                    if (lane == 0) *reinterpret_cast<float*>(sm + L::common + (key0 / 32) * 4) = asf(ex << 23);
-                }
-                const float part_of = tk * asf((254u - ex) << 23);
-                const bool wide = __any_sync(0xffffffffu, fine && bits && ((bits >> 23) + 10 < ex || (bits >> 23) > ex + 11));
                 const bool odd_v = __any_sync(0xffffffffu, !finite(tv));
-                const __half2 t2 = __float2half2_rn(wide ? 1.0f : part_of);
-                const uint32_t tt = *reinterpret_cast<const uint32_t*>(&t2);
                 if (e >= L::nst) warp_wait(b_empty + 8 * (e % L::nst), ((e / L::nst) - 1) & 1, bad);
                 TileScales& ts = tile_scales[i % L::slots];
                 ts.v[key0 + lane] = tv;
-                ts.k[key0 + lane] = wide ? part_of : 1.0f;
-                if (lane == 0) ts.odd[key0 / 32] = (wide ? 1u : 0u) | (odd_v ? 2u : 0u);
+                ts.k[key0 + lane] = tk;
+                if (lane == 0) ts.odd[key0 / 32] = odd_v;
                 ask_scales(i + 1);
-#pragma unroll 8
-                for (int j = 0; j < 32 / kKeys; ++j)
-                    *dst_of(stage, j) = k_operand(words[32 * j], __shfl_sync(0xffffffffu, tt, j * kKeys + in_key));
+                constexpr int kGroups = D / 16;
+                const unsigned char* own = raw + (e % kRaw) * L::codes;
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {  // keys 16 x + quad and + 8
+                    uint32_t z[2][kGroups][2];  // [key][group][half of its channels]
+#pragma unroll
+                    for (int g2 = 0; g2 < kGroups / 2; ++g2) {  // two groups: four words
+                        uint4 w[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            w[y] = *reinterpret_cast<const uint4*>(own + (16 * x + 8 * y + quad) * (D / 2) + g2 * 16);
+                        const int sh = 4 * qi;
+                        const uint32_t a0 = k_pair(w[0].x >> sh), a1 = k_pair(w[1].x >> sh);
+                        const uint32_t a2 = k_pair(w[0].y >> sh), a3 = k_pair(w[1].y >> sh);
+                        const uint32_t c0 = k_pair(w[0].z >> sh), c1 = k_pair(w[1].z >> sh);
+                        const uint32_t c2 = k_pair(w[0].w >> sh), c3 = k_pair(w[1].w >> sh);
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb) {
+                            mma_half(z[0][2 * g2][nb], z[1][2 * g2][nb], a0, a1, a2, a3, h16[nb][0], h16[nb][1]);
+                            mma_half(z[0][2 * g2 + 1][nb], z[1][2 * g2 + 1][nb], c0, c1, c2, c3, h16[nb][0], h16[nb][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                            for (int h = 1; h < kGroups; h <<= 1)
+#pragma unroll
+                                for (int q = 0; q < kGroups; ++q)
+                                    if (!(q & h)) {
+                                        const uint32_t a = z[y][q][nb], c = z[y][q + h][nb];
+                                        z[y][q][nb] = hadd2(a, c), z[y][q + h][nb] = hsub2(a, c);
+                                    }
+                        z[y][0][0] = hadd2(z[y][0][0], half_sum);
+                        // channels 16 q + 8 nb + 2 qi and the next: 4 bytes of piece 2 q + nb
+                        const int key = key0 + 16 * x + 8 * y + quad;  // (key & 7 is quad)
+#pragma unroll
+                        for (int q = 0; q < kGroups; ++q)
+#pragma unroll
+                            for (int nb = 0; nb < 2; ++nb) {
+                                const int pc = 2 * q + nb;
+                                *reinterpret_cast<uint32_t*>(stage + (pc / 8) * (kTile * 128) + key * 128 +
+                                                             (((pc % 8) ^ quad) << 4) + 4 * qi) = z[y][q][nb];
+                            }
+                    }
+                }
             } else {
                 if (e >= L::nst) warp_wait(b_empty + 8 * (e % L::nst), ((e / L::nst) - 1) & 1, bad);
 #pragma unroll 8
@@ -566,11 +597,11 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
         float m = -CUDART_INF_F, l = 0.0f;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         // ------------------------------------------------------------ softmax
-        // H q of the rows, a warp per row, in fp16 (rows past the block repeat its last)
+        // the rows, a warp each, in fp16 times a power of two (rows past the block repeat its last)
         float* rowf = reinterpret_cast<float*>(sm + L::rowf);
         {
             const int nq = two ? kRows : kTile;
-#pragma unroll 2
+#pragma unroll 4
             for (int r = warp - 4; r < nq; r += kSoftmax / 32) {
                 const int rr = min(r, nr - 1), i = pages::div_group(p, j_begin + rr);
                 const uint16_t* src = p.Q + (long long)(b.q0 + i_begin + i) * p.q_stride +
@@ -582,26 +613,16 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                 }
                 const uint32_t top = __reduce_max_sync(
                     0xffffffffu, max(max(asu(fabsf(x.x)), asu(fabsf(x.y))), max(asu(fabsf(x.z)), asu(fabsf(x.w)))));
-                const int e = min(max((int)(top >> 23) - 126, -126), 126);
-                const float down = asf((uint32_t)(127 - e) << 23);
-                x.x *= down, x.y *= down, x.z *= down, x.w *= down;
-                pages::transform4<D>(x);
-                const __half2 a = __floats2half2_rn(x.x, x.y), c = __floats2half2_rn(x.z, x.w);
-                const float2 fa = __half22float2(a), fc = __half22float2(c);
-                float yy = fmaf(x.x, x.x, x.y * x.y) + fmaf(x.z, x.z, x.w * x.w);
-                float yr = fmaf(x.x, fa.x, x.y * fa.y) + fmaf(x.z, fc.x, x.w * fc.y);
-#pragma unroll
-                for (int o = D / 8; o; o >>= 1) {
-                    yy += __shfl_xor_sync(0xffffffffu, yy, o);
-                    yr += __shfl_xor_sync(0xffffffffu, yr, o);
-                }
+                const int e = min(max((int)(top >> 23) - 126, -122), 126);
+                const float up = asf((uint32_t)(127 + 4 - e) << 23);
+                const __half2 a = __floats2half2_rn(x.x * up, x.y * up), c = __floats2half2_rn(x.z * up, x.w * up);
                 if (lane < D / 4) {
                     const int q = r & 127, ch = lane * 4;
                     *reinterpret_cast<uint2*>(sm + (r >> 7) * L::stage + (ch / 64) * (kTile * 128) + q * 128 +
                                               ((((ch % 64) / 8) ^ (q & 7)) << 4) + (ch & 4) * 2) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
                 }
-                if (lane == 0) rowf[r] = asf((uint32_t)(127 + e) << 23) * (yr > 0.0f ? yy / yr : 1.0f);
+                if (lane == 0) rowf[r] = asf((uint32_t)(127 - 4 + e) << 23);
             }
             ptx::fence_proxy_async();  // the MMAs read Q through the async proxy
         }
@@ -638,15 +659,15 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             return ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
                              ptx::max3(x[7], x[8], x[9]), x[10]);
         };
-        // what a tile's scales ask for beyond the common factors; K's join the scores here
-        auto odd_of = [&](const TileScales& ts) {
-            const uint4 o = *reinterpret_cast<const uint4*>(ts.odd);
-            const uint32_t all = o.x | o.y | o.z | o.w;
-            if (__builtin_expect(all & 1u, 0)) {
-                scale_scores(tS + 32 * part, ts.k + 32 * part);
-                ptx::bar_sync(b_pair, 64);  // (the pair's other warp has the other keys' scores)
+        // scores of 32 keys times their scales
+        auto times = [&](const float* t, uint32_t (&u)[32]) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(t + k);
+                const float2 x = __fmul2_rn(make_float2(asf(u[k]), asf(u[k + 1])), make_float2(f.x, f.y));
+                const float2 y = __fmul2_rn(make_float2(asf(u[k + 2]), asf(u[k + 3])), make_float2(f.z, f.w));
+                u[k] = asu(x.x), u[k + 1] = asu(x.y), u[k + 2] = asu(y.x), u[k + 3] = asu(y.y);
             }
-            return all;
         };
         // the row's reference becomes mt (its maximum in both parts) where that passes
         // it; O, which no MMA works on, follows
@@ -671,46 +692,40 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             }
             if (move) m = mt;
         };
-        // the factors of the thread's two groups of keys in every tile
-        const float* common = reinterpret_cast<const float*>(sm + L::common);
-        float f0 = 0.0f, f1 = 0.0f;
-        uint32_t odd = 0;
-        if (mine > 0 && some) {
-            warp_wait(b_s + 8 * w, 0, bad);
-            ptx::tc_fence_after();
-            f0 = mul * common[part], f1 = mul * common[2 + part];
-        }
         if (!SCORED && mine > 0 && some) {
             // The first reference is the maximum of the first half tile. (A row that
             // sees none of its keys sees none at all: the causal mask alone.)
             const int i0 = two ? 0 : w, t0 = (ta + i0) * kTile;  // (plain scores: no gap)
-            odd = odd_of(tile_scales[i0 % L::slots]);
+            warp_wait(b_s + 8 * w, 0, bad);
+            ptx::tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 64; c += 32) {
                 uint32_t u[32];
                 ptx::tmem_ld32(tS + c, u);
                 ptx::tmem_wait_ld(u);
+                times(tile_scales[i0 % L::slots].k + c, u);
                 mask(t0 + c, u, -CUDART_INF_F);
-                m = fmaxf(m, max_of(u) * (mul * common[c / 32]));
+                m = fmaxf(m, max_of(u) * mul);
             }
             // products of minus infinity alone are no reference: such a row is done again
             if (live && m == -CUDART_INF_F && see.some(t0, t0 + 64)) l = CUDART_NAN_F;
             ptx::bar_sync(b_pair, 64);  // P of either part overwrites what both have read
         }
         float top = -CUDART_INF_F;  // the part's maximum in the tile before
-        // the scores of the part's 32 keys from k0 on, -inf where the row sees none; what is left of their factor f
-        auto scores_of = [&](float f, int k0, bool whole, uint32_t (&u)[32]) {
+        constexpr bool kLeft = !CHANGED;  // the row's factor is left for the exponent
+        const float f = kLeft ? mul : 1.0f;
+        // the scores of the part's 32 keys from k0 on, -inf where the row sees none
+        auto scores_of = [&](const float* t, int k0, bool whole, uint32_t (&u)[32]) {
+            times(t, u);
             if constexpr (CHANGED) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) u[k] = asu(asf(u[k]) * f);
-                f = 1.0f;
+                for (int k = 0; k < 32; ++k) u[k] = asu(asf(u[k]) * mul);
                 const bool behind = p.slopes && __all_sync(0xffffffffu, !live || pos >= k0 + 31);
                 // (what an unseen place holds has no say in the form that a cap takes)
                 if (!whole && p.cap2 > 0.0f) mask(k0, u, 0.0f);
                 pages::scores32<KIND == kWideScores>(p, *reinterpret_cast<float (*)[32]>(u), slope2, pos, k0, behind, live);
             }
             if (!whole) mask(k0, u, -CUDART_INF_F);
-            return f;
         };
         for (int it = 0; it < mine; ++it) {
             const int i = two ? it : 2 * it + w;  // tile of this CTA
@@ -729,7 +744,6 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                 if (lane < 2) ptx::mbar_arrive(b_p + 16 * w + 8 * lane);
                 continue;
             }
-            if (SCORED || it > 0) odd = odd_of(ts);
             // (S came after every P V before it: O rests)
             if (moves) move_ref(top, true);
             top = -CUDART_INF_F;
@@ -740,7 +754,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                     uint32_t u[32];
                     ptx::tmem_ld32(tS + c, u);
                     ptx::tmem_wait_ld(u);
-                    const float f = scores_of(c < 64 ? f0 : f1, t0 + c, false, u);
+                    scores_of(ts.k + c, t0 + c, false, u);
                     top = fmaxf(top, max_of(u) * f);
                 }
                 if (ptx::bar_or(b_pair, 64, top > m + kLazy || (m == -CUDART_INF_F && top > m))) move_ref(top, it > 0);
@@ -762,7 +776,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                     uint32_t u[32];
                     ptx::tmem_ld32(tSh, u);
                     ptx::tmem_wait_ld(u);
-                    const float f = scores_of(h ? f1 : f0, k0, whole, u);
+                    scores_of(ts.k + in, k0, whole, u);
                     const float x = max_of(u) * f;
                     if constexpr (CHANGED) {
                         if (ptx::bar_or(b_pair, 64, x > m + kLazy || (m == -CUDART_INF_F && x > m))) {
@@ -783,7 +797,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                         sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                         return e;
                     };
-                    if (__builtin_expect(!(odd & 2u), 1)) {
+                    if (__builtin_expect(!ts.odd[in / 32], 1)) {
 #pragma unroll
                         for (int k = 0; k < 16; k += 2) {
                             const float4 t = *reinterpret_cast<const float4*>(&ts.v[in + 2 * k]);

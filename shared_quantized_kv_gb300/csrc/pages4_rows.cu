@@ -28,6 +28,7 @@
 // split the keys, in distributed shared memory: no workspace, no second launch.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "pages4.cuh"
 
@@ -41,8 +42,10 @@ constexpr int kUnit = 32;   // keys per unit
 constexpr int kStages = 3;  // units in a warp's ring
 constexpr float kLazyMax = 8.0f;
 constexpr int kMaxSplit = 16;
-// CTAs per SM, by their registers: 8, 16 and 32 rows
-constexpr int ctas_per_sm(int NR) { return NR == 1 ? 4 : NR == 2 ? 3 : 2; }
+// Sequences of fewer keys take H q in two fp16 parts.
+constexpr int kLowKeys = 16384;
+// CTAs per SM, by their registers: 8 and 16 rows
+constexpr int ctas_per_sm(int NR) { return NR == 1 ? 4 : 3; }
 
 template <int D, int NR>
 struct Lay {
@@ -125,7 +128,6 @@ pages4_rows_kernel(const PagedAttend4 p4) {
     constexpr int MB = D / 16;   // blocks of 16 channels of P V
     constexpr int W = D / 32;    // words of a key per lane in Q K^T
     constexpr int RS = L::rs;
-    constexpr bool kApart = NR == 1;
     const PagedAttend& p = p4.a;
     extern __shared__ __align__(128) unsigned char sm[];
     const PagedSeqs& s = p.s;
@@ -149,6 +151,7 @@ pages4_rows_kernel(const PagedAttend4 p4) {
         if (!pages::find_block(s, p.G, kRows, blockIdx.x / S, b)) return;
     }
     const int T = b.T;
+    const bool low = T < kLowKeys;  // H q in two parts
     const int32_t* table = s.table + (long long)b.seq * s.tstride;
 
     for (;; ++b.blk) {
@@ -174,21 +177,29 @@ pages4_rows_kernel(const PagedAttend4 p4) {
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
             x.x *= down, x.y *= down, x.z *= down, x.w *= down;
             pages::transform4<D>(x);
-            float sum = (x.x + x.y) + (x.z + x.w);
-#pragma unroll
-            for (int o = D / 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float4 y = x;
             // channels 4 l + 2 and + 3 meet 16 (u - 8)
             x.z *= 0.0625f, x.w *= 0.0625f;
             const __half2 h0 = __floats2half2_rn(x.x, x.y), h1 = __floats2half2_rn(x.z, x.w);
             const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
             const __half2 l0 = __floats2half2_rn(x.x - f0.x, x.y - f0.y), l1 = __floats2half2_rn(x.z - f1.x, x.w - f1.y);
+            // (with one part: the factor that makes the rounded row's product with the row itself exact)
+            float sum = low ? (y.x + y.y) + (y.z + y.w) : (f0.x + f0.y) + 16.0f * (f1.x + f1.y);
+            float yy = fmaf(y.x, y.x, y.y * y.y) + fmaf(y.z, y.z, y.w * y.w);
+            float yr = fmaf(y.x, f0.x, y.y * f0.y) + 16.0f * fmaf(y.z, f1.x, y.w * f1.y);
+#pragma unroll
+            for (int o = D / 8; o; o >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                yy += __shfl_xor_sync(0xffffffffu, yy, o);
+                yr += __shfl_xor_sync(0xffffffffu, yr, o);
+            }
             auto bits = [](const __half2& h) { return *reinterpret_cast<const uint32_t*>(&h); };
             if (lane < D / 4)  // step lane % KS of the quarter-row lane / KS
                 *reinterpret_cast<uint4*>(sm + L::q + (((r >> 3) * KS + lane % KS) * 32 + (r & 7) * 4 + lane / KS) * 16) =
                     make_uint4(bits(h0), bits(h1), bits(l0), bits(l1));
             if (lane == 0)
                 *reinterpret_cast<float2*>(sm + L::info + r * 8) =
-                    make_float2(0.5f * sum, __uint_as_float((uint32_t)(127 + e) << 23));
+                    make_float2(0.5f * sum, __uint_as_float((uint32_t)(127 + e) << 23) * (!low && yr > 0.0f ? yy / yr : 1.0f));
         }
         __syncthreads();
         float off[NR][2], mul[NR][2];  // of this lane's rows 8 n + 2 qi + h
@@ -328,13 +339,12 @@ pages4_rows_kernel(const PagedAttend4 p4) {
             const float* vt = kt + kUnit;
             // ---- scores: c[n][i][e]: key t0 + 16 i + quad (+ 8 for e >= 2), row 8 n + 2 qi + (e & 1)
             float c[NR][2][4];
-            float cl[kApart ? NR : 1][2][4];  // of the low parts (shorter chains, where there are registers)
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) c[n][i][e] = off[n][e & 1], cl[kApart ? n : 0][i][e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) c[n][i][e] = off[n][e & 1];
             uint32_t w[4][W];  // keys quad + 8 y
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -347,25 +357,30 @@ pages4_rows_kernel(const PagedAttend4 p4) {
                     w[y][0] = v.x, w[y][1] = v.y;
                 }
             }
+            auto products = [&](auto low) {
 #pragma unroll
-            for (int j = 0; j < 2 * W; ++j) {  // a step: four channels of each lane, half a word
-                uint32_t a[4], a16[4];
+                for (int j = 0; j < 2 * W; ++j) {  // a step: four channels of each lane, half a word
+                    uint32_t a[4], a16[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    if (j & 1) w[y][j / 2] >>= 8;
-                    a[y] = half_centred(w[y][j / 2], 0x000F000Fu, 0xE408E408u);    // u - 8
-                    a16[y] = half_centred(w[y][j / 2], 0x00F000F0u, 0xE480E480u);  // 16 (u - 8)
-                }
+                    for (int y = 0; y < 4; ++y) {
+                        if (j & 1) w[y][j / 2] >>= 8;
+                        a[y] = half_centred(w[y][j / 2], 0x000F000Fu, 0xE408E408u);    // u - 8
+                        a16[y] = half_centred(w[y][j / 2], 0x00F000F0u, 0xE480E480u);  // 16 (u - 8)
+                    }
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    const uint4 q = qs[(n * KS + j) * 32];
+                    for (int n = 0; n < NR; ++n) {
+                        const uint4 q = qs[(n * KS + j) * 32];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        mma_f16(c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.x, q.y);
-                        mma_f16(kApart ? cl[kApart ? n : 0][i] : c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.z, q.w);
+                        for (int i = 0; i < 2; ++i) {
+                            mma_f16(c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.x, q.y);
+                            if constexpr (decltype(low)::value)
+                                mma_f16(c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.z, q.w);
+                        }
                     }
                 }
-            }
+            };
+            if (low) products(std::true_type());
+            else products(std::false_type());
             // ---- weights
             float tk[4], tv[4];  // keys t0 + quad + 8 i
 #pragma unroll
@@ -383,9 +398,18 @@ pages4_rows_kernel(const PagedAttend4 p4) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float t = tk[2 * i + (e >> 1)];
+                        const float2 x = __fmul2_rn(__fmul2_rn(make_float2(c[n][i][e], c[n][i][e + 1]), make_float2(mul[n][0], mul[n][1])),
+                                                    make_float2(t, t));
+                        c[n][i][e] = x.x, c[n][i][e + 1] = x.y;
+                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int h = e & 1, kk = 2 * i + (e >> 1), j = t0 + quad + 8 * kk;
-                        float x = (kApart ? c[n][i][e] + cl[kApart ? n : 0][i][e] : c[n][i][e]) * mul[n][h] * tk[kk];
+                        float x = c[n][i][e];
                         if constexpr (SCORED) x = pages::score<SCORED>(p, x, slope2[n][h], pos[n][h], j);
                         if (!whole && !see[n][h].has(j)) x = -CUDART_INF_F;
                         c[n][i][e] = x;
@@ -415,21 +439,24 @@ pages4_rows_kernel(const PagedAttend4 p4) {
             uint32_t pb[NR][2][2];  // operands of P V: keys of 16 i, in two eights
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                const float ref[2] = {m[n][0] == -CUDART_INF_F ? 0.0f : m[n][0], m[n][1] == -CUDART_INF_F ? 0.0f : m[n][1]};
+                const float2 nref = make_float2(m[n][0] == -CUDART_INF_F ? 0.0f : -m[n][0], m[n][1] == -CUDART_INF_F ? 0.0f : -m[n][1]);
+                float2 sum = make_float2(l[n][0], l[n][1]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         const float t = tv[2 * i + (e >> 1)];
-                        const float w0 = ptx::ex2(c[n][i][e] - ref[0]), w1 = ptx::ex2(c[n][i][e + 1] - ref[1]);
-                        l[n][0] += w0, l[n][1] += w1;
-                        float v0 = w0 * t, v1 = w1 * t;
+                        const float2 d = __fadd2_rn(make_float2(c[n][i][e], c[n][i][e + 1]), nref);
+                        const float2 w = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
+                        sum = __fadd2_rn(sum, w);
+                        float2 v = __fmul2_rn(w, make_float2(t, t));
                         if (!whole) {  // what a masked place's scale holds has no say
-                            v0 = w0 == 0.0f ? 0.0f : v0;
-                            v1 = w1 == 0.0f ? 0.0f : v1;
+                            v.x = w.x == 0.0f ? 0.0f : v.x;
+                            v.y = w.y == 0.0f ? 0.0f : v.y;
                         }
-                        pb[n][i][e >> 1] = transposed(pack_bf2(v0, v1));
+                        pb[n][i][e >> 1] = transposed(pack_bf2(v.x, v.y));
                     }
+                l[n][0] = sum.x, l[n][1] = sum.y;
             }
             // ---- O += P V; lane: channels of the D / 8 from quad on, keys 2 qi, 2 qi + 1 of each eight
             const unsigned char* sv = st + L::codes;
@@ -610,11 +637,14 @@ cudaError_t launch_rows(const PagedAttend4& p, int max_q, int max_kv, int sm_cou
 
 cudaError_t launch_pages4_rows(const PagedAttend4& a, int head_dim, int max_q, int max_kv, int sm_count,
                                cudaStream_t st) {
+    // Blocks of 8 rows fill the GPU sooner and take less time to start; blocks of 16
+    // take the codes apart half as often, which pays where there are many units of
+    // keys (32 sequences of 16K keys, 16 rows: 233 us against 297; 8 of 4,096: 32
+    // against 26).
     const long long rows = (long long)max_q * a.a.G;
-#define KVP_PG4_ROWS(DD)                                                         \
-    (rows <= 8    ? launch_rows<DD, 1>(a, max_q, max_kv, sm_count, st)  \
-     : rows <= 16 ? launch_rows<DD, 2>(a, max_q, max_kv, sm_count, st)  \
-                  : launch_rows<DD, 4>(a, max_q, max_kv, sm_count, st))
+    const bool two = rows > 8 && (double)a.a.s.seqs * ((rows + 15) / 16) * a.a.s.Hk * max_kv >= (double)(1 << 20);
+#define KVP_PG4_ROWS(DD) \
+    (two ? launch_rows<DD, 2>(a, max_q, max_kv, sm_count, st) : launch_rows<DD, 1>(a, max_q, max_kv, sm_count, st))
     return head_dim == 64 ? KVP_PG4_ROWS(64) : KVP_PG4_ROWS(128);
 #undef KVP_PG4_ROWS
 }
