@@ -18,14 +18,15 @@
 // make operands of codes and weights of scores close behind. The frame is that
 // of pages_chunk.cu: up to 256 rows of one sequence and KV head per CTA, two
 // slots of tensor memory worked on in turn, key tiles of 128 in a ring, a
-// cluster's CTAs on shares of the keys. What differs: four warps take the place
-// of the loaders. They read codes (coalesced, the next tile's on their way in
-// registers), expand them into the swizzled tiles that the MMAs read, and note
-// each tile's scales beside the ring.
+// cluster's CTAs on shares of the keys. What differs: six warps take the place
+// of the loaders. They read codes (by copies into small rings of their own), expand
+// them into the swizzled tiles that the MMAs read, and note each tile's scales
+// beside them.
 //   warps 1, 2    issuers of the MMAs, one per slot
 //   warps 4-19    softmax, two threads per row of a slot: 32 keys of every 64
 //                 each, and half the channels of the output
-//   warps 20-23   expanders, 32 keys of every tile each
+//   warps 20-23   expanders of K, 32 keys of every tile each
+//   warps 0, 3    expanders of V, 64 keys of every tile each
 // Every wait on a barrier in memory is bounded; one that expires is recorded in
 // the status word, and the CTA runs to its end without waiting again.
 #include <algorithm>
@@ -50,11 +51,12 @@ constexpr float kLazyMax = 8.0f, kLazyScores = 60.0f;
 constexpr uint32_t kTryNs = 1000, kTries = 1u << 18;
 constexpr uint32_t kCols = 512;         // tensor memory: S0, S1, O0, O1
 // named barriers: Q is staged (issuers and softmax warps); every role is done; the merge rows are written;
-// a slot's turn at the tensor cores; the two warps of 32 rows (8 barriers)
-constexpr uint32_t kBarQ = 1, kBarDone = 2, kBarRows = 3, kBarTurn = 4, kBarPair = 6;
+// a slot's turn at the tensor cores; the two warps of 32 rows (8 barriers); the rows' factors are read
+constexpr uint32_t kBarQ = 1, kBarDone = 2, kBarRows = 3, kBarTurn = 4, kBarPair = 6, kBarRead = 14;
 constexpr int kSoftmax = 512;           // softmax threads
-constexpr int kExpanders = 4;           // expander warps, from warp 20 on
-constexpr int kRaw = 3;                 // entries of codes in an expander's own ring
+// expander warps of K (20 to 23, 32 keys of a tile each) and of V (0 and 3, 64 each), and how many times 32 keys'
+// codes their own rings hold
+constexpr int kWarpsK = 4, kWarpsV = 2, kRawK = 2, kRawV = 3;
 constexpr float kLn2 = 0.6931471805599453f;
 // registers: 6 warpgroups launched with 80 each; 64 + 4 x 88 + 64 = 6 x 80
 constexpr int kRegsIssue = 64, kRegsMany = 88, kRegsExpand = 64;
@@ -69,20 +71,20 @@ struct TileScales {
 template <int D>
 struct Lay {
     static constexpr int stage = kTile * D * 2;  // a K or V tile
-    static constexpr int nst = D == 128 ? 4 : 8;
-    // A tile's scales are written before its K: by then V of nst / 2 + 2 tiles
-    // before (4 or 6) has been released, so no softmax reads that slot any more.
-    static constexpr int slots = D == 128 ? 4 : 8;
-    static constexpr int ring = 2 * stage;       // after the two Q tiles
-    static constexpr int codes = 32 * D / 2;     // of an expander's share of a tile
-    static constexpr int raw = ring + nst * stage;
-    static constexpr int scales = raw + kExpanders * kRaw * codes;
-    static constexpr int rowf = scales + slots * (int)sizeof(TileScales);
-    static constexpr int bars = rowf + kRows * 4;
-    // barriers: full, empty per ring stage; per slot S, P (of each half), P V of the first, all done
-    static constexpr int bar_s = bars + 2 * nst * 8, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_fin = bar_o + 16;
+    static constexpr int nst = D == 128 ? 2 : 4; // of K, and as many of V
+    // A tile's scales are written before its K: by then the K of nst tiles before is
+    // released, and a softmax may still be at the tile before that one (where the
+    // slots take every second tile, one lets the other's next K pass early).
+    static constexpr int slots = nst + 2;
+    static constexpr int ring = 2 * stage;       // after the two Q tiles: K's stages, then V's
+    static constexpr int codes = 32 * D / 2;     // of 32 keys
+    static constexpr int raw = ring + 2 * nst * stage;
+    static constexpr int scales = raw + (kWarpsK * kRawK + kWarpsV * kRawV) * codes;
+    static constexpr int bars = scales + slots * (int)sizeof(TileScales);
+    // barriers: full, empty per stage of K, of V; per slot S, P (of each half), P V of the first, all done
+    static constexpr int bar_s = bars + 4 * nst * 8, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_fin = bar_o + 16;
     static constexpr int info = bar_fin + 16;  // rng[2][2], tensor memory address, prefixes' end, windows' begin
-    static constexpr int pair = info + 32;       // per slot a float per row, then a word per 32 rows
+    static constexpr int pair = info + 32;       // per slot a float per row (the rows' factors before), then a word per 32 rows
     static constexpr int total = pair + 2 * kTile * 4 + 32 + 1024;  // + alignment of the base
     static constexpr int rs = D + 4;             // floats of a merge row: O, m, l
     static_assert(kRows * (rs + kMaxParts) * 4 <= raw, "merge rows and weights fit in the tiles");
@@ -96,10 +98,6 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
 __device__ __forceinline__ float asf(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t asu(float f) { return __float_as_uint(f); }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < CUDART_INF_F; }
-
-// ring entries of tile i's K and V, of n tiles: K0 K1 V0 K2 V1 K3 ...
-__device__ __forceinline__ int k_entry(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int v_entry(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
 
 // Wait for phase `parity` of the barrier by a whole warp; after kTries tries
 // (each suspends the warp for a while; about a quarter of a second in all) `bad` is set, and
@@ -170,6 +168,62 @@ __device__ __forceinline__ uint4 v_operand(uint32_t w) {
     return make_uint4(one(w << 1), one(w >> 3), one(w >> 7), one(w >> 11));
 }
 
+// An expander warp's share of every tile, 16 * BLOCKS keys from key0 on: where its
+// codes lie (a page holds 16 keys at least), and copies of them on their way into
+// the warp's own ring, 32 keys to an entry.
+template <int D, int BLOCKS>
+struct CodeReader {
+    static constexpr int kTiles = 32 / BLOCKS;  // of one lookup, a lane per 16 keys
+    static constexpr int kEntries = BLOCKS / 2, kDepth = BLOCKS == 2 ? kRawK : kRawV;
+    static constexpr int kBytes = 32 * D / 2;
+    const PagedSeqs& s;
+    const int32_t* table;
+    int g, T, n, key0, lane, now, next, batch;
+    unsigned char* raw;
+    __device__ __forceinline__ CodeReader(const PagedAttend& p, const PagedSeqs& s_, int g_, int seq, int T_, int n_, int key0_,
+                                          int lane_, unsigned char* raw_)
+        : s(s_), table(s_.table + (long long)seq * s_.tstride), g(g_), T(T_), n(n_), key0(key0_), lane(lane_), raw(raw_) {}
+    // index of the vector of the first of the lane's 16 keys, -1 for none, in the m-th kTiles tiles
+    template <class F>
+    __device__ __forceinline__ int lookup(int m, F tile_at) const {
+        const int i = kTiles * m + lane / BLOCKS, t = i < n ? tile_at(i) * kTile + key0 + 16 * (lane % BLOCKS) : T;
+        if (t >= T) return -1;
+        const int page = __ldg(table + (t >> s.pshift));
+        if (page < 0 || page >= s.pages) {
+            pages::flag(s.status, kPgBadPage);
+            return -1;
+        }
+        return ((page * s.Hk + g) << s.pshift) + (t & ((1 << s.pshift) - 1));
+    }
+    template <class F>
+    __device__ __forceinline__ void start(F tile_at) {
+        batch = 0, now = lookup(0, tile_at), next = lookup(1, tile_at);
+    }
+    // tile i is under way: no tile before it is asked for any more
+    template <class F>
+    __device__ __forceinline__ void next_batch(int i, F tile_at) {
+        if (i < kTiles * (batch + 1)) return;
+        ++batch;
+        now = next, next = lookup(batch + 1, tile_at);
+    }
+    __device__ __forceinline__ int vector_of(int i, int block) const {
+        return __shfl_sync(0xffffffffu, i / kTiles == batch ? now : next, (i % kTiles) * BLOCKS + block);
+    }
+    __device__ __forceinline__ unsigned char* slot(int i, int c) const {
+        return raw + ((i * kEntries + c) % kDepth) * kBytes;
+    }
+    __device__ __forceinline__ void ask(const uint16_t* codes, int i, int c) const {
+        const uint32_t to = ptx::smem_u32(slot(i, c)) + lane * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = vector_of(i, 2 * c + h);
+            const unsigned char* src = reinterpret_cast<const unsigned char*>(codes) + (long long)max(at, 0) * (D / 2) + lane * 16;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) cp_async16(to + (h * (D / 64) + j) * 512, src + j * 512, at < 0 ? 0 : 16);
+        }
+    }
+};
+
 // KIND: the causal mask alone; other masks too; scores that a cap or a bias by
 // distance changes; the same with a cap so wide that each key takes a form of its own.
 enum { kPlain, kMasks, kScores, kWideScores };
@@ -208,12 +262,13 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
     // row r of the block: token row b.q0 + i_begin + div_group(j_begin + r), and the head of the group
     const int i_begin = r_begin / p.G, j_begin = r_begin - i_begin * p.G;
 
-    const uint32_t b_full = ptx::smem_u32(sm + L::bars), b_empty = b_full + 8 * L::nst;
+    // full, empty: of K's stages, V's nst further on
+    const uint32_t b_full = ptx::smem_u32(sm + L::bars), b_empty = b_full + 16 * L::nst;
     const uint32_t b_s = ptx::smem_u32(sm + L::bar_s), b_p = ptx::smem_u32(sm + L::bar_p);
     const uint32_t b_o = ptx::smem_u32(sm + L::bar_o), b_fin = ptx::smem_u32(sm + L::bar_fin);
     if (tid == 0) {
-        for (int i = 0; i < L::nst; ++i) {
-            ptx::mbar_init(b_full + 8 * i, kExpanders);
+        for (int i = 0; i < 2 * L::nst; ++i) {
+            ptx::mbar_init(b_full + 8 * i, i < L::nst ? kWarpsK : kWarpsV);
             ptx::mbar_init(b_empty + 8 * i, 2);  // both slots
         }
         for (int w = 0; w < 2; ++w) {
@@ -321,14 +376,18 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             const uint32_t tS = tm + kColS + 128 * slot, tO = tm + kColO + 128 * slot;
             const uint32_t idS = ptx::idesc_f16(kTile, kTile, 0, 0);
             const uint32_t idO = ptx::idesc_bf16(kTile, D, 0, 1);
-            const uint32_t u_full = base + L::bars, u_empty = u_full + 8 * L::nst;
+            const uint32_t u_full = base + L::bars, u_empty = u_full + 16 * L::nst;
             const uint32_t u_s = base + L::bar_s + 8 * slot, u_p = base + L::bar_p + 16 * slot;
             const uint32_t u_o = base + L::bar_o + 8 * slot, u_fin = base + L::bar_fin + 8 * slot;
             const uint64_t dq = ptx::sdesc(base + (pairs ? slot : 0) * L::stage, 16, 1024);
-            auto full = [&](int e) { warp_wait(u_full + 8 * (e % L::nst), (e / L::nst) & 1, bad); };
-            auto release = [&](int e) { ptx::mma_commit_elect(u_empty + 8 * (e % L::nst)); };
+            // an entry: K of tile i is 2 i, its V 2 i + 1; the stage that has it
+            auto k_entry = [](int i) { return 2 * i; };
+            auto v_entry = [](int i) { return 2 * i + 1; };
+            auto stage_of = [](int e) { return (e >> 1) % L::nst + (e & 1) * L::nst; };
+            auto full = [&](int e) { warp_wait(u_full + 8 * stage_of(e), ((e >> 1) / L::nst) & 1, bad); };
+            auto release = [&](int e) { ptx::mma_commit_elect(u_empty + 8 * stage_of(e)); };
             auto qk = [&](int e) {
-                const uint64_t dk = ptx::sdesc(ring + (e % L::nst) * L::stage, 16, 1024);
+                const uint64_t dk = ptx::sdesc(ring + stage_of(e) * L::stage, 16, 1024);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t o = ((ks / 4) * (kTile * 128) + (ks % 4) * 32) >> 4;  // descriptor units
@@ -337,7 +396,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                 ptx::mma_commit_elect(u_s);
             };
             auto pv = [&](int e, int it) {
-                const uint64_t dv = ptx::sdesc(ring + (e % L::nst) * L::stage, kTile * 128, 1024);
+                const uint64_t dv = ptx::sdesc(ring + stage_of(e) * L::stage, kTile * 128, 1024);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (h) {
@@ -373,7 +432,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             // a tile that the other slot alone works on: its K or V is not needed here
             auto pass = [&](int e) {
                 full(e);
-                if (lane == 0) ptx::mbar_arrive(u_empty + 8 * (e % L::nst));
+                if (lane == 0) ptx::mbar_arrive(u_empty + 8 * stage_of(e));
             };
             if (pairs) {
                 if (nn > 0) {
@@ -387,7 +446,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                     }
                 }
                 for (int i = 0; i < nn; ++i) {
-                    const int ev = v_entry(i, nn), ek = k_entry(i + 1);
+                    const int ev = v_entry(i), ek = k_entry(i + 1);
                     turn(i, nt > i, ev, nt > i + 1, ek);
                     if (nt <= i) pass(ev);
                     if (nt <= i + 1 && i + 1 < nn) pass(ek);
@@ -409,12 +468,12 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                 }
                 for (int i = 0; i < nn; i += 2) {
                     if (slot) {
-                        pass(v_entry(i, nn));
+                        pass(v_entry(i));
                         if (i + 2 < nn) pass(k_entry(i + 2));
                     }
-                    turn(i >> 1, i + slot < nn, v_entry(i + slot, nn), i + 2 + slot < nn, k_entry(i + 2 + slot));
+                    turn(i >> 1, i + slot < nn, v_entry(i + slot), i + 2 + slot < nn, k_entry(i + 2 + slot));
                     if (!slot) {
-                        if (i + 1 < nn) pass(v_entry(i + 1, nn));
+                        if (i + 1 < nn) pass(v_entry(i + 1));
                         if (i + 3 < nn) pass(k_entry(i + 3));
                     }
                 }
@@ -427,6 +486,45 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                 bad = bad || late;
             }
             __syncwarp();
+        } else {
+            // ---------------------------------------------- expanders of V
+            // D / 8 lanes take a key, a word each, which becomes 16 bytes of its row.
+            constexpr int kLanes = D / 8, kKeys = 32 / kLanes;  // lanes of a key, keys at a time
+            const int vw = warp / 3, in_row = lane % kLanes, in_key = lane / kLanes;
+            CodeReader<D, 4> in(p, s, g, b.seq, T, n, vw * 64, lane,
+                                sm + L::raw + (kWarpsK * kRawK + vw * kRawV) * L::codes);
+            auto tile_of = [&](int i) { return tile_at(i); };
+            in.start(tile_of);
+            // (key & 7) changes by kKeys at a time
+            const uint32_t to = (in_row / 8) * (kTile * 128) + (vw * 64 + in_key) * 128;
+            const uint32_t piece = (in_row % 8) ^ (in_key & 7);
+            if (n > 0) in.ask(p.V, 0, 0);
+            cp_commit();
+            if (n > 0) in.ask(p.V, 0, 1);
+            cp_commit();
+            for (int i = 0; i < n; ++i) {
+                const int st = i % L::nst;
+                unsigned char* stage = sm + L::ring + (L::nst + st) * L::stage;
+                if (i >= L::nst) warp_wait(b_empty + 8 * (L::nst + st), ((i / L::nst) - 1) & 1, bad);
+                in.next_batch(i, tile_of);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {  // 32 keys
+                    if (i + 1 < n) in.ask(p.V, i + 1, c);
+                    cp_commit();
+                    cp_wait<2>();
+                    __syncwarp();
+                    const uint32_t* words = reinterpret_cast<const uint32_t*>(in.slot(i, c)) + lane;
+#pragma unroll 8
+                    for (int j = 0; j < 32 / kKeys; ++j)
+                        *reinterpret_cast<uint4*>(stage + to + (32 * c + j * kKeys) * 128 +
+                                                  ((piece ^ ((j * kKeys) & 7)) << 4)) = v_operand(words[32 * j]);
+                    __syncwarp();  // (the codes are read)
+                }
+                ptx::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_full + 8 * (L::nst + st));
+            }
+            cp_wait<0>();
         }
         if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
         if (!direct) {
@@ -435,57 +533,17 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
         }
     } else if (warp >= 20) {
         ptx::regs_dec<kRegsExpand>();
-        // ---------------------------------------------------------- expanders
-        // 32 keys of every tile each, in two halves of 16 (a page holds at least as
-        // many). Codes come by asynchronous copies into the warp's own small ring, two
-        // entries ahead. V: D / 8 lanes take a key, a word each, which becomes 16 bytes of
-        // its row in the tile. K: 16 keys at a time are a matrix operand (u - 8) whose 16
-        // channels of a group the product with H16 transforms; the groups' results then
-        // go through the last stages in registers.
-        constexpr int kLanes = D / 8, kKeys = 32 / kLanes;  // lanes of a key, keys at a time
-        const int key0 = (warp - 20) * 32, in_row = lane % kLanes, in_key = lane / kLanes;
-        const int32_t* table = s.table + (long long)b.seq * s.tstride;
-        const unsigned char* codes_k = reinterpret_cast<const unsigned char*>(p.K) + lane * 16;
-        const unsigned char* codes_v = reinterpret_cast<const unsigned char*>(p.V) + lane * 16;
-        unsigned char* raw = sm + L::raw + (warp - 20) * (kRaw * L::codes);
-        const uint32_t raw_at = ptx::smem_u32(raw) + lane * 16;
-        // Index of the vector of the first of 16 keys, -1 for none: of 16 tiles from
-        // 16 m on, two lanes per tile; the 16 tiles in use, and the next.
-        auto lookup = [&](int m) {
-            const int i = 16 * m + (lane >> 1), t = i < n ? tile_at(i) * kTile + key0 + 16 * (lane & 1) : T;
-            if (t >= T) return -1;
-            const int page = __ldg(table + (t >> s.pshift));
-            if (page < 0 || page >= s.pages) {
-                pages::flag(s.status, kPgBadPage);
-                return -1;
-            }
-            return ((page * s.Hk + g) << s.pshift) + (t & ((1 << s.pshift) - 1));
-        };
-        int now = lookup(0), next = lookup(1), batch = 0;
-        auto vector_of = [&](int i, int h) {
-            return __shfl_sync(0xffffffffu, (i >> 4) == batch ? now : next, (i & 15) * 2 + h);
-        };
-        // entry e's codes: K of tile (e + 1) / 2, or V of tile e / 2 - 1, of the last one at the end
-        auto is_k = [&](int e) { return e == 0 || ((e & 1) && e < 2 * n - 1); };
-        auto ask = [&](int e) {
-            if (e < 2 * n) {
-                const bool k = is_k(e);
-                const int i = k ? (e + 1) / 2 : e == 2 * n - 1 ? n - 1 : e / 2 - 1;
-                const uint32_t to = raw_at + (e % kRaw) * L::codes;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int at = vector_of(i, h);
-                    const unsigned char* src = (k ? codes_k : codes_v) + (long long)max(at, 0) * (D / 2);
-#pragma unroll
-                    for (int j = 0; j < D / 64; ++j)
-                        cp_async16(to + (h * (D / 64) + j) * 512, src + j * 512, at < 0 ? 0 : 16);
-                }
-            }
-            cp_commit();  // an empty group past the last entry keeps the count
-        };
+        // -------------------------------------------------- expanders of K
+        // 16 keys at a time are a matrix operand (u - 8) whose 16 channels of a group the
+        // product with H16 transforms; the groups' results then go through the last
+        // stages in registers.
+        const int key0 = (warp - 20) * 32;
+        CodeReader<D, 2> in(p, s, g, b.seq, T, n, key0, lane, sm + L::raw + (warp - 20) * (kRawK * L::codes));
+        auto tile_of = [&](int i) { return tile_at(i); };
+        in.start(tile_of);
         float tk = 0.0f, tv = 0.0f;
         auto ask_scales = [&](int i) {  // lane: key key0 + lane
-            const int at = vector_of(i, lane >> 4);
+            const int at = in.vector_of(i, lane >> 4);
             const bool held = at >= 0 && i < n && tile_at(i) * kTile + key0 + lane < T;
             tk = held ? __ldg(p4.Kt + at + (lane & 15)) : 0.0f;
             tv = held ? __ldg(p4.Vt + at + (lane & 15)) : 0.0f;
@@ -501,90 +559,74 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                 h16[nb][y] = sign(2 * qi + 8 * y) | sign(2 * qi + 8 * y + 1) << 16;
             }
         const uint32_t half_sum = qi == 0 ? (D == 128 ? 0x5400u : 0x5000u) : 0u;  // D / 2 to channel 0
-        // where this lane's 16 bytes of a key go; (key & 7) changes by kKeys at a time
-        const uint32_t to = (in_row / 8) * (kTile * 128) + (key0 + in_key) * 128;
-        const uint32_t piece = (in_row % 8) ^ (in_key & 7);
-        auto dst_of = [&](unsigned char* stage, int j) {
-            return reinterpret_cast<uint4*>(stage + to + j * kKeys * 128 + ((piece ^ ((j * kKeys) & 7)) << 4));
-        };
         ask_scales(0);
-#pragma unroll
-        for (int e = 0; e < kRaw - 1; ++e) ask(e);
-        for (int e = 0; e < 2 * n; ++e) {
-            ask(e + kRaw - 1);
-            cp_wait<kRaw - 1>();
+        in.ask(p.K, 0, 0);
+        cp_commit();
+        for (int i = 0; i < n; ++i) {
+            if (i + 1 < n) in.ask(p.K, i + 1, 0);
+            cp_commit();
+            cp_wait<1>();
             __syncwarp();
-            const uint32_t* words = reinterpret_cast<const uint32_t*>(raw + (e % kRaw) * L::codes) + lane;
-            unsigned char* stage = sm + L::ring + (e % L::nst) * L::stage;
-            if (is_k(e)) {
-                const int i = (e + 1) / 2;
-                const bool odd_v = __any_sync(0xffffffffu, !finite(tv));
-                if (e >= L::nst) warp_wait(b_empty + 8 * (e % L::nst), ((e / L::nst) - 1) & 1, bad);
-                TileScales& ts = tile_scales[i % L::slots];
-                ts.v[key0 + lane] = tv;
-                ts.k[key0 + lane] = tk;
-                if (lane == 0) ts.odd[key0 / 32] = odd_v;
-                ask_scales(i + 1);
-                constexpr int kGroups = D / 16;
-                const unsigned char* own = raw + (e % kRaw) * L::codes;
+            const bool odd_v = __any_sync(0xffffffffu, !finite(tv));
+            const int st = i % L::nst;
+            unsigned char* stage = sm + L::ring + st * L::stage;
+            if (i >= L::nst) warp_wait(b_empty + 8 * st, ((i / L::nst) - 1) & 1, bad);
+            TileScales& ts = tile_scales[i % L::slots];
+            ts.v[key0 + lane] = tv;
+            ts.k[key0 + lane] = tk;
+            if (lane == 0) ts.odd[key0 / 32] = odd_v;
+            in.next_batch(i, tile_of);
+            ask_scales(i + 1);
+            constexpr int kGroups = D / 16;
+            const unsigned char* own = in.slot(i, 0);
 #pragma unroll 1
-                for (int x = 0; x < 2; ++x) {  // keys 16 x + quad and + 8
-                    uint32_t z[2][kGroups][2];  // [key][group][half of its channels]
+            for (int x = 0; x < 2; ++x) {  // keys 16 x + quad and + 8
+                uint32_t z[2][kGroups][2];  // [key][group][half of its channels]
 #pragma unroll
-                    for (int g2 = 0; g2 < kGroups / 2; ++g2) {  // two groups: four words
-                        uint4 w[2];
+                for (int g2 = 0; g2 < kGroups / 2; ++g2) {  // two groups: four words
+                    uint4 w[2];
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            w[y] = *reinterpret_cast<const uint4*>(own + (16 * x + 8 * y + quad) * (D / 2) + g2 * 16);
-                        const int sh = 4 * qi;
-                        const uint32_t a0 = k_pair(w[0].x >> sh), a1 = k_pair(w[1].x >> sh);
-                        const uint32_t a2 = k_pair(w[0].y >> sh), a3 = k_pair(w[1].y >> sh);
-                        const uint32_t c0 = k_pair(w[0].z >> sh), c1 = k_pair(w[1].z >> sh);
-                        const uint32_t c2 = k_pair(w[0].w >> sh), c3 = k_pair(w[1].w >> sh);
+                    for (int y = 0; y < 2; ++y)
+                        w[y] = *reinterpret_cast<const uint4*>(own + (16 * x + 8 * y + quad) * (D / 2) + g2 * 16);
+                    const int sh = 4 * qi;
+                    const uint32_t a0 = k_pair(w[0].x >> sh), a1 = k_pair(w[1].x >> sh);
+                    const uint32_t a2 = k_pair(w[0].y >> sh), a3 = k_pair(w[1].y >> sh);
+                    const uint32_t c0 = k_pair(w[0].z >> sh), c1 = k_pair(w[1].z >> sh);
+                    const uint32_t c2 = k_pair(w[0].w >> sh), c3 = k_pair(w[1].w >> sh);
 #pragma unroll
-                        for (int nb = 0; nb < 2; ++nb) {
-                            mma_half(z[0][2 * g2][nb], z[1][2 * g2][nb], a0, a1, a2, a3, h16[nb][0], h16[nb][1]);
-                            mma_half(z[0][2 * g2 + 1][nb], z[1][2 * g2 + 1][nb], c0, c1, c2, c3, h16[nb][0], h16[nb][1]);
-                        }
-                    }
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-#pragma unroll
-                        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                            for (int h = 1; h < kGroups; h <<= 1)
-#pragma unroll
-                                for (int q = 0; q < kGroups; ++q)
-                                    if (!(q & h)) {
-                                        const uint32_t a = z[y][q][nb], c = z[y][q + h][nb];
-                                        z[y][q][nb] = hadd2(a, c), z[y][q + h][nb] = hsub2(a, c);
-                                    }
-                        z[y][0][0] = hadd2(z[y][0][0], half_sum);
-                        // channels 16 q + 8 nb + 2 qi and the next: 4 bytes of piece 2 q + nb
-                        const int key = key0 + 16 * x + 8 * y + quad;  // (key & 7 is quad)
-#pragma unroll
-                        for (int q = 0; q < kGroups; ++q)
-#pragma unroll
-                            for (int nb = 0; nb < 2; ++nb) {
-                                const int pc = 2 * q + nb;
-                                *reinterpret_cast<uint32_t*>(stage + (pc / 8) * (kTile * 128) + key * 128 +
-                                                             (((pc % 8) ^ quad) << 4) + 4 * qi) = z[y][q][nb];
-                            }
+                    for (int nb = 0; nb < 2; ++nb) {
+                        mma_half(z[0][2 * g2][nb], z[1][2 * g2][nb], a0, a1, a2, a3, h16[nb][0], h16[nb][1]);
+                        mma_half(z[0][2 * g2 + 1][nb], z[1][2 * g2 + 1][nb], c0, c1, c2, c3, h16[nb][0], h16[nb][1]);
                     }
                 }
-            } else {
-                if (e >= L::nst) warp_wait(b_empty + 8 * (e % L::nst), ((e / L::nst) - 1) & 1, bad);
-#pragma unroll 8
-                for (int j = 0; j < 32 / kKeys; ++j) *dst_of(stage, j) = v_operand(words[32 * j]);
-                if ((e >> 1) >= 16 * (batch + 1)) {  // (tiles before e / 2 - 1 are done with)
-                    now = next;
-                    ++batch;
-                    next = lookup(batch + 1);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                        for (int h = 1; h < kGroups; h <<= 1)
+#pragma unroll
+                            for (int q = 0; q < kGroups; ++q)
+                                if (!(q & h)) {
+                                    const uint32_t a = z[y][q][nb], c = z[y][q + h][nb];
+                                    z[y][q][nb] = hadd2(a, c), z[y][q + h][nb] = hsub2(a, c);
+                                }
+                    z[y][0][0] = hadd2(z[y][0][0], half_sum);
+                    // channels 16 q + 8 nb + 2 qi and the next: 4 bytes of piece 2 q + nb
+                    const int key = key0 + 16 * x + 8 * y + quad;  // (key & 7 is quad)
+#pragma unroll
+                    for (int q = 0; q < kGroups; ++q)
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb) {
+                            const int pc = 2 * q + nb;
+                            *reinterpret_cast<uint32_t*>(stage + (pc / 8) * (kTile * 128) + key * 128 +
+                                                         (((pc % 8) ^ quad) << 4) + 4 * qi) = z[y][q][nb];
+                        }
                 }
             }
             ptx::fence_proxy_async();
-            __syncwarp();  // (and the raw words are read)
-            if (lane == 0) ptx::mbar_arrive(b_full + 8 * (e % L::nst));
+            __syncwarp();  // (and the codes are read)
+            if (lane == 0) ptx::mbar_arrive(b_full + 8 * st);
         }
         cp_wait<0>();
         if (bad && lane == 0) pages::flag(s.status, kPgTimeout);
@@ -598,7 +640,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         // ------------------------------------------------------------ softmax
         // the rows, a warp each, in fp16 times a power of two (rows past the block repeat its last)
-        float* rowf = reinterpret_cast<float*>(sm + L::rowf);
+        float* rowf = reinterpret_cast<float*>(sm + L::pair);
         {
             const int nq = two ? kRows : kTile;
 #pragma unroll 4
@@ -631,6 +673,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
         const bool some = __any_sync(0xffffffffu, live);
         const float slope2 = SCORED && live && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.0f;
         const float mul = rowf[two ? w * kTile + lr : lr] * (CHANGED ? 1.0f : p.scale_log2);
+        ptx::bar_sync(kBarRead, kSoftmax);  // (its place is used for other things from here on)
         const uint32_t tS = tmem + kColS + 128 * w + lane_off, tO = tmem + kColO + 128 * w + lane_off;
         float* xch = reinterpret_cast<float*>(sm + L::pair) + w * kTile + lr;
         const uint32_t b_pair = kBarPair + 4 * w + (warp & 3);
