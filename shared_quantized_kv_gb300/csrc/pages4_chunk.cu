@@ -58,8 +58,8 @@ constexpr int kSoftmax = 512;           // softmax threads
 // codes their own rings hold
 constexpr int kWarpsK = 4, kWarpsV = 2, kRawK = 2, kRawV = 3;
 constexpr float kLn2 = 0.6931471805599453f;
-// registers: 6 warpgroups launched with 80 each; 64 + 4 x 88 + 64 = 6 x 80
-constexpr int kRegsIssue = 64, kRegsMany = 88, kRegsExpand = 64;
+// registers: 6 warpgroups launched with 80 each; 56 + 4 x 88 + 72 = 6 x 80
+constexpr int kRegsIssue = 56, kRegsMany = 88, kRegsExpand = 72;
 
 // What the softmax needs to know of a tile's scales, beside the ring: a slot per tile
 struct TileScales {

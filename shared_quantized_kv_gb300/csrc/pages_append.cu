@@ -273,60 +273,95 @@ append_kernel(const AppendArgs a) {
     }
 }
 
-// Tokens of the 4-bit pages as bf16 rows: t H (u - 7.5). The sums are of halves
-// of whole numbers, exact in float32 in any order.
+// Tokens of the 4-bit pages as bf16 rows: t H (u - 7.5) = t (H (u - 8) + (D / 2)
+// e_0). The sums are whole numbers up to 8 D + D / 2, exact in fp16 in any order,
+// two to a register; one rounding to float32 with t, one to bf16. A warp takes a
+// token, its D / 16 lanes a head-vector, several of them asked for at once.
+constexpr int kReadWarps = 4, kReadAhead = 4;
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t as_bits(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+// the eight u - 8 of a word, neighbouring channels in a register
+__device__ __forceinline__ void levels(uint32_t w, __half2 (&x)[4]) {
+    const __half2 even = as_half2(0xE408E408u), odd = as_half2(0xD480D480u), part = as_half2(0x2C002C00u);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t v = k ? w >> 8 : w;
+        x[2 * k] = __hadd2(as_half2((v & 0x000F000Fu) | 0x64006400u), even);             // 1024 + u - 1032
+        x[2 * k + 1] = __hfma2(as_half2((v & 0x00F000F0u) | 0x64006400u), part, odd);  // (1024 + 16 u) / 16 - 72
+    }
+}
+
 template <int D>
-__global__ void __launch_bounds__(kAppThreads)
+__global__ void __launch_bounds__(kReadWarps * 32)
 read_kernel(const PagedSeqs s, const uint32_t* __restrict__ Kc, const uint32_t* __restrict__ Vc,
             const float* __restrict__ Kt, const float* __restrict__ Vt, uint16_t* __restrict__ K,
             uint16_t* __restrict__ V) {
-    constexpr int L = D / 16, kSlots = kAppThreads / L;
-    const int tok = blockIdx.x, slot = threadIdx.x / L, j = threadIdx.x % L, lane = threadIdx.x & 31;
+    constexpr int L = D / 16, kVectors = 32 / L;  // lanes of a vector, vectors of a warp at a time
+    const int tok = blockIdx.x * kReadWarps + threadIdx.x / 32, lane = threadIdx.x & 31, j = lane % L;
+    if (tok >= s.tokens) return;
     int pos;
     long long vec;
     if (!place_of(s, tok, pos, vec)) return;
-    for (int v0 = 0; v0 < 2 * s.Hk; v0 += kSlots) {
-        const int v = v0 + slot;
-        const bool mine = v < 2 * s.Hk, k = v < s.Hk;
-        const int h = k ? v : v - s.Hk;
-        uint32_t w0 = 0, w1 = 0;
-        float t = 0.0f;
-        if (mine && vec >= 0) {
-            const long long at = vec + ((long long)h << s.pshift);
-            const uint32_t* from = (k ? Kc : Vc) + at * (D / 8) + j;
-            w0 = __ldg(from), w1 = __ldg(from + L), t = __ldg((k ? Kt : Vt) + at);
-        }
-        float x0[8], x1[8];
+    const __half2 first = j == 0 ? __floats2half2_rn(D / 2, 0.0f) : __floats2half2_rn(0.0f, 0.0f);
+    const __half2 turn = __floats2half2_rn(1.0f, -1.0f);
+    for (int v0 = lane / L; v0 - lane / L < 2 * s.Hk; v0 += kVectors * kReadAhead) {
+        uint32_t w0[kReadAhead], w1[kReadAhead];
+        float t[kReadAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int sh = 2 * (i & 6) + 16 * (i & 1);
-            const float a = (float)(w0 >> sh & 15) - 7.5f, b = (float)(w1 >> sh & 15) - 7.5f;
-            x0[i] = a + b, x1[i] = a - b;  // the halves' stage
-        }
-#pragma unroll
-        for (int n = 1; n < 8; n <<= 1)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!(i & n)) {
-                    float a = x0[i], b = x0[i + n];
-                    x0[i] = a + b, x0[i + n] = a - b;
-                    a = x1[i], b = x1[i + n];
-                    x1[i] = a + b, x1[i + n] = a - b;
-                }
-#pragma unroll
-        for (int o = 1; o < L; o <<= 1) {
-            const float sign = lane & o ? -1.0f : 1.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x0[i] = fmaf(sign, x0[i], __shfl_xor_sync(0xffffffffu, x0[i], o));
-                x1[i] = fmaf(sign, x1[i], __shfl_xor_sync(0xffffffffu, x1[i], o));
+        for (int u = 0; u < kReadAhead; ++u) {
+            const int v = v0 + kVectors * u;
+            w0[u] = w1[u] = 0x88888888u;  // (tokens without a page: zeros)
+            t[u] = 0.0f;
+            if (v < 2 * s.Hk && vec >= 0) {
+                const bool k = v < s.Hk;
+                const long long at = vec + ((long long)(k ? v : v - s.Hk) << s.pshift);
+                const uint32_t* from = (k ? Kc : Vc) + at * (D / 8) + j;
+                w0[u] = __ldg(from), w1[u] = __ldg(from + L), t[u] = __ldg((k ? Kt : Vt) + at);
             }
         }
-        if (mine) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x0[i] = vec < 0 ? 0.0f : x0[i] * t, x1[i] = vec < 0 ? 0.0f : x1[i] * t;
-            uint4* to = reinterpret_cast<uint4*>((k ? K : V) + ((long long)tok * s.Hk + h) * D) + j;
-            to[0] = pack8(x0), to[L] = pack8(x1);
+        for (int u = 0; u < kReadAhead; ++u) {
+            const int v = v0 + kVectors * u;
+            if (v - lane / L >= 2 * s.Hk) break;  // (the whole warp's)
+            __half2 x[8], a[4], c[4];  // channels 8 j ..., and D / 2 further on
+            levels(w0[u], a);
+            levels(w1[u], c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __hadd2(a[i], c[i]), x[4 + i] = __hsub2(a[i], c[i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __hfma2(x[i], turn, __lowhigh2highlow(x[i]));  // neighbours
+#pragma unroll
+            for (int h = 1; h < 4; h <<= 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!(i & h)) {
+                        const __half2 p = x[i], q = x[i + h];
+                        x[i] = __hadd2(p, q), x[i + h] = __hsub2(p, q);
+                    }
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) {
+                const __half2 sign = lane & o ? __floats2half2_rn(-1.0f, -1.0f) : __floats2half2_rn(1.0f, 1.0f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = __hfma2(x[i], sign, as_half2(__shfl_xor_sync(0xffffffffu, as_bits(x[i]), o)));
+            }
+            x[0] = __hadd2(x[0], first);
+            if (v < 2 * s.Hk) {
+                const bool k = v < s.Hk;
+                uint4* to = reinterpret_cast<uint4*>((k ? K : V) + ((long long)tok * s.Hk + (k ? v : v - s.Hk)) * D) + j;
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 z = __half22float2(x[4 * i + e]);
+                        // (a page that is not there reads as zeros whatever the sum)
+                        y[2 * e] = z.x * t[u], y[2 * e + 1] = z.y * t[u];
+                    }
+                    to[i * L] = pack8(y);
+                }
+            }
         }
     }
 }
@@ -352,8 +387,9 @@ cudaError_t launch_append(const AppendArgs& a, int head_dim, bool four, cudaStre
 
 cudaError_t launch_pages4_read(const PagedSeqs& s, int head_dim, const uint32_t* Kc, const uint32_t* Vc, const float* Kt,
                                const float* Vt, uint16_t* K, uint16_t* V, cudaStream_t st) {
-    if (head_dim == 64) read_kernel<64><<<s.tokens, kAppThreads, 0, st>>>(s, Kc, Vc, Kt, Vt, K, V);
-    else read_kernel<128><<<s.tokens, kAppThreads, 0, st>>>(s, Kc, Vc, Kt, Vt, K, V);
+    const int grid = (s.tokens + kReadWarps - 1) / kReadWarps;
+    if (head_dim == 64) read_kernel<64><<<grid, kReadWarps * 32, 0, st>>>(s, Kc, Vc, Kt, Vt, K, V);
+    else read_kernel<128><<<grid, kReadWarps * 32, 0, st>>>(s, Kc, Vc, Kt, Vt, K, V);
     return cudaGetLastError();
 }
 

@@ -387,12 +387,21 @@ def _need(t, dtype, name, dev):
     return t.data_ptr()
 
 
-def _raw_stream(stream, dev):
-    """cudaStream_t of `stream`, or of the current stream."""
-    import torch
+_CURRENT = None
+_NO_STREAM = contextlib.nullcontext()
 
+
+def _raw_stream(stream, dev):
+    """cudaStream_t of `stream`, or of the current stream (asked for without a
+    Stream object where torch has a call for that: a microsecond of each step's calls)."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        global _CURRENT
+        if _CURRENT is None:
+            import torch
+
+            _CURRENT = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda d: torch.cuda.current_stream(d).cuda_stream)
+        return _CURRENT(dev)
     if stream.device.index != dev:
         raise ValueError(f"stream must be one of the current CUDA device ({dev})")
     return stream.cuda_stream
@@ -502,44 +511,46 @@ def _rotary(rotary, at, tokens, dev):
                      1 if rotary[2] else 0, _i32(rotary[3], "offset"), at)
 
 
-def _append_turned(call, pages, layer, K, V, table, kv_len, q_start, rotary, Q, Q_out, positions, stream):
-    """Append into the cache that pages(device) describes, with K and Q turned."""
+def _append_turned(call, pages, dev, layer, K, V, table, kv_len, q_start, rotary, Q, Q_out, positions, stream):
+    """`call`'s append into the cache that `pages` describes, with K and Q turned."""
     import torch
 
-    layer = _i32(layer, "layer")
-    dev = _here()
-    pg = pages(dev)
     n = K.shape[0]
     if V.shape[0] != n:
         raise ValueError("K and V must have the same shape")
-    kp, ks = _token_rows(K, "K", pg.kv_heads, pg.head_dim, dev)
-    vp, vs = _token_rows(V, "V", pg.kv_heads, pg.head_dim, dev)
+    hk, d = pages.kv_heads, pages.head_dim
+    kp, ks = _token_rows(K, "K", hk, d, dev)
+    vp, vs = _token_rows(V, "V", hk, d, dev)
     sq = _seqs(table, kv_len, q_start, n, 0, 0, dev)
-    if rotary is None:
-        if Q is not None or Q_out is not None or positions is not None:
-            raise ValueError("Q, Q_out and positions go with a rotary")
-        turn = None
-    else:
+    if rotary is not None:
         turn = ctypes.byref(_rotary(rotary, positions, n, dev))
+    elif Q is not None or Q_out is not None or positions is not None:
+        raise ValueError("Q, Q_out and positions go with a rotary")
+    else:
+        turn = None
     raw = _raw_stream(stream, dev)
-    qp = qs = op = os_ = None
-    hq = 0
+    qp = op = None
+    qs = os_ = hq = 0
     if Q is not None:
-        if Q.dim() != 3 or Q.shape[0] != n:
+        shape = Q.shape
+        if len(shape) != 3 or shape[0] != n:
             raise ValueError(f"Q must be [{n}, q_heads, head_dim]")
-        hq = Q.shape[1]
-        qp, qs = _token_rows(Q, "Q", hq, pg.head_dim, dev)
+        hq = shape[1]
+        qp, qs = _token_rows(Q, "Q", hq, d, dev)
         if Q_out is None:
             # on the stream that writes it, so that the allocator knows it
-            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-                Q_out = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
-        elif Q_out.shape != Q.shape:
-            raise ValueError("Q_out must have Q's shape")
-        op, os_ = _token_rows(Q_out, "Q_out", hq, pg.head_dim, dev)
+            with _NO_STREAM if stream is None else torch.cuda.stream(stream):
+                Q_out = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
+            op, os_ = Q_out.data_ptr(), hq * d
+        else:
+            if Q_out.shape != shape:
+                raise ValueError("Q_out must have Q's shape")
+            op, os_ = _token_rows(Q_out, "Q_out", hq, d, dev)
     elif Q_out is not None:
         raise ValueError("Q_out goes with Q")
-    _check(getattr(_lib(), call)(ctypes.byref(pg), layer, ctypes.byref(sq), turn, kp, ks, vp, vs, qp, qs or 0, hq, op,
-                                 os_ or 0, raw), call)
+    rc = call(ctypes.byref(pages), layer, ctypes.byref(sq), turn, kp, ks, vp, vs, qp, qs, hq, op, os_, raw)
+    if rc:
+        _check(rc, call.__name__)
     return Q_out
 
 
@@ -555,8 +566,10 @@ def pages_append_rotary(K_pages, V_pages, layer, K, V, table, kv_len, q_start, r
     its token."""
     if rotary is None:
         raise ValueError("rotary is needed: pages_append writes K as it is")
-    return _append_turned("kvpool_pages_append_rotary", lambda dev: _pages(K_pages, V_pages, status, dev), layer, K, V,
-                          table, kv_len, q_start, rotary, Q, Q_out, positions, stream)
+    layer = _i32(layer, "layer")
+    dev = _here()
+    return _append_turned(_lib().kvpool_pages_append_rotary, _pages(K_pages, V_pages, status, dev), dev, layer, K, V, table,
+                          kv_len, q_start, rotary, Q, Q_out, positions, stream)
 
 
 def _copy_args(src, dst):
@@ -618,8 +631,10 @@ def pages4_append(pages, layer, K, V, table, kv_len, q_start, rotary=None, Q=Non
     """Write new tokens into pages of 4 bits (kvpool_pages4_append): pages a
     Pages4, the rest as pages_append, and pages_append_rotary where a rotary is
     given (K goes from its rotation to codes without a rounding to bf16)."""
-    return _append_turned("kvpool_pages4_append", lambda dev: _pages4(pages, status, dev), layer, K, V, table, kv_len,
-                          q_start, rotary, Q, Q_out, positions, stream)
+    layer = _i32(layer, "layer")
+    dev = _here()
+    return _append_turned(_lib().kvpool_pages4_append, _pages4(pages, status, dev), dev, layer, K, V, table, kv_len, q_start,
+                          rotary, Q, Q_out, positions, stream)
 
 
 def pages4_read(pages, layer, table, kv_len, q_start, tokens, K=None, V=None, status=None, stream=None):
@@ -634,13 +649,17 @@ def pages4_read(pages, layer, table, kv_len, q_start, tokens, K=None, V=None, st
     sq = _seqs(table, kv_len, q_start, tokens, 0, 0, dev)
     shape = (tokens, pg.kv_heads, pg.head_dim)
     raw = _raw_stream(stream, dev)
+    bf16 = torch.bfloat16
     for t, name in ((K, "K"), (V, "V")):
         if t is not None and tuple(t.shape) != shape:
             raise ValueError(f"{name} must have shape {shape}")
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-        K, V = (torch.empty(shape, dtype=torch.bfloat16, device=pages[0].device) if t is None else t for t in (K, V))
-    _check(_lib().kvpool_pages4_read(ctypes.byref(pg), layer, ctypes.byref(sq), _need(K, torch.bfloat16, "K", dev),
-                                     _need(V, torch.bfloat16, "V", dev), raw), "kvpool_pages4_read")
+    if K is None or V is None:
+        # on the stream that writes them, so that the allocator knows it
+        with _NO_STREAM if stream is None else torch.cuda.stream(stream):
+            K = torch.empty(shape, dtype=bf16, device=pages[0].device) if K is None else K
+            V = torch.empty(shape, dtype=bf16, device=pages[0].device) if V is None else V
+    _check(_lib().kvpool_pages4_read(ctypes.byref(pg), layer, ctypes.byref(sq), _need(K, bf16, "K", dev),
+                                     _need(V, bf16, "V", dev), raw), "kvpool_pages4_read")
     return K, V
 
 
@@ -657,8 +676,10 @@ def pages4_attend(pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=No
                   stream=None):
     """pages_attend over pages of 4 bits (kvpool_pages4_attend): pages a Pages4,
     the rest and the results as pages_attend's."""
-    return _attend("kvpool_pages4_attend", lambda dev: _pages4(pages, status, dev), layer, Q, table, kv_len, q_start,
-                   max_q, max_kv, cap, slopes, window, first, prefix, out, lse, return_lse, softmax_scale, stream)
+    layer = _i32(layer, "layer")
+    dev = _here()
+    return _attend(_lib().kvpool_pages4_attend, _pages4(pages, status, dev), dev, layer, Q, table, kv_len, q_start, max_q,
+                   max_kv, cap, slopes, window, first, prefix, out, lse, return_lse, softmax_scale, stream)
 
 
 def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=None, cap=0.0, slopes=None,
@@ -675,22 +696,22 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
     Returns out bf16 [tokens, q_heads, d], or (out, lse float32 [tokens,
     q_heads]) with return_lse or an lse to write to. A row that sees no key
     gets 0 and -inf; rows behind the last sequence are left as they are."""
-    return _attend("kvpool_pages_attend", lambda dev: _pages(K_pages, V_pages, status, dev), layer, Q, table, kv_len,
-                   q_start, max_q, max_kv, cap, slopes, window, first, prefix, out, lse, return_lse, softmax_scale, stream)
-
-
-def _attend(call, pages, layer, Q, table, kv_len, q_start, max_q, max_kv, cap, slopes, window, first, prefix, out, lse,
-            return_lse, softmax_scale, stream):
-    """Attention over the cache that pages(device) describes."""
-    import torch
-
     layer = _i32(layer, "layer")
     dev = _here()
-    pg = pages(dev)
-    if Q.dim() != 3:
+    return _attend(_lib().kvpool_pages_attend, _pages(K_pages, V_pages, status, dev), dev, layer, Q, table, kv_len, q_start,
+                   max_q, max_kv, cap, slopes, window, first, prefix, out, lse, return_lse, softmax_scale, stream)
+
+
+def _attend(call, pages, dev, layer, Q, table, kv_len, q_start, max_q, max_kv, cap, slopes, window, first, prefix, out,
+            lse, return_lse, softmax_scale, stream):
+    """Attention of `call` over the cache that `pages` describes."""
+    import torch
+
+    shape = Q.shape
+    if len(shape) != 3:
         raise ValueError("Q must be [tokens, q_heads, head_dim]")
-    n, hq, d = Q.shape
-    qp, qs = _token_rows(Q, "Q", hq, pg.head_dim, dev)
+    n, hq, d = shape
+    qp, qs = _token_rows(Q, "Q", hq, pages.head_dim, dev)
     sq = _seqs(table, kv_len, q_start, n, max_q, max_kv, dev)
 
     def given(t, dtype, name, *shape):
@@ -705,18 +726,20 @@ def _attend(call, pages, layer, Q, table, kv_len, q_start, max_q, max_kv, cap, s
         sc = ctypes.byref(Score(cap, _i32(window, "window"), given(slopes, torch.float32, "slopes", hq),
                                 given(first, torch.int32, "first", n), given(prefix, torch.int32, "prefix", sq.seqs)))
     raw = _raw_stream(stream, dev)
-    op, lp = given(out, torch.bfloat16, "out", n, hq, d), given(lse, torch.float32, "lse", n, hq)
+    op = None if out is None else given(out, torch.bfloat16, "out", n, hq, d)
+    lp = None if lse is None else given(lse, torch.float32, "lse", n, hq)
     if op is None or (return_lse and lp is None):
         # on the stream that writes them, so that the allocator knows it
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with _NO_STREAM if stream is None else torch.cuda.stream(stream):
             if op is None:
-                out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=Q.device)
+                out = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
                 op = out.data_ptr()
             if return_lse and lp is None:
                 lse = torch.empty((n, hq), dtype=torch.float32, device=Q.device)
                 lp = lse.data_ptr()
-    _check(getattr(_lib(), call)(ctypes.byref(pg), layer, ctypes.byref(sq), qp, qs, hq, sc, op, lp, softmax_scale, raw),
-           call)
+    rc = call(ctypes.byref(pages), layer, ctypes.byref(sq), qp, qs, hq, sc, op, lp, softmax_scale, raw)
+    if rc:
+        _check(rc, call.__name__)
     return out if lse is None else (out, lse)
 
 
