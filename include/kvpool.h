@@ -634,11 +634,20 @@ int kvpool_pages4_read(const kvpool_pages4_t* pages, int layer, const kvpool_seq
 int kvpool_pages4_copy(const kvpool_pages4_t* pages, const int32_t* src, const int32_t* dst, int n, void* stream);
 
 /* kvpool_pages_attend over what the codes stand for (the same Q, bf16 and after
- * its rotation, the same modifiers, outputs and errors): no dequantised copy is
- * made, no workspace needed, nothing allocated. */
+ * its rotation, the same modifiers, outputs and errors). workspace: device
+ * memory, 16-byte aligned, scratch, or NULL with 0 bytes. Chunks of many tokens
+ * read each key many times; with a workspace its operand is made once per call
+ * and kept there. It changes no result, and any size may be given: sequences
+ * that it has no room for do without. Calls that overlap on the GPU must not
+ * share one. Allocates nothing. */
 int kvpool_pages4_attend(const kvpool_pages4_t* pages, int layer, const kvpool_seqs_t* seqs, const void* Q,
                          long long q_stride, int q_heads, const kvpool_score_t* score, void* out, float* lse,
-                         float softmax_scale, void* stream);
+                         float softmax_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes with which kvpool_pages4_attend runs fastest on these sequences (by
+ * their max_q and max_kv): 0 where it has no use for a workspace, and for
+ * invalid arguments. */
+size_t kvpool_pages4_attend_ws_bytes(const kvpool_pages4_t* pages, const kvpool_seqs_t* seqs, int q_heads);
 
 /* kvpool_pages_status of a 4-bit cache's word. */
 int kvpool_pages4_status(const kvpool_pages4_t* pages, void* stream);

@@ -56,7 +56,10 @@ cudaError_t launch_pages4_read(const PagedSeqs& s, int head_dim, const uint32_t*
 // The two kinds of attention, as of the bf16 pages (pages4_rows.cu, pages4_chunk.cu).
 cudaError_t launch_pages4_rows(const PagedAttend4& a, int head_dim, int max_q, int max_kv, int sm_count,
                                cudaStream_t st);
-cudaError_t launch_pages4_chunk(const PagedAttend4& a, int head_dim, int max_q, int max_kv, cudaStream_t st);
+// (ws: memory for tiles made of codes once per call, or null; sequences that it has no room for go without)
+long long pages4_chunk_ws_bytes(const PagedSeqs& s, int head_dim, int max_kv);
+cudaError_t launch_pages4_chunk(const PagedAttend4& a, int head_dim, int max_q, int max_kv, void* ws, size_t ws_bytes,
+                                cudaStream_t st);
 
 // Checks that the entries of the bf16 pages and of the 4-bit pages share.
 int check_pages_args(const kvpool_pages_t* pg, int layer);

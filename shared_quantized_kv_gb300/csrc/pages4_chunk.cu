@@ -39,7 +39,6 @@ namespace {
 
 using pages::Seen;
 
-constexpr int kThreads = 768;
 constexpr int kTile = 128;              // keys per tile, rows per slot
 constexpr int kRows = 2 * kTile;        // rows per CTA
 constexpr int kFewTiles = 8;            // key tiles that a cluster does not split
@@ -58,8 +57,13 @@ constexpr int kSoftmax = 512;           // softmax threads
 // codes their own rings hold
 constexpr int kWarpsK = 4, kWarpsV = 2, kRawK = 2, kRawV = 3;
 constexpr float kLn2 = 0.6931471805599453f;
-// registers: 6 warpgroups launched with 80 each; 56 + 4 x 88 + 72 = 6 x 80
-constexpr int kRegsIssue = 56, kRegsMany = 88, kRegsExpand = 72;
+// MADE: the tiles lie in a workspace, made before (no expanders). Registers of the warpgroups of warps 0 to 3, of the
+// softmax (4 of them), of K's expanders: 56 + 4 x 88 + 72 = 6 x 80, and 64 + 4 x 104 = 5 x 96 at launch.
+template <bool MADE>
+struct Shape {
+    static constexpr int threads = MADE ? 640 : 768;
+    static constexpr int regs_issue = MADE ? 64 : 56, regs_many = MADE ? 104 : 88, regs_expand = 72;
+};
 
 // What the softmax needs to know of a tile's scales, beside the ring: a slot per tile
 struct TileScales {
@@ -67,8 +71,12 @@ struct TileScales {
     float k[kTile];     // K's
     uint32_t odd[4];    // of 32 keys: V's are not all finite
 };
-
+// A tile in the workspace, as shared memory takes it: K, V, the scales.
 template <int D>
+constexpr int made_bytes() { return 2 * kTile * D * 2 + (int)sizeof(TileScales) + 112; }
+static_assert(made_bytes<64>() % 128 == 0 && made_bytes<128>() % 128 == 0 && sizeof(TileScales) % 16 == 0, "alignment");
+
+template <int D, bool MADE>
 struct Lay {
     static constexpr int stage = kTile * D * 2;  // a K or V tile
     static constexpr int nst = D == 128 ? 2 : 4; // of K, and as many of V
@@ -79,7 +87,7 @@ struct Lay {
     static constexpr int ring = 2 * stage;       // after the two Q tiles: K's stages, then V's
     static constexpr int codes = 32 * D / 2;     // of 32 keys
     static constexpr int raw = ring + 2 * nst * stage;
-    static constexpr int scales = raw + (kWarpsK * kRawK + kWarpsV * kRawV) * codes;
+    static constexpr int scales = raw + (MADE ? 0 : (kWarpsK * kRawK + kWarpsV * kRawV) * codes);
     static constexpr int bars = scales + slots * (int)sizeof(TileScales);
     // barriers: full, empty per stage of K, of V; per slot S, P (of each half), P V of the first, all done
     static constexpr int bar_s = bars + 4 * nst * 8, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_fin = bar_o + 16;
@@ -168,6 +176,85 @@ __device__ __forceinline__ uint4 v_operand(uint32_t w) {
     return make_uint4(one(w << 1), one(w >> 3), one(w >> 7), one(w >> 11));
 }
 
+// H16's columns as operands: entry (k, n) is -1 to the ones that k and n share.
+__device__ __forceinline__ void h16_operands(uint32_t (&h16)[2][2]) {
+    const int lane = threadIdx.x & 31, quad = lane >> 2, qi = lane & 3;
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            auto sign = [&](int k) { return __popc(k & (quad + 8 * nb)) & 1 ? 0xBC00u : 0x3C00u; };
+            h16[nb][y] = sign(2 * qi + 8 * y) | sign(2 * qi + 8 * y + 1) << 16;
+        }
+}
+// A warp's 32 keys from key0 of a tile on: H (u - 7.5) of their codes `own`, into
+// the tile. 16 keys at a time are a matrix operand (u - 8) whose 16 channels of a
+// group the product with H16 transforms; the groups' results then go through the
+// last stages in registers. half_sum: D / 2 where the lane has channel 0.
+template <int D>
+__device__ __forceinline__ void expand_k(const unsigned char* own, unsigned char* stage, int key0, const uint32_t (&h16)[2][2],
+                                         uint32_t half_sum) {
+    const int lane = threadIdx.x & 31, quad = lane >> 2, qi = lane & 3;
+                constexpr int kGroups = D / 16;
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {  // keys 16 x + quad and + 8
+                    uint32_t z[2][kGroups][2];  // [key][group][half of its channels]
+#pragma unroll
+                    for (int g2 = 0; g2 < kGroups / 2; ++g2) {  // two groups: four words
+                        uint4 w[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            w[y] = *reinterpret_cast<const uint4*>(own + (16 * x + 8 * y + quad) * (D / 2) + g2 * 16);
+                        const int sh = 4 * qi;
+                        const uint32_t a0 = k_pair(w[0].x >> sh), a1 = k_pair(w[1].x >> sh);
+                        const uint32_t a2 = k_pair(w[0].y >> sh), a3 = k_pair(w[1].y >> sh);
+                        const uint32_t c0 = k_pair(w[0].z >> sh), c1 = k_pair(w[1].z >> sh);
+                        const uint32_t c2 = k_pair(w[0].w >> sh), c3 = k_pair(w[1].w >> sh);
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb) {
+                            mma_half(z[0][2 * g2][nb], z[1][2 * g2][nb], a0, a1, a2, a3, h16[nb][0], h16[nb][1]);
+                            mma_half(z[0][2 * g2 + 1][nb], z[1][2 * g2 + 1][nb], c0, c1, c2, c3, h16[nb][0], h16[nb][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                            for (int h = 1; h < kGroups; h <<= 1)
+#pragma unroll
+                                for (int q = 0; q < kGroups; ++q)
+                                    if (!(q & h)) {
+                                        const uint32_t a = z[y][q][nb], c = z[y][q + h][nb];
+                                        z[y][q][nb] = hadd2(a, c), z[y][q + h][nb] = hsub2(a, c);
+                                    }
+                        z[y][0][0] = hadd2(z[y][0][0], half_sum);
+                        // channels 16 q + 8 nb + 2 qi and the next: 4 bytes of piece 2 q + nb
+                        const int key = key0 + 16 * x + 8 * y + quad;  // (key & 7 is quad)
+#pragma unroll
+                        for (int q = 0; q < kGroups; ++q)
+#pragma unroll
+                            for (int nb = 0; nb < 2; ++nb) {
+                                const int pc = 2 * q + nb;
+                                *reinterpret_cast<uint32_t*>(stage + (pc / 8) * (kTile * 128) + key * 128 +
+                                                             (((pc % 8) ^ quad) << 4) + 4 * qi) = z[y][q][nb];
+                            }
+                    }
+                }
+}
+// The same of V: u - 7.5 as they are. D / 8 lanes take a key, a word each, which becomes 16 bytes of its row.
+template <int D>
+__device__ __forceinline__ void expand_v(const unsigned char* own, unsigned char* stage, int key0) {
+    constexpr int kLanes = D / 8, kKeys = 32 / kLanes;  // lanes of a key, keys at a time
+    const int lane = threadIdx.x & 31, in_row = lane % kLanes, in_key = lane / kLanes;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(own) + lane;
+    unsigned char* to = stage + (in_row / 8) * (kTile * 128) + (key0 + in_key) * 128;
+    const uint32_t piece = (in_row % 8) ^ (in_key & 7);  // ((key & 7) changes by kKeys at a time)
+#pragma unroll 8
+    for (int j = 0; j < 32 / kKeys; ++j)
+        *reinterpret_cast<uint4*>(to + j * kKeys * 128 + ((piece ^ ((j * kKeys) & 7)) << 4)) = v_operand(words[32 * j]);
+}
+
 // An expander warp's share of every tile, 16 * BLOCKS keys from key0 on: where its
 // codes lie (a page holds 16 keys at least), and copies of them on their way into
 // the warp's own ring, 32 keys to an entry.
@@ -224,13 +311,23 @@ struct CodeReader {
     }
 };
 
+// The workspace: room for so many tiles of each sequence and KV head. Sequences
+// that fit are the MADE kernel's, others the other one's.
+struct Made {
+    unsigned char* tiles;
+    int room;
+    __host__ __device__ bool has(long long tokens) const { return room > 0 && tokens <= (long long)room * kTile; }
+};
+
 // KIND: the causal mask alone; other masks too; scores that a cap or a bias by
 // distance changes; the same with a cap so wide that each key takes a form of its own.
 enum { kPlain, kMasks, kScores, kWideScores };
-template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads, 1)
-pages4_chunk_kernel(const PagedAttend4 p4) {
-    using L = Lay<D>;
+template <int D, int KIND, bool MADE>
+__global__ void __launch_bounds__(Shape<MADE>::threads, 1)
+pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
+    using L = Lay<D, MADE>;
+    using SH = Shape<MADE>;
+    constexpr int kThreads = SH::threads;
     const PagedAttend& p = p4.a;
     constexpr bool SCORED = KIND != kPlain;
     constexpr bool CHANGED = KIND == kScores || KIND == kWideScores;
@@ -249,7 +346,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
     // blocks of a sequence from its last (the one that sees most) to its first
     const int job = blockIdx.x / CS, g = job % s.Hk;
     pages::RowBlock b;
-    if (!pages::find_block(s, p.G, kRows, job / s.Hk, b)) {  // the whole cluster's
+    if (!pages::find_block(s, p.G, kRows, job / s.Hk, b) || made.has(b.T) != MADE) {  // the whole cluster's
         __syncthreads();
         if (warp == 1) ptx::tmem_dealloc(*tslot, kCols);
         return;
@@ -268,7 +365,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
     const uint32_t b_o = ptx::smem_u32(sm + L::bar_o), b_fin = ptx::smem_u32(sm + L::bar_fin);
     if (tid == 0) {
         for (int i = 0; i < 2 * L::nst; ++i) {
-            ptx::mbar_init(b_full + 8 * i, i < L::nst ? kWarpsK : kWarpsV);
+            ptx::mbar_init(b_full + 8 * i, MADE ? 1 : i < L::nst ? kWarpsK : kWarpsV);
             ptx::mbar_init(b_empty + 8 * i, 2);  // both slots
         }
         for (int w = 0; w < 2; ++w) {
@@ -364,7 +461,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
     TileScales* tile_scales = reinterpret_cast<TileScales*>(sm + L::scales);
 
     if (warp < 4) {
-        ptx::regs_dec<kRegsIssue>();
+        ptx::regs_dec<SH::regs_issue>();
         if (warp == 1 || warp == 2) {
             // ------------------------------------------------------ issuers
             // One warp per slot; the whole warp runs this with uniform values, an elected lane issues.
@@ -486,18 +583,35 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                 bad = bad || late;
             }
             __syncwarp();
+        } else if constexpr (MADE) {
+            // ------------------------------------------------------- loaders
+            // Warp 0: K and the scales, warp 3: V; a tile in one or two bulk copies.
+            const bool v = warp == 3;
+            const unsigned char* tiles = made.tiles + ((long long)b.seq * s.Hk + g) * made.room * made_bytes<D>() + (v ? L::stage : 0);
+            for (int i = 0; i < n; ++i) {
+                const int st = i % L::nst + (v ? L::nst : 0);
+                if (i >= L::nst) warp_wait(b_empty + 8 * st, ((i / L::nst) - 1) & 1, bad);
+                if (lane == 0) {
+                    const unsigned char* src = tiles + (long long)tile_at(i) * made_bytes<D>();
+                    ptx::mbar_expect_tx(b_full + 8 * st, L::stage + (v ? 0 : (int)sizeof(TileScales)));
+                    ptx::bulk_g2s(ptx::smem_u32(sm + L::ring + st * L::stage), src, L::stage, b_full + 8 * st);
+                    if (!v)
+                        ptx::bulk_g2s(ptx::smem_u32(tile_scales + i % L::slots), src + 2 * L::stage, sizeof(TileScales), b_full + 8 * st);
+                }
+                __syncwarp();
+            }
+            // every requested tile has landed before the CTA may go on
+            for (int i = max(0, n - L::nst); i < n; ++i) {
+                bool late = false;
+                warp_wait(b_full + 8 * (i % L::nst + (v ? L::nst : 0)), (i / L::nst) & 1, late);
+            }
         } else {
             // ---------------------------------------------- expanders of V
-            // D / 8 lanes take a key, a word each, which becomes 16 bytes of its row.
-            constexpr int kLanes = D / 8, kKeys = 32 / kLanes;  // lanes of a key, keys at a time
-            const int vw = warp / 3, in_row = lane % kLanes, in_key = lane / kLanes;
+            const int vw = warp / 3;
             CodeReader<D, 4> in(p, s, g, b.seq, T, n, vw * 64, lane,
                                 sm + L::raw + (kWarpsK * kRawK + vw * kRawV) * L::codes);
             auto tile_of = [&](int i) { return tile_at(i); };
             in.start(tile_of);
-            // (key & 7) changes by kKeys at a time
-            const uint32_t to = (in_row / 8) * (kTile * 128) + (vw * 64 + in_key) * 128;
-            const uint32_t piece = (in_row % 8) ^ (in_key & 7);
             if (n > 0) in.ask(p.V, 0, 0);
             cp_commit();
             if (n > 0) in.ask(p.V, 0, 1);
@@ -513,11 +627,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
                     cp_commit();
                     cp_wait<2>();
                     __syncwarp();
-                    const uint32_t* words = reinterpret_cast<const uint32_t*>(in.slot(i, c)) + lane;
-#pragma unroll 8
-                    for (int j = 0; j < 32 / kKeys; ++j)
-                        *reinterpret_cast<uint4*>(stage + to + (32 * c + j * kKeys) * 128 +
-                                                  ((piece ^ ((j * kKeys) & 7)) << 4)) = v_operand(words[32 * j]);
+                    expand_v<D>(in.slot(i, c), stage, vw * 64 + 32 * c);
                     __syncwarp();  // (the codes are read)
                 }
                 ptx::fence_proxy_async();
@@ -531,12 +641,9 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             ptx::bar_sync(kBarDone, kThreads);
             ptx::bar_sync(kBarRows, kThreads);
         }
-    } else if (warp >= 20) {
-        ptx::regs_dec<kRegsExpand>();
+    } else if (!MADE && warp >= 20) {
+        ptx::regs_dec<SH::regs_expand>();
         // -------------------------------------------------- expanders of K
-        // 16 keys at a time are a matrix operand (u - 8) whose 16 channels of a group the
-        // product with H16 transforms; the groups' results then go through the last
-        // stages in registers.
         const int key0 = (warp - 20) * 32;
         CodeReader<D, 2> in(p, s, g, b.seq, T, n, key0, lane, sm + L::raw + (warp - 20) * (kRawK * L::codes));
         auto tile_of = [&](int i) { return tile_at(i); };
@@ -548,17 +655,9 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             tk = held ? __ldg(p4.Kt + at + (lane & 15)) : 0.0f;
             tv = held ? __ldg(p4.Vt + at + (lane & 15)) : 0.0f;
         };
-        // H16's columns as operands: entry (k, n) is -1 to the ones that k and n share
-        const int quad = lane >> 2, qi = lane & 3;
         uint32_t h16[2][2];
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                auto sign = [&](int k) { return __popc(k & (quad + 8 * nb)) & 1 ? 0xBC00u : 0x3C00u; };
-                h16[nb][y] = sign(2 * qi + 8 * y) | sign(2 * qi + 8 * y + 1) << 16;
-            }
-        const uint32_t half_sum = qi == 0 ? (D == 128 ? 0x5400u : 0x5000u) : 0u;  // D / 2 to channel 0
+        h16_operands(h16);
+        const uint32_t half_sum = (lane & 3) == 0 ? (D == 128 ? 0x5400u : 0x5000u) : 0u;  // D / 2 to channel 0
         ask_scales(0);
         in.ask(p.K, 0, 0);
         cp_commit();
@@ -577,53 +676,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             if (lane == 0) ts.odd[key0 / 32] = odd_v;
             in.next_batch(i, tile_of);
             ask_scales(i + 1);
-            constexpr int kGroups = D / 16;
-            const unsigned char* own = in.slot(i, 0);
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x) {  // keys 16 x + quad and + 8
-                uint32_t z[2][kGroups][2];  // [key][group][half of its channels]
-#pragma unroll
-                for (int g2 = 0; g2 < kGroups / 2; ++g2) {  // two groups: four words
-                    uint4 w[2];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        w[y] = *reinterpret_cast<const uint4*>(own + (16 * x + 8 * y + quad) * (D / 2) + g2 * 16);
-                    const int sh = 4 * qi;
-                    const uint32_t a0 = k_pair(w[0].x >> sh), a1 = k_pair(w[1].x >> sh);
-                    const uint32_t a2 = k_pair(w[0].y >> sh), a3 = k_pair(w[1].y >> sh);
-                    const uint32_t c0 = k_pair(w[0].z >> sh), c1 = k_pair(w[1].z >> sh);
-                    const uint32_t c2 = k_pair(w[0].w >> sh), c3 = k_pair(w[1].w >> sh);
-#pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) {
-                        mma_half(z[0][2 * g2][nb], z[1][2 * g2][nb], a0, a1, a2, a3, h16[nb][0], h16[nb][1]);
-                        mma_half(z[0][2 * g2 + 1][nb], z[1][2 * g2 + 1][nb], c0, c1, c2, c3, h16[nb][0], h16[nb][1]);
-                    }
-                }
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-#pragma unroll
-                    for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                        for (int h = 1; h < kGroups; h <<= 1)
-#pragma unroll
-                            for (int q = 0; q < kGroups; ++q)
-                                if (!(q & h)) {
-                                    const uint32_t a = z[y][q][nb], c = z[y][q + h][nb];
-                                    z[y][q][nb] = hadd2(a, c), z[y][q + h][nb] = hsub2(a, c);
-                                }
-                    z[y][0][0] = hadd2(z[y][0][0], half_sum);
-                    // channels 16 q + 8 nb + 2 qi and the next: 4 bytes of piece 2 q + nb
-                    const int key = key0 + 16 * x + 8 * y + quad;  // (key & 7 is quad)
-#pragma unroll
-                    for (int q = 0; q < kGroups; ++q)
-#pragma unroll
-                        for (int nb = 0; nb < 2; ++nb) {
-                            const int pc = 2 * q + nb;
-                            *reinterpret_cast<uint32_t*>(stage + (pc / 8) * (kTile * 128) + key * 128 +
-                                                         (((pc % 8) ^ quad) << 4) + 4 * qi) = z[y][q][nb];
-                        }
-                }
-            }
+            expand_k<D>(in.slot(i, 0), stage, key0, h16, half_sum);
             ptx::fence_proxy_async();
             __syncwarp();  // (and the codes are read)
             if (lane == 0) ptx::mbar_arrive(b_full + 8 * st);
@@ -635,7 +688,7 @@ pages4_chunk_kernel(const PagedAttend4 p4) {
             ptx::bar_sync(kBarRows, kThreads);
         }
     } else {
-        ptx::regs_inc<kRegsMany>();
+        ptx::regs_inc<SH::regs_many>();
         float m = -CUDART_INF_F, l = 0.0f;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         // ------------------------------------------------------------ softmax
@@ -1090,19 +1143,19 @@ struct Fit {
     cudaError_t err = cudaSuccess;
     int clusters[4] = {};
 };
-template <int D, int KIND>
+template <int D, int KIND, bool MADE>
 const Fit& fit(int device) {
     static std::once_flag once[kPagedDevices];
     static Fit fits[kPagedDevices];
     std::call_once(once[device], [device] {
-        auto kern = pages4_chunk_kernel<D, KIND>;
+        auto kern = pages4_chunk_kernel<D, KIND, MADE>;
         Fit& x = fits[device];
-        x.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::total);
+        x.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (Lay<D, MADE>::total));
         for (int i = 0; i < 4 && x.err == cudaSuccess; ++i) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(1 << i, 1, 1);
-            cfg.blockDim = dim3(kThreads, 1, 1);
-            cfg.dynamicSmemBytes = Lay<D>::total;
+            cfg.blockDim = dim3(Shape<MADE>::threads, 1, 1);
+            cfg.dynamicSmemBytes = (Lay<D, MADE>::total);
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = 1 << i;
@@ -1116,14 +1169,14 @@ const Fit& fit(int device) {
     return fits[device];
 }
 
-template <int D, int KIND>
-cudaError_t launch(const PagedAttend4& p4, int max_q, int max_kv, cudaStream_t st) {
+template <int D, int KIND, bool MADE>
+cudaError_t launch(const PagedAttend4& p4, const Made& made, int max_q, int max_kv, cudaStream_t st) {
     const PagedAttend& a = p4.a;
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     if (device >= kPagedDevices) return cudaErrorInvalidDevice;
-    const Fit& f = fit<D, KIND>(device);
+    const Fit& f = fit<D, KIND, MADE>(device);
     if (f.err != cudaSuccess) return f.err;
     const long long rows = (long long)a.s.tokens * a.G;
     const long long blocks = rows / kRows + a.s.seqs;  // at least as many as there are
@@ -1148,8 +1201,8 @@ cudaError_t launch(const PagedAttend4& p4, int max_q, int max_kv, cudaStream_t s
     if (split * blocks * a.s.Hk > INT_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(split * blocks * a.s.Hk), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Lay<D>::total;
+    cfg.blockDim = dim3(Shape<MADE>::threads, 1, 1);
+    cfg.dynamicSmemBytes = (Lay<D, MADE>::total);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1158,18 +1211,114 @@ cudaError_t launch(const PagedAttend4& p4, int max_q, int max_kv, cudaStream_t s
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, pages4_chunk_kernel<D, KIND>, p4);
+    return cudaLaunchKernelEx(&cfg, pages4_chunk_kernel<D, KIND, MADE>, p4, made);
+}
+
+// Tiles of the workspace: K expanded, V expanded, the scales, as the kernel takes
+// them. A CTA per tile of a sequence and KV head, four warps of 32 keys, through
+// shared memory and out in bulk. Memory bound: 512 bytes written per key and head of
+// 128 (16K keys of 8 heads, 67 MB).
+constexpr int kMakeThreads = 128;
+template <int D>
+__global__ void __launch_bounds__(kMakeThreads)
+pages4_make_kernel(const PagedAttend4 p4, const Made made) {
+    constexpr int kStage = kTile * D * 2, kCodes = 32 * D / 2;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    const PagedAttend& p = p4.a;
+    const PagedSeqs& s = p.s;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, key0 = warp * 32;
+    const int seq = blockIdx.z, g = blockIdx.y, tile = blockIdx.x;
+    const int len = pages::length_of(s, seq), T = pages::held_tokens(s, len);
+    if (pages::row_begin(s, seq + 1) <= pages::row_begin(s, seq)) return;  // no rows, nobody reads it
+    if (!made.has(T) || tile * kTile >= T) return;
+    CodeReader<D, 2> in(p, s, g, seq, T, 1, key0, lane, sm + 2 * kStage + sizeof(TileScales) + warp * 2 * kCodes);
+    in.start([&](int) { return tile; });
+    in.ask(p.K, 0, 0);
+    cp_commit();
+    in.raw += kCodes;
+    in.ask(p.V, 0, 0);
+    cp_commit();
+    const int at = in.vector_of(0, lane >> 4);
+    const bool held = at >= 0 && tile * kTile + key0 + lane < T;
+    const float tk = held ? __ldg(p4.Kt + at + (lane & 15)) : 0.0f, tv = held ? __ldg(p4.Vt + at + (lane & 15)) : 0.0f;
+    TileScales& ts = *reinterpret_cast<TileScales*>(sm + 2 * kStage);
+    ts.k[key0 + lane] = tk;
+    ts.v[key0 + lane] = tv;
+    const bool odd_v = __any_sync(0xffffffffu, !finite(tv));
+    if (lane == 0) ts.odd[warp] = odd_v;
+    uint32_t h16[2][2];
+    h16_operands(h16);
+    cp_wait<1>();
+    __syncwarp();
+    expand_k<D>(in.raw - kCodes, sm, key0, h16, (lane & 3) == 0 ? (D == 128 ? 0x5400u : 0x5000u) : 0u);
+    cp_wait<0>();
+    __syncwarp();
+    expand_v<D>(in.raw, sm + kStage, key0);
+    ptx::fence_proxy_async();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        unsigned char* dst = made.tiles + (((long long)seq * s.Hk + g) * made.room + tile) * made_bytes<D>();
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_u32(sm)),
+                     "r"(2 * kStage + (int)sizeof(TileScales)) : "memory");
+        ptx::bulk_commit();
+        ptx::bulk_wait_read();  // (shared memory stays until it has been read)
+    }
+}
+
+template <int D>
+cudaError_t launch_make(const PagedAttend4& p4, const Made& made, cudaStream_t st) {
+    constexpr int smem = 2 * kTile * D * 2 + (int)sizeof(TileScales) + 4 * 2 * (32 * D / 2) + 128;
+    static std::once_flag once[kPagedDevices];
+    static cudaError_t opt[kPagedDevices];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device >= kPagedDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[device], [&] {
+        opt[device] = cudaFuncSetAttribute(pages4_make_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (opt[device] != cudaSuccess) return opt[device];
+    pages4_make_kernel<D><<<dim3(made.room, p4.a.s.Hk, p4.a.s.seqs), kMakeThreads, smem, st>>>(p4, made);
+    return cudaGetLastError();
+}
+
+template <int D, int KIND>
+cudaError_t launch_kind(const PagedAttend4& p4, const Made& made, int max_q, int max_kv, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (made.room > 0) {
+        e = launch_make<D>(p4, made, st);
+        if (e == cudaSuccess) e = launch<D, KIND, true>(p4, made, max_q, max_kv, st);
+        // no sequence can be longer than the workspace's room: the other kernel has nothing to do
+        if (made.has((long long)p4.a.s.tstride << p4.a.s.pshift)) return e;
+    }
+    return e == cudaSuccess ? launch<D, KIND, false>(p4, made, max_q, max_kv, st) : e;
 }
 
 }  // namespace
 
-cudaError_t launch_pages4_chunk(const PagedAttend4& p4, int head_dim, int max_q, int max_kv, cudaStream_t st) {
+// Bytes of a workspace with room for max_kv tokens of every sequence.
+long long pages4_chunk_ws_bytes(const PagedSeqs& s, int head_dim, int max_kv) {
+    const long long tiles = (max_kv + kTile - 1) / kTile * (long long)s.Hk * s.seqs;
+    return tiles * (head_dim == 64 ? made_bytes<64>() : made_bytes<128>());
+}
+
+cudaError_t launch_pages4_chunk(const PagedAttend4& p4, int head_dim, int max_q, int max_kv, void* ws, size_t ws_bytes,
+                                cudaStream_t st) {
     const PagedAttend& a = p4.a;
     const int kind = a.cap2 > pages::kWideCap2        ? kWideScores
                      : a.cap2 > 0.0f || a.slopes ? kScores
                      : paged_scored(a)           ? kMasks
                                                  : kPlain;
-#define KVP_PG4_CHUNK(KK) (head_dim == 64 ? launch<64, KK>(p4, max_q, max_kv, st) : launch<128, KK>(p4, max_q, max_kv, st))
+    // room for no more tiles than max_kv has: longer sequences are the kernel's that makes its tiles itself
+    Made made{static_cast<unsigned char*>(ws), 0};
+    if (ws) {
+        const long long each = (long long)a.s.seqs * a.s.Hk * (head_dim == 64 ? made_bytes<64>() : made_bytes<128>());
+        made.room = (int)std::min<long long>((long long)ws_bytes / each, (max_kv + kTile - 1) / kTile);
+        if (a.s.seqs > 65535) made.room = 0;  // (a grid's third extent)
+    }
+#define KVP_PG4_CHUNK(KK) \
+    (head_dim == 64 ? launch_kind<64, KK>(p4, made, max_q, max_kv, st) : launch_kind<128, KK>(p4, made, max_q, max_kv, st))
     if (kind == kWideScores) return KVP_PG4_CHUNK(kWideScores);
     if (kind == kScores) return KVP_PG4_CHUNK(kScores);
     return kind == kMasks ? KVP_PG4_CHUNK(kMasks) : KVP_PG4_CHUNK(kPlain);

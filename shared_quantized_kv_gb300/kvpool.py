@@ -145,7 +145,9 @@ _SIGS = {
                                           ctypes.c_void_p]),
     "kvpool_pages4_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                             ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
-                                            ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p]),
+                                            ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t,
+                                            ctypes.c_void_p]),
+    "kvpool_pages4_attend_ws_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int]),
     "kvpool_pages4_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "kvpool_pages_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                          ctypes.c_void_p]),
@@ -671,15 +673,44 @@ def pages4_copy(pages, src, dst, stream=None):
     _check(_lib().kvpool_pages4_copy(ctypes.byref(pg), *args, _raw_stream(stream, dev)), "kvpool_pages4_copy")
 
 
+def pages4_attend_ws_bytes(pages, table, kv_len, q_start, tokens, q_heads, max_q=None, max_kv=None) -> int:
+    """Bytes of a workspace with which pages4_attend runs fastest (kvpool_pages4_attend_ws_bytes; 0: it has no use for one)."""
+    dev = _here()
+    pg = _pages4(pages, None, dev)
+    sq = _seqs(table, kv_len, q_start, _i32(tokens, "tokens"), max_q, max_kv, dev)
+    return int(_lib().kvpool_pages4_attend_ws_bytes(ctypes.byref(pg), ctypes.byref(sq), _i32(q_heads, "q_heads")))
+
+
 def pages4_attend(pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=None, cap=0.0, slopes=None, window=0,
                   first=None, prefix=None, out=None, lse=None, return_lse=False, softmax_scale=0.0, status=None,
-                  stream=None):
+                  stream=None, workspace=None):
     """pages_attend over pages of 4 bits (kvpool_pages4_attend): pages a Pages4,
-    the rest and the results as pages_attend's."""
+    the rest and the results as pages_attend's. workspace: a tensor on the
+    device, any size (an empty one: none); None: as much as the call has use for
+    (pages4_attend_ws_bytes) is allocated, which a chunk of many tokens does.
+    It changes no result."""
+    import torch
+
     layer = _i32(layer, "layer")
     dev = _here()
-    return _attend(_lib().kvpool_pages4_attend, _pages4(pages, status, dev), dev, layer, Q, table, kv_len, q_start, max_q,
-                   max_kv, cap, slopes, window, first, prefix, out, lse, return_lse, softmax_scale, stream)
+    pg = _pages4(pages, status, dev)
+
+    def scratch(sq, hq):
+        if workspace is not None:
+            n = workspace.numel() * workspace.element_size()
+            return workspace, _need(workspace, workspace.dtype, "workspace", dev) if n else None, n
+        # (one new token, or a few rows, have no use for it)
+        n = _lib().kvpool_pages4_attend_ws_bytes(ctypes.byref(pg), ctypes.byref(sq), hq) if sq.max_q != 1 else 0
+        if not n:
+            return None, None, 0
+        # on the stream that uses it, so that the allocator knows it
+        with _NO_STREAM if stream is None else torch.cuda.stream(stream):
+            ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+        return ws, ws.data_ptr(), n
+
+    return _attend(_lib().kvpool_pages4_attend, pg, dev, layer, Q, table, kv_len, q_start, max_q, max_kv, cap, slopes,
+                   window, first, prefix, out, lse, return_lse, softmax_scale, stream, scratch)
+
 
 
 def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=None, cap=0.0, slopes=None,
@@ -703,8 +734,9 @@ def pages_attend(K_pages, V_pages, layer, Q, table, kv_len, q_start, max_q=None,
 
 
 def _attend(call, pages, dev, layer, Q, table, kv_len, q_start, max_q, max_kv, cap, slopes, window, first, prefix, out,
-            lse, return_lse, softmax_scale, stream):
-    """Attention of `call` over the cache that `pages` describes."""
+            lse, return_lse, softmax_scale, stream, scratch=None):
+    """Attention of `call` over the cache that `pages` describes. scratch: None, or what gives the workspace's address
+    and bytes."""
     import torch
 
     shape = Q.shape
@@ -737,7 +769,11 @@ def _attend(call, pages, dev, layer, Q, table, kv_len, q_start, max_q, max_kv, c
             if return_lse and lp is None:
                 lse = torch.empty((n, hq), dtype=torch.float32, device=Q.device)
                 lp = lse.data_ptr()
-    rc = call(ctypes.byref(pages), layer, ctypes.byref(sq), qp, qs, hq, sc, op, lp, softmax_scale, raw)
+    if scratch is None:
+        rc = call(ctypes.byref(pages), layer, ctypes.byref(sq), qp, qs, hq, sc, op, lp, softmax_scale, raw)
+    else:
+        ws, wp, nbytes = scratch(sq, hq)  # (ws: held until the call is enqueued)
+        rc = call(ctypes.byref(pages), layer, ctypes.byref(sq), qp, qs, hq, sc, op, lp, softmax_scale, wp, nbytes, raw)
     if rc:
         _check(rc, call.__name__)
     return out if lse is None else (out, lse)

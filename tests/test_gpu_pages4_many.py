@@ -39,6 +39,25 @@ def test_ragged_batch(kp, hk, hq, d, P, room):
     run(kp, many(Batch4(hk, hq, d, P, q, kv, seed=hq), 1 << 16), max_kv=room)
 
 
+@pytest.mark.parametrize("tiles", [0, 1, 3, 8, 100])
+@pytest.mark.parametrize("hk,hq,d", [(2, 8, 128), (1, 5, 64)])
+def test_workspaces_of_any_size(kp, hk, hq, d, tiles):
+    """None, room for the shorter sequences, room for all: the same results."""
+    import torch
+
+    q, kv = [300, 1, 0, 150, 90, 257], [300, 40, 90, 1024, 1025, 700]
+    b = many(Batch4(hk, hq, d, 32, q, kv, seed=41), 1 << 16)
+    dev = b.dev4(kp)
+    n = kp.pages4_attend_ws_bytes(*dev[:1], *dev[3:], b.tokens, hq)
+    each = len(q) * hk * (4 * 128 * d + 1152)
+    assert n == each * ((1 << 16) // 128)
+    ws = torch.full((tiles * each + 64,), 255, dtype=torch.uint8, device="cuda")
+    out, lse = kp.pages4_attend(*dev, return_lse=True, workspace=ws if tiles else ws[:0], max_kv=None if tiles < 100 else 1025)
+    check4(out.float().cpu().numpy(), lse.cpu().numpy(), b.ref4())
+    same = kp.pages4_attend(*dev, return_lse=True, workspace=ws if tiles else ws[:0], max_kv=None if tiles < 100 else 1025)
+    assert torch.equal(out, same[0]) and torch.equal(lse, same[1])
+
+
 @pytest.mark.parametrize("hk,seqs", [(1, 12), (4, 7), (4, 17), (8, 20)])
 def test_cluster_sizes(kp, hk, seqs):
     """Between 12 and 160 blocks: splits in 8, 4 and 2."""

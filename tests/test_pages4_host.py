@@ -87,7 +87,7 @@ def test_pages4_calls_refuse(kp):
     def calls(pg, sq):
         yield append(kp, True, pg, sq, ref(rotary(kp)), GOOD)
         yield lib.kvpool_pages4_read(ref(pg), 0, ref(sq), A, A, None)
-        yield lib.kvpool_pages4_attend(ref(pg), 0, ref(sq), A, 256, 4, None, A, None, 0.0, None)
+        yield lib.kvpool_pages4_attend(ref(pg), 0, ref(sq), A, 256, 4, None, A, None, 0.0, None, 0, None)
 
     for bad in BAD_PAGES:
         for rc in calls(pages4(kp, **bad), seqs(kp)):
@@ -106,8 +106,17 @@ def test_pages4_calls_refuse(kp):
                                        (A, 256, 4, None, None, 0.0), (A, 256, 4, A + 8, None, 0.0),
                                        (A, 256, 4, A, A + 2, 0.0), (A, 256, 4, A, None, -1.0),
                                        (A, 256, 4, A, None, float("inf")), (A, 256, 4, A, None, float("nan"))):
-        assert lib.kvpool_pages4_attend(ref(pg), 0, ref(sq), Q, qs, hq, None, out, lse, scale, None) == INVALID
-    assert lib.kvpool_pages4_attend(None, 0, ref(sq), A, 256, 4, None, A, None, 0.0, None) == INVALID
+        assert lib.kvpool_pages4_attend(ref(pg), 0, ref(sq), Q, qs, hq, None, out, lse, scale, None, 0, None) == INVALID
+    assert lib.kvpool_pages4_attend(ref(pg), 0, ref(sq), A, 256, 4, None, A, None, 0.0, A + 8, 100, None) == INVALID
+    # a workspace where there is use for one: many rows over many keys
+    big = seqs(kp, seqs=3, table_stride=1000, tokens=900)
+    need = lib.kvpool_pages4_attend_ws_bytes(ref(pg), ref(big), 4)
+    assert need == 3 * 2 * 125 * (2 * 128 * 64 * 2 + 1152)
+    assert lib.kvpool_pages4_attend_ws_bytes(ref(pg), ref(seqs(kp, seqs=3, table_stride=1000, tokens=900, max_q=128)), 4) == 0
+    assert lib.kvpool_pages4_attend_ws_bytes(ref(pg), ref(sq), 4) == 0
+    assert lib.kvpool_pages4_attend_ws_bytes(ref(pg), ref(big), 3) == 0
+    assert lib.kvpool_pages4_attend_ws_bytes(None, ref(big), 4) == 0
+    assert lib.kvpool_pages4_attend(None, 0, ref(sq), A, 256, 4, None, A, None, 0.0, None, 0, None) == INVALID
     assert lib.kvpool_pages4_status(ref(pg), None) == INVALID and lib.kvpool_pages4_status(None, None) == INVALID
     for src, dst, n in ((one, one, 1), (one, two, -1), (one, two, 11), (None, two, 1)):
         assert lib.kvpool_pages4_copy(ref(pg), src, dst, n, None) == INVALID
