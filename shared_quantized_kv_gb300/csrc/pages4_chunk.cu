@@ -53,6 +53,7 @@ constexpr uint32_t kCols = 512;         // tensor memory: S0, S1, O0, O1
 // a slot's turn at the tensor cores; the two warps of 32 rows (8 barriers); the rows' factors are read
 constexpr uint32_t kBarQ = 1, kBarDone = 2, kBarRows = 3, kBarTurn = 4, kBarPair = 6, kBarRead = 14;
 constexpr int kSoftmax = 512;           // softmax threads
+constexpr int kEarly = 4;               // scales (in fours) asked for before S has come
 // expander warps of K (20 to 23, 32 keys of a tile each) and of V (0 and 3, 64 each), and how many times 32 keys'
 // codes their own rings hold
 constexpr int kWarpsK = 4, kWarpsV = 2, kRawK = 2, kRawV = 3;
@@ -755,15 +756,24 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
             return ptx::max3(ptx::max3(ptx::max3(x[0], x[1], x[2]), ptx::max3(x[3], x[4], x[5]), x[6]),
                              ptx::max3(x[7], x[8], x[9]), x[10]);
         };
-        // scores of 32 keys times their scales
-        auto times = [&](const float* t, uint32_t (&u)[32]) {
+        // scores of 32 keys times their scales t, the first of which have been asked for
+        auto times = [&](const float4 (&early)[kEarly], const float* t, uint32_t (&u)[32]) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(t + k);
+                const float4 f = k / 4 < kEarly ? early[k / 4 < kEarly ? k / 4 : 0] : *reinterpret_cast<const float4*>(t + k);
                 const float2 x = __fmul2_rn(make_float2(asf(u[k]), asf(u[k + 1])), make_float2(f.x, f.y));
                 const float2 y = __fmul2_rn(make_float2(asf(u[k + 2]), asf(u[k + 3])), make_float2(f.z, f.w));
                 u[k] = asu(x.x), u[k + 1] = asu(x.y), u[k + 2] = asu(y.x), u[k + 3] = asu(y.y);
             }
+        };
+        // (while the scores are on their way from tensor memory: what a tile's scales cost
+        // is the loads' place in the path from S to P)
+        auto ask_early = [&](float4 (&early)[kEarly], const float* t) {
+#pragma unroll
+            for (int k = 0; k < kEarly; ++k)
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(early[k].x), "=f"(early[k].y), "=f"(early[k].z), "=f"(early[k].w)
+                             : "r"(ptx::smem_u32(t + 4 * k)));
         };
         // the row's reference becomes mt (its maximum in both parts) where that passes
         // it; O, which no MMA works on, follows
@@ -797,9 +807,11 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
 #pragma unroll 1
             for (int c = 0; c < 64; c += 32) {
                 uint32_t u[32];
+                float4 early[kEarly];
                 ptx::tmem_ld32(tS + c, u);
+                ask_early(early, tile_scales[i0 % L::slots].k + c);
                 ptx::tmem_wait_ld(u);
-                times(tile_scales[i0 % L::slots].k + c, u);
+                times(early, tile_scales[i0 % L::slots].k + c, u);
                 mask(t0 + c, u, -CUDART_INF_F);
                 m = fmaxf(m, max_of(u) * mul);
             }
@@ -811,8 +823,8 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
         constexpr bool kLeft = !CHANGED;  // the row's factor is left for the exponent
         const float f = kLeft ? mul : 1.0f;
         // the scores of the part's 32 keys from k0 on, -inf where the row sees none
-        auto scores_of = [&](const float* t, int k0, bool whole, uint32_t (&u)[32]) {
-            times(t, u);
+        auto scores_of = [&](const float4 (&early)[kEarly], const float* t, int k0, bool whole, uint32_t (&u)[32]) {
+            times(early, t, u);
             if constexpr (CHANGED) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) u[k] = asu(asf(u[k]) * mul);
@@ -848,9 +860,11 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
 #pragma unroll 1
                 for (int c = 32 * part; c < kTile; c += 64) {
                     uint32_t u[32];
+                    float4 early[kEarly];
                     ptx::tmem_ld32(tS + c, u);
+                    ask_early(early, ts.k + c);
                     ptx::tmem_wait_ld(u);
-                    scores_of(ts.k + c, t0 + c, false, u);
+                    scores_of(early, ts.k + c, t0 + c, false, u);
                     top = fmaxf(top, max_of(u) * f);
                 }
                 if (ptx::bar_or(b_pair, 64, top > m + kLazy || (m == -CUDART_INF_F && top > m))) move_ref(top, it > 0);
@@ -870,9 +884,13 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
                 float2 sum[2] = {};
                 if (any) {
                     uint32_t u[32];
+                    float4 early[kEarly];
+                    uint32_t odd;
                     ptx::tmem_ld32(tSh, u);
+                    ask_early(early, ts.k + in);
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(odd) : "r"(ptx::smem_u32(&ts.odd[in / 32])));
                     ptx::tmem_wait_ld(u);
-                    scores_of(ts.k + in, k0, whole, u);
+                    scores_of(early, ts.k + in, k0, whole, u);
                     const float x = max_of(u) * f;
                     if constexpr (CHANGED) {
                         if (ptx::bar_or(b_pair, 64, x > m + kLazy || (m == -CUDART_INF_F && x > m))) {
@@ -893,7 +911,7 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
                         sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                         return e;
                     };
-                    if (__builtin_expect(!ts.odd[in / 32], 1)) {
+                    if (__builtin_expect(!odd, 1)) {
 #pragma unroll
                         for (int k = 0; k < 16; k += 2) {
                             const float4 t = *reinterpret_cast<const float4*>(&ts.v[in + 2 * k]);
