@@ -42,6 +42,7 @@ constexpr int kUnit = 32;   // keys per unit
 constexpr int kStages = 3;  // units in a warp's ring
 constexpr float kLazyMax = 8.0f;
 constexpr int kMaxSplit = 16;
+constexpr int kWave = 100;  // what a wave of CTAs costs beside its units, in units of an SM
 // Sequences of fewer keys take H q in two fp16 parts.
 constexpr int kLowKeys = 16384;
 // CTAs per SM, by their registers: 8 and 16 rows
@@ -620,11 +621,20 @@ cudaError_t launch_rows(const PagedAttend4& p, int max_q, int max_kv, int sm_cou
     constexpr int kRows = 8 * NR;
     const bool direct = (long long)max_q * a.G <= kRows;
     const long long blocks = direct ? a.s.seqs : (long long)a.s.tokens * a.G / kRows + a.s.seqs;
-    // keys split over a cluster as far as all CTAs still run at once and every warp keeps two units
-    const long long jobs = std::min(blocks, a.s.seqs * (((long long)max_q * a.G + kRows - 1) / kRows)) * a.s.Hk;
-    long long split = std::min<long long>((long long)ctas_per_sm(NR) * sm_count / std::max(1LL, jobs),
-                                          max_kv / (2 * kWarps * kUnit));
-    split = std::max<long long>(1, std::min<long long>(split, kMaxSplit));
+    // Keys split over a cluster, every warp with two units at least, so that the
+    // fullest SM has least to do: its CTAs' units, and for every wave of CTAs a start
+    // and an end that take about as long as kWave units of an SM (32 sequences of 32K
+    // keys, 8 KV heads: 270 us in 2, one wave of 512 CTAs on 152 SMs, 233 in 4; 15 of
+    // 4,096 keys: 29 us in 5, 35 in 10).
+    const long long jobs = std::max(1LL, std::min(blocks, a.s.seqs * (((long long)max_q * a.G + kRows - 1) / kRows)) * a.s.Hk);
+    const long long units = std::max(1, (max_kv + kUnit - 1) / kUnit), most = std::min(kMaxSplit, max_kv / (2 * kWarps * kUnit));
+    long long split = 1, best = LLONG_MAX;
+    for (long long k = 1; k <= std::max(1LL, most); ++k) {
+        const long long ctas = jobs * k, slots = (long long)ctas_per_sm(NR) * sm_count;
+        const long long per_sm = (ctas + sm_count - 1) / sm_count;  // (a CTA alone takes half as long again)
+        const long long cost = (2 * per_sm + 1) * ((units + k - 1) / k) + (ctas + slots - 1) / slots * 2 * kWave;
+        if (cost < best) best = cost, split = k;
+    }
     if (split * blocks > INT_MAX) return cudaErrorInvalidValue;
     if (paged_scored(a))
         return direct ? launch<D, NR, true, true>(p, (int)split, blocks, st)
