@@ -66,15 +66,22 @@ struct Shape {
     static constexpr int regs_issue = MADE ? 64 : 56, regs_many = MADE ? 104 : 88, regs_expand = 72;
 };
 
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < CUDART_INF_F; }
+
 // What the softmax needs to know of a tile's scales, beside the ring: a slot per tile
+// (where V's is not finite: 0, and K's NaN. A row that sees the key then has a sum that is NaN and is done again key by
+// key; for others, whose weight of it is 0, nothing has to be looked at.)
 struct TileScales {
-    float v[kTile];     // V's
-    float k[kTile];     // K's
-    uint32_t odd[4];    // of 32 keys: V's are not all finite
+    float v[kTile];
+    float k[kTile];
+    __device__ __forceinline__ void set(int key, float tk, float tv) {
+        v[key] = finite(tv) ? tv : 0.0f;
+        k[key] = finite(tv) ? tk : CUDART_NAN_F;
+    }
 };
 // A tile in the workspace, as shared memory takes it: K, V, the scales.
 template <int D>
-constexpr int made_bytes() { return 2 * kTile * D * 2 + (int)sizeof(TileScales) + 112; }
+constexpr int made_bytes() { return 2 * kTile * D * 2 + (int)sizeof(TileScales); }
 static_assert(made_bytes<64>() % 128 == 0 && made_bytes<128>() % 128 == 0 && sizeof(TileScales) % 16 == 0, "alignment");
 
 template <int D, bool MADE>
@@ -106,7 +113,6 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
 }
 __device__ __forceinline__ float asf(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t asu(float f) { return __float_as_uint(f); }
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) < CUDART_INF_F; }
 
 // Wait for phase `parity` of the barrier by a whole warp; after kTries tries
 // (each suspends the warp for a while; about a quarter of a second in all) `bad` is set, and
@@ -332,6 +338,7 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
     const PagedAttend& p = p4.a;
     constexpr bool SCORED = KIND != kPlain;
     constexpr bool CHANGED = KIND == kScores || KIND == kWideScores;
+    constexpr bool kQuad = KIND == kPlain;  // the softmax has four rows to a lane, else a row to a lane
     constexpr float kLazy = CHANGED ? kLazyScores : kLazyMax;
     constexpr uint32_t kColS = 0, kColO = 256;  // slot w: 128 w columns on
     extern __shared__ unsigned char smem_raw[];
@@ -667,14 +674,11 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
             cp_commit();
             cp_wait<1>();
             __syncwarp();
-            const bool odd_v = __any_sync(0xffffffffu, !finite(tv));
             const int st = i % L::nst;
             unsigned char* stage = sm + L::ring + st * L::stage;
             if (i >= L::nst) warp_wait(b_empty + 8 * st, ((i / L::nst) - 1) & 1, bad);
             TileScales& ts = tile_scales[i % L::slots];
-            ts.v[key0 + lane] = tv;
-            ts.k[key0 + lane] = tk;
-            if (lane == 0) ts.odd[key0 / 32] = odd_v;
+            ts.set(key0 + lane, tk, tv);
             in.next_batch(i, tile_of);
             ask_scales(i + 1);
             expand_k<D>(in.slot(i, 0), stage, key0, h16, half_sum);
@@ -727,6 +731,11 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
         const bool some = __any_sync(0xffffffffu, live);
         const float slope2 = SCORED && live && p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.0f;
         const float mul = rowf[two ? w * kTile + lr : lr] * (CHANGED ? 1.0f : p.scale_log2);
+        float mul4[4];  // kQuad: of rows quad + 8 a of the warp's 32
+        if constexpr (kQuad)
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+                mul4[a] = rowf[(two ? w * kTile : 0) + (warp & 3) * 32 + (lane >> 2) + 8 * a] * p.scale_log2;
         ptx::bar_sync(kBarRead, kSoftmax);  // (its place is used for other things from here on)
         const uint32_t tS = tmem + kColS + 128 * w + lane_off, tO = tmem + kColO + 128 * w + lane_off;
         float* xch = reinterpret_cast<float*>(sm + L::pair) + w * kTile + lr;
@@ -798,27 +807,190 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
             }
             if (move) m = mt;
         };
-        if (!SCORED && mine > 0 && some) {
-            // The first reference is the maximum of the first half tile. (A row that
-            // sees none of its keys sees none at all: the causal mask alone.)
-            const int i0 = two ? 0 : w, t0 = (ta + i0) * kTile;  // (plain scores: no gap)
-            warp_wait(b_s + 8 * w, 0, bad);
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 64; c += 32) {
-                uint32_t u[32];
-                float4 early[kEarly];
-                ptx::tmem_ld32(tS + c, u);
-                ask_early(early, tile_scales[i0 % L::slots].k + c);
-                ptx::tmem_wait_ld(u);
-                times(early, tile_scales[i0 % L::slots].k + c, u);
-                mask(t0 + c, u, -CUDART_INF_F);
-                m = fmaxf(m, max_of(u) * mul);
+        if constexpr (kQuad) {
+            // A lane has keys 8 j + 2 qi and the next of 32 in four rows, quad + 8 a of the
+            // warp's 32 (the layout of 16 rows x 256 bits): a scale then serves four scores,
+            // not one, and what the loads of scales give each lane is a quarter (2,048
+            // tokens over 16K keys: 466 us, 538 with a row to a lane).
+            const int quad = lane >> 2, qi = lane & 3;
+            constexpr uint32_t k16 = 16u << 16;  // 16 rows on, in tensor memory
+            float qm[4], ql[4], top4[4];
+            int end4[4];
+            const int row0 = (two ? w * kTile : 0) + (warp & 3) * 32 + quad;
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                qm[a] = top4[a] = -CUDART_INF_F, ql[a] = 0.0f;
+                const int i = pages::div_group(p, j_begin + row0 + 8 * a);
+                end4[a] = row0 + 8 * a < nr ? min(b.p0 + i_begin + i + 1, T) : INT_MAX;
             }
-            // products of minus infinity alone are no reference: such a row is done again
-            if (live && m == -CUDART_INF_F && see.some(t0, t0 + 64)) l = CUDART_NAN_F;
-            ptx::bar_sync(b_pair, 64);  // P of either part overwrites what both have read
-        }
+            const int all_see = __reduce_min_sync(0xffffffffu, min(min(end4[0], end4[1]), min(end4[2], end4[3])));
+            // scores (without the rows' factors) of the 32 keys at `in` of the tile, which are keys k0 and on
+            auto load4 = [&](const TileScales& ts, int in, int k0, float2 (&x)[4][4], float2 (&tv)[4]) {  // [row][keys]; V's scales
+                uint32_t u[32];
+                ptx::tmem_ld_16x256(tS + in, u);
+                ptx::tmem_ld_16x256(tS + in + k16, u + 16);
+                float2 t[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // (while S is on its way)
+                    const uint32_t at = ptx::smem_u32(ts.k + in + 8 * j + 2 * qi), at_v = ptx::smem_u32(ts.v + in + 8 * j + 2 * qi);
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(t[j].x), "=f"(t[j].y) : "r"(at));
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(tv[j].x), "=f"(tv[j].y) : "r"(at_v));
+                }
+                ptx::tmem_wait_ld(u);
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int e = 16 * (a >> 1) + 4 * j + 2 * (a & 1);
+                        x[a][j] = __fmul2_rn(make_float2(asf(u[e]), asf(u[e + 1])), t[j]);
+                    }
+                if (k0 + 32 > all_see) {
+#pragma unroll
+                    for (int a = 0; a < 4; ++a)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = k0 + 8 * j + 2 * qi;
+                            if (key >= end4[a]) x[a][j].x = -CUDART_INF_F;
+                            if (key + 1 >= end4[a]) x[a][j].y = -CUDART_INF_F;
+                        }
+                }
+            };
+            auto max8 = [](const float2 (&x)[4]) {
+                return ptx::max3(ptx::max3(x[0].x, x[0].y, x[1].x), ptx::max3(x[1].y, x[2].x, x[2].y), fmaxf(x[3].x, x[3].y));
+            };
+            auto over_lanes = [](float v) {  // the largest of a row's four lanes
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+            };
+            // of this lane's row in the layout of a row per lane
+            auto per_row = [&](const float (&v)[4]) {
+                float r = 0.0f;
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const float y = __shfl_sync(0xffffffffu, v[a], (lane & 7) * 4);
+                    if (lane >> 3 == a) r = y;
+                }
+                return r;
+            };
+            // The references become the maxima of both parts where these have passed them; O follows.
+            auto move4 = [&] {
+                float* x = reinterpret_cast<float*>(sm + L::pair) + w * kTile + (warp & 3) * 32;
+                float al[4];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    top4[a] = over_lanes(top4[a]);
+                    if (!part && qi == 0) x[quad + 8 * a] = top4[a];
+                }
+                ptx::bar_sync(b_pair, 64);
+                if (part) {
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) top4[a] = fmaxf(top4[a], x[quad + 8 * a]);
+                    __syncwarp();
+                    if (qi == 0)
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) x[quad + 8 * a] = top4[a];
+                }
+                ptx::bar_sync(b_pair, 64);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const float mt = part ? top4[a] : x[quad + 8 * a];
+                    const bool move = mt > qm[a] + kLazy || (qm[a] == -CUDART_INF_F && mt > qm[a]);
+                    // (in two steps: a maximum may have passed the reference by up to 2^128, and ex2 gives 0 below 2^-126)
+                    al[a] = move && qm[a] != -CUDART_INF_F ? ptx::ex2(0.5f * (qm[a] - mt)) : 1.0f;
+                    ql[a] = ql[a] * al[a] * al[a];
+                    if (move) qm[a] = mt;
+                }
+                const float of = per_row(al);
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 32) {
+                    uint32_t o[32];
+                    ptx::tmem_ld32(tO + part * (D / 2) + c, o);
+                    ptx::tmem_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = asu(asf(o[k]) * of * of);
+                    ptx::tmem_st32x(tO + part * (D / 2) + c, o);
+                }
+                ptx::tmem_wait_st();
+            };
+            if (mine > 0 && some) {
+                // The first reference is the maximum of the first half tile, which both parts look at.
+                const int i0 = two ? 0 : w, t0 = (ta + i0) * kTile;  // (plain scores: no gap)
+                warp_wait(b_s + 8 * w, 0, bad);
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 32) {
+                    float2 x[4][4], none[4];
+                    load4(tile_scales[i0 % L::slots], c, t0 + c, x, none);
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) qm[a] = fmaxf(qm[a], max8(x[a]) * mul4[a]);
+                }
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    qm[a] = over_lanes(qm[a]);
+                    // products of minus infinity alone are no reference: such a row is done again
+                    if (row0 + 8 * a < nr && qm[a] == -CUDART_INF_F && end4[a] > t0) ql[a] = CUDART_NAN_F;
+                }
+                ptx::bar_sync(b_pair, 64);  // P of either part overwrites what both have read
+            }
+            for (int it = 0; it < mine; ++it) {
+                const int i = two ? it : 2 * it + w;  // tile of this CTA
+                const int t0 = tile_at(i) * kTile;
+                const TileScales& ts = tile_scales[i % L::slots];
+                // A maximum that passes the reference by 2^8 moves it before the next tile
+                // (until then the weights are that much larger, which float32 has room for up to
+                // 2^128; rows beyond it come out infinite and are done again).
+                const bool far = top4[0] > qm[0] + kLazy || top4[1] > qm[1] + kLazy || top4[2] > qm[2] + kLazy || top4[3] > qm[3] + kLazy;
+                const bool moves = it > 0 && some && ptx::bar_or(b_pair, 64, far);
+                warp_wait(b_s + 8 * w, it & 1, bad);
+                ptx::tc_fence_after();
+                if (!some) {  // no row of this warp: only the barriers' counts
+                    __syncwarp();
+                    if (lane < 2) ptx::mbar_arrive(b_p + 16 * w + 8 * lane);
+                    continue;
+                }
+                // (S came after every P V before it: O rests)
+                if (moves) move4();
+#pragma unroll
+                for (int a = 0; a < 4; ++a) top4[a] = -CUDART_INF_F;
+                // The tile's keys in two halves, so that P V of the first runs while P of the second is formed.
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int in = 64 * h + 32 * part;
+                    float2 x[4][4], t[4];
+                    load4(ts, in, t0 + in, x, t);
+                    uint32_t pw[2][8];  // rows quad + 16 hh and + 8
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        top4[a] = fmaxf(top4[a], max8(x[a]) * mul4[a]);
+                        const float ref = qm[a] == -CUDART_INF_F ? 0.0f : qm[a];
+                        const float2 sc = make_float2(mul4[a], mul4[a]), nm = make_float2(-ref, -ref);
+                        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 d = __ffma2_rn(x[a][j], sc, nm);
+                            const float2 e = make_float2(ptx::ex2(d.x), ptx::ex2(d.y)), y = __fmul2_rn(e, t[j]);
+                            sum = __fadd2_rn(sum, e);
+                            pw[a >> 1][2 * j + (a & 1)] = pack_bf2(y.x, y.y);
+                        }
+                        ql[a] += sum.x + sum.y;
+                    }
+                    // P over the part's own columns of S
+                    ptx::tmem_st_16x128(tS + in, pw[0]);
+                    ptx::tmem_st_16x128(tS + in + k16, pw[1]);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(b_p + 16 * w + 8 * h);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                ql[a] += __shfl_xor_sync(0xffffffffu, ql[a], 1);
+                ql[a] += __shfl_xor_sync(0xffffffffu, ql[a], 2);
+            }
+            l = per_row(ql);
+            m = per_row(qm);
+        } else {
         float top = -CUDART_INF_F;  // the part's maximum in the tile before
         constexpr bool kLeft = !CHANGED;  // the row's factor is left for the exponent
         const float f = kLeft ? mul : 1.0f;
@@ -877,18 +1049,15 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
                 const uint32_t tSh = tS + in;
                 const bool whole = __all_sync(0xffffffffu, see.all(k0, k0 + 32));
                 // nothing seen by either part (beyond the diagonal, other documents): weights
-                // of 0 whatever S holds (with the causal mask alone these are the diagonal's
-                // few, and the test costs every tile more than they save)
-                const bool any = !SCORED || __any_sync(0xffffffffu, live && see.some(half, half + 64));
+                // of 0 whatever S holds
+                const bool any = __any_sync(0xffffffffu, live && see.some(half, half + 64));
                 uint32_t pw[16];
                 float2 sum[2] = {};
                 if (any) {
                     uint32_t u[32];
                     float4 early[kEarly];
-                    uint32_t odd;
                     ptx::tmem_ld32(tSh, u);
                     ask_early(early, ts.k + in);
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(odd) : "r"(ptx::smem_u32(&ts.odd[in / 32])));
                     ptx::tmem_wait_ld(u);
                     scores_of(early, ts.k + in, k0, whole, u);
                     const float x = max_of(u) * f;
@@ -911,21 +1080,12 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
                         sum[k & 1] = __fadd2_rn(sum[k & 1], e);
                         return e;
                     };
-                    if (__builtin_expect(!odd, 1)) {
 #pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            const float4 t = *reinterpret_cast<const float4*>(&ts.v[in + 2 * k]);
-                            const float2 a = __fmul2_rn(weights(k), make_float2(t.x, t.y));
-                            const float2 c = __fmul2_rn(weights(k + 1), make_float2(t.z, t.w));
-                            pw[k] = pack_bf2(a.x, a.y), pw[k + 1] = pack_bf2(c.x, c.y);
-                        }
-                    } else {  // what a masked place's scale holds has no say
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float2 e = weights(k);
-                            pw[k] = pack_bf2(e.x == 0.0f ? 0.0f : e.x * ts.v[in + 2 * k],
-                                             e.y == 0.0f ? 0.0f : e.y * ts.v[in + 2 * k + 1]);
-                        }
+                    for (int k = 0; k < 16; k += 2) {
+                        const float4 t = *reinterpret_cast<const float4*>(&ts.v[in + 2 * k]);
+                        const float2 a = __fmul2_rn(weights(k), make_float2(t.x, t.y));
+                        const float2 c = __fmul2_rn(weights(k + 1), make_float2(t.z, t.w));
+                        pw[k] = pack_bf2(a.x, a.y), pw[k + 1] = pack_bf2(c.x, c.y);
                     }
                 } else {
 #pragma unroll
@@ -939,6 +1099,7 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
                 if (lane == 0) ptx::mbar_arrive(b_p + 16 * w + 8 * h);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
+        }
         }
         if (mine > 0) {
             warp_wait(b_fin + 8 * w, 0, bad);  // every MMA of the slot
@@ -1261,10 +1422,7 @@ pages4_make_kernel(const PagedAttend4 p4, const Made made) {
     const bool held = at >= 0 && tile * kTile + key0 + lane < T;
     const float tk = held ? __ldg(p4.Kt + at + (lane & 15)) : 0.0f, tv = held ? __ldg(p4.Vt + at + (lane & 15)) : 0.0f;
     TileScales& ts = *reinterpret_cast<TileScales*>(sm + 2 * kStage);
-    ts.k[key0 + lane] = tk;
-    ts.v[key0 + lane] = tv;
-    const bool odd_v = __any_sync(0xffffffffu, !finite(tv));
-    if (lane == 0) ts.odd[warp] = odd_v;
+    ts.set(key0 + lane, tk, tv);
     uint32_t h16[2][2];
     h16_operands(h16);
     cp_wait<1>();

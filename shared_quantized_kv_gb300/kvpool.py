@@ -389,6 +389,7 @@ def _need(t, dtype, name, dev):
     return t.data_ptr()
 
 
+_WORKSPACE_MOST = 1 << 32  # bytes of a workspace that pages4_attend allocates by itself
 _CURRENT = None
 _NO_STREAM = contextlib.nullcontext()
 
@@ -687,8 +688,8 @@ def pages4_attend(pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=No
     """pages_attend over pages of 4 bits (kvpool_pages4_attend): pages a Pages4,
     the rest and the results as pages_attend's. workspace: a tensor on the
     device, any size (an empty one: none); None: as much as the call has use for
-    (pages4_attend_ws_bytes) is allocated, which a chunk of many tokens does.
-    It changes no result."""
+    (pages4_attend_ws_bytes, which is 0 but for chunks of many tokens; 4 GiB at
+    most) is allocated. It changes no result."""
     import torch
 
     layer = _i32(layer, "layer")
@@ -703,9 +704,14 @@ def pages4_attend(pages, layer, Q, table, kv_len, q_start, max_q=None, max_kv=No
         n = _lib().kvpool_pages4_attend_ws_bytes(ctypes.byref(pg), ctypes.byref(sq), hq) if sq.max_q != 1 else 0
         if not n:
             return None, None, 0
-        # on the stream that uses it, so that the allocator knows it
+        # A table wide enough for sequences that nobody has asks for more than there is: any
+        # size will do. On the stream that uses it, so that the allocator knows it.
+        n = min(n, _WORKSPACE_MOST)
         with _NO_STREAM if stream is None else torch.cuda.stream(stream):
-            ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+            try:
+                ws = torch.empty(n, dtype=torch.uint8, device=Q.device)
+            except torch.cuda.OutOfMemoryError:
+                return None, None, 0
         return ws, ws.data_ptr(), n
 
     return _attend(_lib().kvpool_pages4_attend, pg, dev, layer, Q, table, kv_len, q_start, max_q, max_kv, cap, slopes,

@@ -49,7 +49,7 @@ def test_workspaces_of_any_size(kp, hk, hq, d, tiles):
     b = many(Batch4(hk, hq, d, 32, q, kv, seed=41), 1 << 16)
     dev = b.dev4(kp)
     n = kp.pages4_attend_ws_bytes(*dev[:1], *dev[3:], b.tokens, hq)
-    each = len(q) * hk * (4 * 128 * d + 1152)
+    each = len(q) * hk * (4 * 128 * d + 1024)
     assert n == each * ((1 << 16) // 128)
     ws = torch.full((tiles * each + 64,), 255, dtype=torch.uint8, device="cuda")
     out, lse = kp.pages4_attend(*dev, return_lse=True, workspace=ws if tiles else ws[:0], max_kv=None if tiles < 100 else 1025)

@@ -111,7 +111,7 @@ def test_pages4_calls_refuse(kp):
     # a workspace where there is use for one: many rows over many keys
     big = seqs(kp, seqs=3, table_stride=1000, tokens=900)
     need = lib.kvpool_pages4_attend_ws_bytes(ref(pg), ref(big), 4)
-    assert need == 3 * 2 * 125 * (2 * 128 * 64 * 2 + 1152)
+    assert need == 3 * 2 * 125 * (2 * 128 * 64 * 2 + 1024)
     assert lib.kvpool_pages4_attend_ws_bytes(ref(pg), ref(seqs(kp, seqs=3, table_stride=1000, tokens=900, max_q=128)), 4) == 0
     assert lib.kvpool_pages4_attend_ws_bytes(ref(pg), ref(sq), 4) == 0
     assert lib.kvpool_pages4_attend_ws_bytes(ref(pg), ref(big), 3) == 0
