@@ -13,6 +13,10 @@
 // head-vector, each lane two pieces of 8 channels that lie D / 2 apart: the
 // pairs (i, i + D / 2) are then in one lane, a lane's angles serve all heads, and
 // of the transform's log2 D stages four stay in registers.
+// Measured: 17 thousand tokens of 32 query heads on 8 of 128, half of the channels
+// turned, 576 MB in 99 us (5.8 TB/s); into 4 bits with 64 query heads, 620 MB in
+// 115 us; 15 tokens in 3 us of a captured graph. Blocks of 256 threads leave a
+// token's tail of heads idle (124 us), of 64 take 97 but 3.8 us for the 15 tokens.
 #include "pages4.cuh"
 
 namespace kvp {
@@ -277,6 +281,8 @@ append_kernel(const AppendArgs a) {
 // e_0). The sums are whole numbers up to 8 D + D / 2, exact in fp16 in any order,
 // two to a register; one rounding to float32 with t, one to bf16. A warp takes a
 // token, its D / 16 lanes a head-vector, several of them asked for at once.
+// Memory bound: 42,600 tokens of 8 KV heads, 316 MB in 62 us (a block per token,
+// sums in float32: 111).
 constexpr int kReadWarps = 4, kReadAhead = 4;
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }

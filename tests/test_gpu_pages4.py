@@ -432,3 +432,57 @@ def test_agents_lives(kp, bits):
             cache.read(0, [b])
     assert cache.status() == 0
     cache.close()
+
+
+def test_joint_softmax_takes_bf16_pages(kp):
+    """A 4-bit cache is refused there, by name."""
+    import torch
+
+    cache = kp.PagedCache(1, 2, 64, 4, 16, bits=4)
+    batch = cache.grow([cache.new()], [3])
+    pool = kp.KVPool(1, 2, 64, 130, [4])
+    Q = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="16 bits"):
+        pool.attend_pages(0, Q, cache, batch)
+    with pytest.raises(ValueError):
+        kp.pages4_attend(cache.pages4._replace(K=cache.pages4.K.view(torch.int8)), 0, Q, batch.table, batch.kv_len, batch.q_start)
+    with pytest.raises(ValueError):
+        kp.pages4_attend(cache.pages4._replace(V_scale=cache.pages4.V_scale[:, :2]), 0, Q, batch.table, batch.kv_len, batch.q_start)
+    with pytest.raises(ValueError):
+        kp.pages4_attend(cache.pages4, 0, Q.float(), batch.table, batch.kv_len, batch.q_start)
+    with pytest.raises(ValueError):
+        cache.append(0, Q[:, :2], Q[:, :2], batch, Q=Q)
+    with pytest.raises(ValueError):
+        cache.append(0, Q[:2, :2], Q[:2, :2], batch)
+    pool.close()
+    cache.close()
+
+
+@pytest.mark.parametrize("rows", [1, 90])
+def test_two_graphs_and_an_eager_call_at_once(kp, rows):
+    """Two captured calls over one cache (each with a workspace of its own) and an eager one, replayed side by side."""
+    import torch
+
+    b = Batch4(2, 16, 64, 16, [rows, 1], [700, 300], seed=51)
+    b.table = np.pad(b.table, ((0, 0), (0, 4096 - b.table.shape[1])), constant_values=-9)
+    dev = b.dev4(kp)
+    outs = [(torch.empty(b.tokens, b.hq, b.d, dtype=torch.bfloat16, device="cuda"), torch.empty(b.tokens, b.hq, device="cuda"))
+            for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graphs = []
+    for st, (o, z) in zip(streams[:2], outs):
+        st.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            kp.pages4_attend(*dev, out=o, lse=z)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+        kp.pages4_attend(*dev, out=outs[2][0], lse=outs[2][1], stream=streams[2])
+    torch.cuda.synchronize()
+    for o, z in outs:
+        assert torch.equal(o, outs[0][0]) and torch.equal(z, outs[0][1])
+    check4(outs[0][0].float().cpu().numpy(), outs[0][1].cpu().numpy(), b.ref4())
