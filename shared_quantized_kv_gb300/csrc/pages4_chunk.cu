@@ -33,15 +33,16 @@
 // Every wait on a barrier in memory is bounded; one that expires is recorded in
 // the status word, and the CTA runs to its end without waiting again.
 //
-// Measured on 2,048 new tokens over 16K keys, 32 query heads on 8 of 128: 467 us
-// with a workspace, 21 of them to make it (1.10 PFLOP/s; the bf16 pages take 352), 743
+// Measured on 2,048 new tokens over 16K keys, 32 query heads on 8 of 128: 448 us
+// with a workspace, 21 of them to make it (1.15 PFLOP/s; the bf16 pages take 352), 743
 // without. The scales cost most beside the products: a version without their
 // multiplications took 344 us. What got it there, without a workspace at first: one
 // warp group for K and V 1001 us, V by the two warps that had nothing to do 765,
 // registers for K's expanders 743; the workspace 546; scales asked for while S is on
-// its way 521; four rows to a lane and no test of the scales 467. Keys' operands with
-// their scales in them, in fp16 (652 us against 743 without a workspace), leave the
-// log of the sum 1e-5 off, which rows of few keys show.
+// its way 521; four rows to a lane and no test of the scales 467; queries asked for at
+// once and the output's transform in registers 448. Keys' operands with their scales
+// in them, in fp16 (652 us against 743 without a workspace), leave the log of the sum
+// 1e-5 off, which rows of few keys show.
 #include <algorithm>
 #include <mutex>
 
@@ -713,17 +714,23 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
         // the rows, a warp each, in fp16 times a power of two (rows past the block repeat its last)
         float* rowf = reinterpret_cast<float*>(sm + L::pair);
         {
+            // (all of a warp's rows are asked for before the first is looked at: 4 at a time took 6 us of a CTA's start)
+            constexpr int kEach = kRows / (kSoftmax / 32);
             const int nq = two ? kRows : kTile;
-#pragma unroll 4
-            for (int r = warp - 4; r < nq; r += kSoftmax / 32) {
-                const int rr = min(r, nr - 1), i = pages::div_group(p, j_begin + rr);
+            uint2 v[kEach];
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int rr = min(warp - 4 + u * (kSoftmax / 32), nr - 1), i = pages::div_group(p, j_begin + rr);
                 const uint16_t* src = p.Q + (long long)(b.q0 + i_begin + i) * p.q_stride +
                                       (long long)(g * p.G + j_begin + rr - i * p.G) * D;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (lane < D / 4) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + lane);
-                    x = make_float4(asf(v.x << 16), asf(v.x & 0xFFFF0000u), asf(v.y << 16), asf(v.y & 0xFFFF0000u));
-                }
+                v[u] = make_uint2(0u, 0u);
+                if (lane < D / 4 && (two || u < kEach / 2)) v[u] = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+            }
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int r = warp - 4 + u * (kSoftmax / 32);
+                if (r >= nq) break;
+                const float4 x = make_float4(asf(v[u].x << 16), asf(v[u].x & 0xFFFF0000u), asf(v[u].y << 16), asf(v[u].y & 0xFFFF0000u));
                 const uint32_t top = __reduce_max_sync(
                     0xffffffffu, max(max(asu(fabsf(x.x)), asu(fabsf(x.y))), max(asu(fabsf(x.z)), asu(fabsf(x.w)))));
                 const int e = min(max((int)(top >> 23) - 126, -122), 126);
@@ -1151,44 +1158,55 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
         constexpr int HC = D / 2;
         const int c0 = part * HC;
         if (direct) {
-            // The slot's Q (no MMA reads it any more) takes 16 rows of every 32 at a time in
-            // float32, pieces of 4 channels exchanged by the row's number; the two warps then
-            // transform a row at a time and write it.
-            const float inv = 1.0f / l;  // (not used where l is 0)
+            // Both threads of a row read all of its O: the transform's stage over channels D / 2
+            // apart leaves part 0 the sums and part 1 the differences, the other stages stay in
+            // registers. The slot's Q (no MMA reads it any more) takes the rows in bf16, pieces of
+            // 8 channels exchanged by the row's number, and the two warps write them in whole
+            // lines. (Over lanes, four channels to each, the transform took 6 us.)
+            const float inv = 1.0f / l, sign = part ? -1.0f : 1.0f;  // (inv: not used where l is 0)
             unsigned char* stage = sm + w * L::stage + (warp & 3) * 32 * (D * 2);
-            constexpr int C4 = D / 4, kPer = 32 / C4;  // pieces of a row, rows of a warp at a time
+            constexpr int C8 = D / 8, kPer = 32 / C8;  // pieces of a row, rows of a warp at a time
             if (live && !part) finish(tok, head, state_m, l * down);
             const long long at = live ? ((long long)tok * p.Hq + head) * D : -1;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-                for (int c = c0; c < c0 + HC; c += 32) {
-                    uint32_t o[32];
-                    ptx::tmem_ld32(tO + c, o);
-                    ptx::tmem_wait_ld(o);
+            float2 y[HC / 2];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        float4 y = make_float4(asf(o[k]), asf(o[k + 1]), asf(o[k + 2]), asf(o[k + 3]));
-                        again = again || (live && l != 0.0f && !(finite(y.x) && finite(y.y) && finite(y.z) && finite(y.w)));
-                        y = l == 0.0f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                      : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-                        if ((lane >> 4) == half)
-                            *reinterpret_cast<float4*>(stage + (lane & 15) * (D * 4) +
-                                                       ((((c + k) / 4) ^ ((lane & 15) & (C4 - 1))) << 4)) = y;
+            for (int c = 0; c < HC; c += 16) {
+                uint32_t u[32];  // 16 channels, and those D / 2 on
+                ptx::tmem_ld16(tO + c, *reinterpret_cast<uint32_t(*)[16]>(u));
+                ptx::tmem_ld16(tO + HC + c, *reinterpret_cast<uint32_t(*)[16]>(u + 16));
+                ptx::tmem_wait_ld(u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float a = fmaf(sign, asf(u[16 + 2 * k]), asf(u[2 * k])) * inv;
+                    const float d = fmaf(sign, asf(u[17 + 2 * k]), asf(u[2 * k + 1])) * inv;
+                    y[c / 2 + k] = make_float2(a + d, a - d);
+                }
+            }
+#pragma unroll
+            for (int h = 1; h < HC / 2; h <<= 1)
+#pragma unroll
+                for (int i = 0; i < HC / 2; ++i)
+                    if (!(i & h)) {
+                        const float2 a = y[i], d = y[i + h];
+                        y[i] = __fadd2_rn(a, d);
+                        y[i + h] = __ffma2_rn(d, make_float2(-1.0f, -1.0f), a);
                     }
-                }
-                ptx::bar_sync(b_pair, 64);
-#pragma unroll 2
-                for (int k = 0; k < 8 / kPer; ++k) {
-                    const int r = 8 * part + kPer * k + lane / C4, c4 = lane % C4;  // of the 16
-                    float4 y = *reinterpret_cast<const float4*>(stage + r * (D * 4) + ((c4 ^ (r & (C4 - 1))) << 4));
-                    pages::transform4<D>(y);
-                    const long long row_at = __shfl_sync(0xffffffffu, at, 16 * half + r);
-                    if (row_at >= 0)
-                        *reinterpret_cast<uint2*>(p.out + row_at + c4 * 4) =
-                            make_uint2(pack_bf2(y.x, y.y), pack_bf2(y.z, y.w));
-                }
-                ptx::bar_sync(b_pair, 64);
+            // (an infinity or NaN in O is in the row's every output)
+            again = again || (live && l != 0.0f && !finite(y[0].x));
+#pragma unroll
+            for (int k = 0; k < HC / 8; ++k) {
+                uint4 v = make_uint4(pack_bf2(y[4 * k].x, y[4 * k].y), pack_bf2(y[4 * k + 1].x, y[4 * k + 1].y),
+                                     pack_bf2(y[4 * k + 2].x, y[4 * k + 2].y), pack_bf2(y[4 * k + 3].x, y[4 * k + 3].y));
+                if (l == 0.0f) v = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(stage + lane * (D * 2) + (((part * (HC / 8) + k) ^ (lane & (C8 - 1))) << 4)) = v;
+            }
+            ptx::bar_sync(b_pair, 64);
+#pragma unroll 4
+            for (int k = 0; k < 16 / kPer; ++k) {
+                const int r = 16 * part + kPer * k + lane / C8, c8 = lane % C8;  // of the 32
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + r * (D * 2) + ((c8 ^ (r & (C8 - 1))) << 4));
+                const long long row_at = __shfl_sync(0xffffffffu, at, r);
+                if (row_at >= 0) *reinterpret_cast<uint4*>(p.out + row_at + c8 * 8) = v;
             }
             const unsigned odds = __ballot_sync(0xffffffffu, again);
             if (part && lane == 0) *flags = odds;
