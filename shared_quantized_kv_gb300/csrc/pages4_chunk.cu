@@ -33,14 +33,14 @@
 // Every wait on a barrier in memory is bounded; one that expires is recorded in
 // the status word, and the CTA runs to its end without waiting again.
 //
-// Measured on 2,048 new tokens over 16K keys, 32 query heads on 8 of 128: 448 us
-// with a workspace, 21 of them to make it (1.15 PFLOP/s; the bf16 pages take 352), 743
+// Measured on 2,048 new tokens over 16K keys, 32 query heads on 8 of 128: 442 us
+// with a workspace, 15 of them to make it (1.16 PFLOP/s; the bf16 pages take 352), 743
 // without. The scales cost most beside the products: a version without their
 // multiplications took 344 us. What got it there, without a workspace at first: one
 // warp group for K and V 1001 us, V by the two warps that had nothing to do 765,
 // registers for K's expanders 743; the workspace 546; scales asked for while S is on
 // its way 521; four rows to a lane and no test of the scales 467; queries asked for at
-// once and the output's transform in registers 448. Keys' operands with their scales
+// once and the output's transform in registers 448; K's and V's tiles made apart 442. Keys' operands with their scales
 // in them, in fp16 (652 us against 743 without a workspace), leave the log of the sum
 // 1e-5 off, which rows of few keys show.
 #include <algorithm>
@@ -1425,9 +1425,10 @@ cudaError_t launch(const PagedAttend4& p4, const Made& made, int max_q, int max_
 }
 
 // Tiles of the workspace: K expanded, V expanded, the scales, as the kernel takes
-// them. A CTA per tile of a sequence and KV head, four warps of 32 keys, through
-// shared memory and out in bulk. Memory bound: 512 bytes written per key and head of
-// 128 (16K keys of 8 heads, 67 MB).
+// them. A CTA per tile's K with the scales, or V, of a sequence and KV head, four
+// warps of 32 keys, through shared memory and out in bulk. Memory bound, 650 bytes per
+// key and head of 128, 512 of them written: 4,096 keys of 8 heads of 19 sequences in 62
+// us, 6.6 TB/s (88 with K and V made by one CTA, two of which an SM has room for).
 constexpr int kMakeThreads = 128;
 template <int D>
 __global__ void __launch_bounds__(kMakeThreads)
@@ -1438,36 +1439,40 @@ pages4_make_kernel(const PagedAttend4 p4, const Made made) {
     const PagedAttend& p = p4.a;
     const PagedSeqs& s = p.s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, key0 = warp * 32;
-    const int seq = blockIdx.z, g = blockIdx.y, tile = blockIdx.x;
+    const int seq = blockIdx.z, g = blockIdx.y, tile = blockIdx.x / 2;
+    const bool values = blockIdx.x & 1;
     const int len = pages::length_of(s, seq), T = pages::held_tokens(s, len);
     if (pages::row_begin(s, seq + 1) <= pages::row_begin(s, seq)) return;  // no rows, nobody reads it
     if (!made.has(T) || tile * kTile >= T) return;
-    CodeReader<D, 2> in(p, s, g, seq, T, 1, key0, lane, sm + 2 * kStage + sizeof(TileScales) + warp * 2 * kCodes);
+    CodeReader<D, 2> in(p, s, g, seq, T, 1, key0, lane, sm + kStage + sizeof(TileScales) + warp * kCodes);
     in.start([&](int) { return tile; });
-    in.ask(p.K, 0, 0);
+    in.ask(values ? p.V : p.K, 0, 0);
     cp_commit();
-    in.raw += kCodes;
-    in.ask(p.V, 0, 0);
-    cp_commit();
-    const int at = in.vector_of(0, lane >> 4);
-    const bool held = at >= 0 && tile * kTile + key0 + lane < T;
-    const float tk = held ? __ldg(p4.Kt + at + (lane & 15)) : 0.0f, tv = held ? __ldg(p4.Vt + at + (lane & 15)) : 0.0f;
-    TileScales& ts = *reinterpret_cast<TileScales*>(sm + 2 * kStage);
-    ts.set(key0 + lane, tk, tv);
-    uint32_t h16[2][2];
-    h16_operands(h16);
-    cp_wait<1>();
-    __syncwarp();
-    expand_k<D>(in.raw - kCodes, sm, key0, h16, (lane & 3) == 0 ? (D == 128 ? 0x5400u : 0x5000u) : 0u);
-    cp_wait<0>();
-    __syncwarp();
-    expand_v<D>(in.raw, sm + kStage, key0);
+    if (values) {
+        cp_wait<0>();
+        __syncwarp();
+        expand_v<D>(in.raw, sm, key0);
+    } else {
+        const int at = in.vector_of(0, lane >> 4);
+        const bool held = at >= 0 && tile * kTile + key0 + lane < T;
+        const float tk = held ? __ldg(p4.Kt + at + (lane & 15)) : 0.0f, tv = held ? __ldg(p4.Vt + at + (lane & 15)) : 0.0f;
+        reinterpret_cast<TileScales*>(sm + kStage)->set(key0 + lane, tk, tv);
+        uint32_t h16[2][2];
+        h16_operands(h16);
+        cp_wait<0>();
+        __syncwarp();
+        expand_k<D>(in.raw, sm, key0, h16, (lane & 3) == 0 ? (D == 128 ? 0x5400u : 0x5000u) : 0u);
+    }
     ptx::fence_proxy_async();
     __syncthreads();
     if (threadIdx.x == 0) {
         unsigned char* dst = made.tiles + (((long long)seq * s.Hk + g) * made.room + tile) * made_bytes<D>();
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_u32(sm)),
-                     "r"(2 * kStage + (int)sizeof(TileScales)) : "memory");
+        auto copy = [](unsigned char* to, const unsigned char* from, int bytes) {
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(ptx::smem_u32(from)),
+                         "r"(bytes) : "memory");
+        };
+        copy(dst + (values ? kStage : 0), sm, kStage);
+        if (!values) copy(dst + 2 * kStage, sm + kStage, (int)sizeof(TileScales));
         ptx::bulk_commit();
         ptx::bulk_wait_read();  // (shared memory stays until it has been read)
     }
@@ -1475,7 +1480,7 @@ pages4_make_kernel(const PagedAttend4 p4, const Made made) {
 
 template <int D>
 cudaError_t launch_make(const PagedAttend4& p4, const Made& made, cudaStream_t st) {
-    constexpr int smem = 2 * kTile * D * 2 + (int)sizeof(TileScales) + 4 * 2 * (32 * D / 2) + 128;
+    constexpr int smem = kTile * D * 2 + (int)sizeof(TileScales) + 4 * (32 * D / 2) + 128;
     static std::once_flag once[kPagedDevices];
     static cudaError_t opt[kPagedDevices];
     int device = 0;
@@ -1486,7 +1491,7 @@ cudaError_t launch_make(const PagedAttend4& p4, const Made& made, cudaStream_t s
         opt[device] = cudaFuncSetAttribute(pages4_make_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (opt[device] != cudaSuccess) return opt[device];
-    pages4_make_kernel<D><<<dim3(made.room, p4.a.s.Hk, p4.a.s.seqs), kMakeThreads, smem, st>>>(p4, made);
+    pages4_make_kernel<D><<<dim3(2 * made.room, p4.a.s.Hk, p4.a.s.seqs), kMakeThreads, smem, st>>>(p4, made);
     return cudaGetLastError();
 }
 
