@@ -34,15 +34,15 @@
 // the status word, and the CTA runs to its end without waiting again.
 //
 // Measured on 2,048 new tokens over 16K keys, 32 query heads on 8 of 128: 442 us
-// with a workspace, 15 of them to make it (1.16 PFLOP/s; the bf16 pages take 352), 743
+// with a workspace, 15 of them to make it (1.16 PFLOP/s; the bf16 pages take 352), 748
 // without. The scales cost most beside the products: a version without their
 // multiplications took 344 us. What got it there, without a workspace at first: one
 // warp group for K and V 1001 us, V by the two warps that had nothing to do 765,
 // registers for K's expanders 743; the workspace 546; scales asked for while S is on
 // its way 521; four rows to a lane and no test of the scales 467; queries asked for at
-// once and the output's transform in registers 448; K's and V's tiles made apart 442. Keys' operands with their scales
-// in them, in fp16 (652 us against 743 without a workspace), leave the log of the sum
-// 1e-5 off, which rows of few keys show.
+// once and the output's transform in registers 448; K's and V's tiles made apart 442.
+// Keys' operands with their scales in them, in fp16 (652 us against 743 without a
+// workspace), leave the log of the sum 1e-5 off, which rows of few keys show.
 #include <algorithm>
 #include <mutex>
 
