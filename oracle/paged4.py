@@ -90,18 +90,25 @@ def attend(u_k, t_k, u_v, t_v, Q, table, kv_len, q_start, P, cap=0.0, slopes=Non
            scale=None):
     """Float64 attention over one layer's codes [pages, kv_heads, P, d] and
     scales [pages, kv_heads, P]: (out, lse, tol, tol_lse). The last two bound a
-    kernel that
+    kernel whose operands of the first product are exact, or H q in two fp16
+    parts, and which rounds weights to bf16 once. Where many independent
+    roundings meet, six standard deviations of their sum are taken (a rounding is
+    uniform within half a step: 6 / sqrt(3) = 3.5 half steps), else the worst.
 
-    * rounds H q to fp16, and code times scale to fp16 (each 2^-11 relative,
-      independent from channel to channel: six standard deviations of both are
-      1.5 * 2^-9 of the root of the sum of squares) and the scale itself once
-      (2^-11 of the score),
-    * adds 1024 + u with the constants' share taken off (d / 16 matrix steps, each
-      2^-23 of the partial sums, whose size the constants make: `big`),
-    * rounds weights to bf16 (2^-8 of the weighted mean of |v|), code times scale
-      of V to bf16 (2^-8 relative, independent: six standard deviations are 3.5 *
-      2^-8 of the root of the sum of squares), the output to bf16 (2^-8), and
-    * sums T terms in float32."""
+    Scores, of c = u - 7.5, y = H q, z = H c, t the key's scale:
+    * the transform of q in float32: 7 stages, 6 sqrt(7 / 3) 2^-24 < 12 * 2^-24 of |q| |c|;
+    * two fp16 parts: 2^-22 of each y_i, and 2^-20 of the largest |q_i| where the low part is
+      subnormal (steps of 2^-24, sixteen times that for the channels which meet 16 (u - 8), of
+      a row whose largest value lies in [1/2, 1));
+    * n = d / 8 matrix steps (two parts of d / 16), each of 17 terms aligned to the largest with 24 bits or more
+      and cut: 6 sqrt(17 n / 12) steps of 2^-23 of the partial sums if the cuts are independent,
+      and n more if all cut the sum towards 0. Partial sums are as large as the constant term,
+      the sum itself and four standard deviations of the products' sum, whichever way the product is taken;
+    * eight float32 roundings of the score, and of its distance from the reference.
+    The sum of n weights: chains of n / 32 additions (a row's keys go to 32 lanes and more), or of n
+    where a row is done again key by key, and 40 of joins and exponentials.
+    Outputs: weights bf16, 2^-8 each; matrix steps of 16 keys, as above, their errors independent
+    from channel to channel of H o; the transform; half a step of bf16 at the end."""
     d = u_k.shape[-1]
     hk = u_k.shape[1]
     H = hadamard(d)
@@ -110,7 +117,9 @@ def attend(u_k, t_k, u_v, t_v, Q, table, kv_len, q_start, P, cap=0.0, slopes=Non
     scale = d ** -0.5 if scale is None else scale
     out, tol = np.full((n_tok, hq, d), np.nan), np.full((n_tok, hq, d), np.nan)
     lse, tol_lse = np.full((n_tok, hq), np.nan), np.full((n_tok, hq), np.nan)
-    even = np.arange(d) % 4 < 2  # channels that meet 1024 + u; the others 1024 + 16 u, a sixteenth of H q
+    six = 6 / 3 ** 0.5
+    steps = d / 8
+    cuts = (6 * (17 * steps / 12) ** 0.5 + steps) * 2.0 ** -23
     for s in range(len(kv_len)):
         a, b, T = int(q_start[s]), int(q_start[s + 1]), int(kv_len[s])
         page, slot = token_slots(table[s], 0, T, P)
@@ -118,6 +127,8 @@ def attend(u_k, t_k, u_v, t_v, Q, table, kv_len, q_start, P, cap=0.0, slopes=Non
             c = u_k[page, g, slot].astype(np.float64) - 7.5
             t = t_k[page, g, slot].astype(np.float64)
             v = values(u_v[page, g, slot], t_v[page, g, slot])
+            c2, z2, v2 = c ** 2, (c @ H) ** 2, v ** 2
+            norm, size = np.sqrt(c2.sum(-1)), np.sqrt(v2.sum(-1))
             for h in range(g * G, g * G + G):
                 for i in range(b - a):
                     p = T - (b - a) + i
@@ -126,12 +137,16 @@ def attend(u_k, t_k, u_v, t_v, Q, table, kv_len, q_start, P, cap=0.0, slopes=Non
                     if not m.any():
                         out[r], lse[r], tol[r], tol_lse[r] = 0.0, -np.inf, 0.0, 0.0
                         continue
-                    y = H @ Q[r].astype(np.float64)
-                    x = scale * t[m] * (c[m] @ y)
-                    off = abs((y * np.where(even, 1031.5, 71.5)).sum())
-                    big = off + 3 * 1040 * np.sqrt((y[even] ** 2).sum())
-                    e = scale * t[m] * (1.5 * 2.0 ** -9 * np.sqrt(c[m] ** 2 @ y ** 2) + (d / 16 + 1) * 2.0 ** -23 * big)
-                    e = e + (2.0 ** -11 + 2.0 ** -21) * np.abs(x)
+                    q = Q[r].astype(np.float64)
+                    y = H @ q
+                    dot = c[m] @ y
+                    x = scale * t[m] * dot
+                    ways = np.sqrt(c2[m] @ y ** 2)
+                    partial = np.abs(dot) + np.maximum(0.5 * abs(y.sum()) + 4 * (ways + 0.5 * np.sqrt((y ** 2).sum())),
+                                                       4 * np.sqrt(z2[m] @ q ** 2))
+                    e = scale * t[m] * (12 * 2.0 ** -24 * np.sqrt((q ** 2).sum()) * norm[m] + six * 2.0 ** -22 * ways
+                                        + six * 2.0 ** -20 * np.abs(q).max() * norm[m] + cuts * partial)
+                    e = e + 2.0 ** -21 * np.abs(x)
                     if cap:
                         x = cap * np.tanh(x / cap)
                         e = e + cap * 2.0 ** -21
@@ -139,13 +154,20 @@ def attend(u_k, t_k, u_v, t_v, Q, table, kv_len, q_start, P, cap=0.0, slopes=Non
                         far = float(slopes[h]) * np.abs(p - np.arange(T)[m])
                         x, e = x - far, e + 2.0 ** -22 * far
                     top = x.max()
+                    e = e + 2.0 ** -23 * np.abs(x) + 2.0 ** -23 * (top - x)
                     w = np.exp(x - top)
                     w, l = w / w.sum(), np.log(w.sum())
                     out[r], lse[r] = w @ v[m], top + l
-                    e = e.max() + 2.0 ** -23 * np.abs(x).max()
-                    size = np.sqrt((v[m] ** 2).sum(-1))
-                    tol[r] = (2.0 ** -8 * np.abs(out[r])
-                              + (2.0 ** -8 * (1 + 2.0 ** -7) + np.expm1(2 * e + 2.0 ** -21)) * (w @ np.abs(v[m]))
-                              + 3.5 * 2.0 ** -8 * np.sqrt((w ** 2 * size ** 2).sum() / d) + T * 2.0 ** -23 * (w @ size) + 1e-30)
-                    tol_lse[r] = e + T * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * abs(lse[r])
+                    n = x.size
+                    chain = (n / 32 + six * n ** 0.5 + 40) * 2.0 ** -24
+                    grown = np.exp(np.minimum(e, 50.0))
+                    mean = np.log(w @ grown)
+                    tol_lse[r] = mean + chain + 2.0 ** -20 + 2.0 ** -22 * abs(lse[r])
+                    keys = n / 16 + 16
+                    spread = np.sqrt(w ** 2 @ v2[m])
+                    tol[r] = (2.0 ** -8 * (1 + 2.0 ** -7) * (np.abs(out[r]) + np.minimum(w @ np.abs(v[m]), six * spread))
+                              + (w * (grown * np.exp(mean) - 1)) @ np.abs(v[m]) + (chain + 2.0 ** -21) * np.abs(out[r])
+                              + 6 * (17 * keys / 12) ** 0.5 * 2.0 ** -23 * (w @ size[m]) / d ** 0.5
+                              + keys * 2.0 ** -23 * (np.abs(out[r]) + 3 * spread)
+                              + 12 * 2.0 ** -24 * np.sqrt((out[r] ** 2).sum()) + 1e-30)
     return out, lse, tol, tol_lse
