@@ -8,9 +8,11 @@
 // running reference m per row, p = 2^(x - m), O and l rescaled when a score
 // passes m by more than 2^8. The weights p t' are rounded to bf16 (off by at
 // most 2^-8 of each, as the output's own rounding is of it), H q to two fp16
-// parts (a power of two has brought the row's largest value into [1/2, 1)), as
-// one part alone, off by 2^-11, is seen in the log of the sum of fewer keys than
-// kLowKeys. Codes enter the
+// parts (a power of two has brought the row's largest value into [1/2, 1)). One
+// part alone, off by 2^-11, leaves the log of the sum 1e-6 off (relative) where
+// 16K keys weigh alike, but 1e-4 where a window, a document or a peaked row leaves
+// few keys that count, at any length; the second costs 32 sequences of 32K keys
+// 7 %. Codes enter the
 // products exactly: of Q K^T as fp16 u - 8 or 16 (u - 8) (one mask and one
 // addition; the sixteenth is in that channel's H q, the other half of a step is
 // the product's first summand), of P V as bf16 u - 7.5.
@@ -40,7 +42,6 @@
 // multiplication (326 against 301).
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "pages4.cuh"
 
@@ -55,12 +56,6 @@ constexpr int kStages = 3;  // units in a warp's ring
 constexpr float kLazyMax = 8.0f;
 constexpr int kMaxSplit = 16;
 constexpr int kWave = 100;  // what a wave of CTAs costs beside its units, in units of an SM
-// Sequences of fewer keys take H q in two fp16 parts. With one the scores are off by
-// up to 2^-11 of each product, independently, and the row's factor is chosen so that
-// the rounded row's product with the row itself is exact: the log of the sum is then
-// 5e-6 off (relative) at 2,048 keys, 1e-6 at 16K, 4e-7 at 32K (two parts: 5e-8), and
-// 32K keys take 270 us instead of 290.
-constexpr int kLowKeys = 16384;
 // CTAs per SM, by their registers: 8 and 16 rows
 constexpr int ctas_per_sm(int NR) { return NR == 1 ? 4 : 3; }
 
@@ -168,7 +163,6 @@ pages4_rows_kernel(const PagedAttend4 p4) {
         if (!pages::find_block(s, p.G, kRows, blockIdx.x / S, b)) return;
     }
     const int T = b.T;
-    const bool low = T < kLowKeys;  // H q in two parts
     const int32_t* table = s.table + (long long)b.seq * s.tstride;
 
     for (;; ++b.blk) {
@@ -194,29 +188,21 @@ pages4_rows_kernel(const PagedAttend4 p4) {
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
             x.x *= down, x.y *= down, x.z *= down, x.w *= down;
             pages::transform4<D>(x);
-            const float4 y = x;
+            float sum = (x.x + x.y) + (x.z + x.w);
             // channels 4 l + 2 and + 3 meet 16 (u - 8)
             x.z *= 0.0625f, x.w *= 0.0625f;
             const __half2 h0 = __floats2half2_rn(x.x, x.y), h1 = __floats2half2_rn(x.z, x.w);
             const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
             const __half2 l0 = __floats2half2_rn(x.x - f0.x, x.y - f0.y), l1 = __floats2half2_rn(x.z - f1.x, x.w - f1.y);
-            // (with one part: the factor that makes the rounded row's product with the row itself exact)
-            float sum = low ? (y.x + y.y) + (y.z + y.w) : (f0.x + f0.y) + 16.0f * (f1.x + f1.y);
-            float yy = fmaf(y.x, y.x, y.y * y.y) + fmaf(y.z, y.z, y.w * y.w);
-            float yr = fmaf(y.x, f0.x, y.y * f0.y) + 16.0f * fmaf(y.z, f1.x, y.w * f1.y);
 #pragma unroll
-            for (int o = D / 8; o; o >>= 1) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                yy += __shfl_xor_sync(0xffffffffu, yy, o);
-                yr += __shfl_xor_sync(0xffffffffu, yr, o);
-            }
+            for (int o = D / 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             auto bits = [](const __half2& h) { return *reinterpret_cast<const uint32_t*>(&h); };
             if (lane < D / 4)  // step lane % KS of the quarter-row lane / KS
                 *reinterpret_cast<uint4*>(sm + L::q + (((r >> 3) * KS + lane % KS) * 32 + (r & 7) * 4 + lane / KS) * 16) =
                     make_uint4(bits(h0), bits(h1), bits(l0), bits(l1));
             if (lane == 0)
                 *reinterpret_cast<float2*>(sm + L::info + r * 8) =
-                    make_float2(0.5f * sum, __uint_as_float((uint32_t)(127 + e) << 23) * (!low && yr > 0.0f ? yy / yr : 1.0f));
+                    make_float2(0.5f * sum, __uint_as_float((uint32_t)(127 + e) << 23));
         }
         __syncthreads();
         float off[NR][2], mul[NR][2];  // of this lane's rows 8 n + 2 qi + h
@@ -374,30 +360,25 @@ pages4_rows_kernel(const PagedAttend4 p4) {
                     w[y][0] = v.x, w[y][1] = v.y;
                 }
             }
-            auto products = [&](auto low) {
 #pragma unroll
-                for (int j = 0; j < 2 * W; ++j) {  // a step: four channels of each lane, half a word
-                    uint32_t a[4], a16[4];
+            for (int j = 0; j < 2 * W; ++j) {  // a step: four channels of each lane, half a word
+                uint32_t a[4], a16[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        if (j & 1) w[y][j / 2] >>= 8;
-                        a[y] = half_centred(w[y][j / 2], 0x000F000Fu, 0xE408E408u);    // u - 8
-                        a16[y] = half_centred(w[y][j / 2], 0x00F000F0u, 0xE480E480u);  // 16 (u - 8)
-                    }
+                for (int y = 0; y < 4; ++y) {
+                    if (j & 1) w[y][j / 2] >>= 8;
+                    a[y] = half_centred(w[y][j / 2], 0x000F000Fu, 0xE408E408u);    // u - 8
+                    a16[y] = half_centred(w[y][j / 2], 0x00F000F0u, 0xE480E480u);  // 16 (u - 8)
+                }
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        const uint4 q = qs[(n * KS + j) * 32];
+                for (int n = 0; n < NR; ++n) {
+                    const uint4 q = qs[(n * KS + j) * 32];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            mma_f16(c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.x, q.y);
-                            if constexpr (decltype(low)::value)
-                                mma_f16(c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.z, q.w);
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        mma_f16(c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.x, q.y);
+                        mma_f16(c[n][i], a[2 * i], a[2 * i + 1], a16[2 * i], a16[2 * i + 1], q.z, q.w);
                     }
                 }
-            };
-            if (low) products(std::true_type());
-            else products(std::false_type());
+            }
             // ---- weights
             float tk[4], tv[4];  // keys t0 + quad + 8 i
 #pragma unroll
