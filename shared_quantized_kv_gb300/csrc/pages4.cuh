@@ -128,6 +128,14 @@ __device__ __noinline__ void careful_row4(const PagedAttend4& p4, int seq, int t
     float q[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) q[e] = bf2f(a.Q[(long long)tok * a.q_stride + (long long)head * D + lane * E + e]);
+    // a power of two brings the row's largest value into [1/2, 1), so that neither H q nor its products overflow
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(fabsf(q[e])));
+    const int e2 = min(max((int)(__reduce_max_sync(0xffffffffu, top) >> 23) - 126, -126), 126);
+    const float down = __uint_as_float((uint32_t)(127 - e2) << 23), up = __uint_as_float((uint32_t)(127 + e2) << 23);
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[e] *= down;
     transform_row<D>(q);
     m = -CUDART_INF_F;
     l = 0.0f;
@@ -153,7 +161,7 @@ __device__ __noinline__ void careful_row4(const PagedAttend4& p4, int seq, int t
         for (int e = 0; e < E; ++e) dot = fmaf(q[e], level(kw, e), dot);
 #pragma unroll
         for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float x = score<SCORED>(a, dot * tk, slope2, pos, j);
+        const float x = score<SCORED>(a, dot * (tk * up), slope2, pos, j);
         const float mn = fmaxf(m, x), ref = mn == -CUDART_INF_F ? 0.0f : mn;
         const float c = l == 0.0f ? 0.0f : ptx::ex2(m - ref), w = ptx::ex2(x - ref);
         l = l == 0.0f ? w : fmaf(l, c, w);

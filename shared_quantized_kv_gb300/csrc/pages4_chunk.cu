@@ -84,13 +84,16 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < CUDART_INF_F
 
 // What the softmax needs to know of a tile's scales, beside the ring: a slot per tile
 // (where V's is not finite: 0, and K's NaN. A row that sees the key then has a sum that is NaN and is done again key by
-// key; for others, whose weight of it is 0, nothing has to be looked at.)
+// key; for others, whose weight of it is 0, nothing has to be looked at. The same where K's scale is so
+// large that it may overflow times the sum of a row's values, up to 16, and the key's whole numbers, 2^18 at most,
+// although the row's factor would bring the score back.)
+constexpr float kMostScale = 0x1p108f;
 struct TileScales {
     float v[kTile];
     float k[kTile];
     __device__ __forceinline__ void set(int key, float tk, float tv) {
         v[key] = finite(tv) ? tv : 0.0f;
-        k[key] = finite(tv) ? tk : CUDART_NAN_F;
+        k[key] = finite(tv) && fabsf(tk) <= kMostScale ? tk : CUDART_NAN_F;
     }
 };
 // A tile in the workspace, as shared memory takes it: K, V, the scales.

@@ -398,8 +398,9 @@ pages4_rows_kernel(const PagedAttend4 p4) {
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         const float t = tk[2 * i + (e >> 1)];
-                        const float2 x = __fmul2_rn(__fmul2_rn(make_float2(c[n][i][e], c[n][i][e + 1]), make_float2(mul[n][0], mul[n][1])),
-                                                    make_float2(t, t));
+                        // (the row's power of two meets the key's scale first: products overflow only where scores do)
+                        const float2 f = __fmul2_rn(make_float2(mul[n][0], mul[n][1]), make_float2(t, t));
+                        const float2 x = __fmul2_rn(make_float2(c[n][i][e], c[n][i][e + 1]), f);
                         c[n][i][e] = x.x, c[n][i][e + 1] = x.y;
                     }
 #pragma unroll
