@@ -449,9 +449,9 @@ pages4_rows_kernel(const PagedAttend4 p4) {
                         const float2 w = make_float2(ptx::ex2(d.x), ptx::ex2(d.y));
                         sum = __fadd2_rn(sum, w);
                         float2 v = __fmul2_rn(w, make_float2(t, t));
-                        if (!whole) {  // what a masked place's scale holds has no say
-                            v.x = w.x == 0.0f ? 0.0f : v.x;
-                            v.y = w.y == 0.0f ? 0.0f : v.y;
+                        if (!whole) {  // what a masked place's scale holds has no say (a seen one's does, at any weight)
+                            v.x = c[n][i][e] == -CUDART_INF_F ? 0.0f : v.x;
+                            v.y = c[n][i][e + 1] == -CUDART_INF_F ? 0.0f : v.y;
                         }
                         pb[n][i][e >> 1] = transposed(pack_bf2(v.x, v.y));
                     }
