@@ -638,8 +638,8 @@ int kvpool_pages4_copy(const kvpool_pages4_t* pages, const int32_t* src, const i
  * its rotation, the same modifiers, outputs and errors). workspace: device
  * memory, 16-byte aligned, scratch, or NULL with 0 bytes. Chunks of many tokens
  * read each key many times; with a workspace its operand is made once per call
- * and kept there. It changes no result, and any size may be given: sequences
- * that it has no room for do without. Calls that overlap on the GPU must not
+ * and kept there. It changes neither results nor what *status records, and any
+ * size may be given: sequences that it has no room for do without. Calls that overlap on the GPU must not
  * share one. Allocates nothing. */
 int kvpool_pages4_attend(const kvpool_pages4_t* pages, int layer, const kvpool_seqs_t* seqs, const void* Q,
                          long long q_stride, int q_heads, const kvpool_score_t* score, void* out, float* lse,

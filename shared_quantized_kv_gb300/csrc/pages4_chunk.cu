@@ -281,8 +281,9 @@ __device__ __forceinline__ void expand_v(const unsigned char* own, unsigned char
 
 // An expander warp's share of every tile, 16 * BLOCKS keys from key0 on: where its
 // codes lie (a page holds 16 keys at least), and copies of them on their way into
-// the warp's own ring, 32 keys to an entry.
-template <int D, int BLOCKS>
+// the warp's own ring, 32 keys to an entry. RECORD: page numbers out of range go to
+// the status word.
+template <int D, int BLOCKS, bool RECORD = true>
 struct CodeReader {
     static constexpr int kTiles = 32 / BLOCKS;  // of one lookup, a lane per 16 keys
     static constexpr int kEntries = BLOCKS / 2, kDepth = BLOCKS == 2 ? kRawK : kRawV;
@@ -301,7 +302,7 @@ struct CodeReader {
         if (t >= T) return -1;
         const int page = __ldg(table + (t >> s.pshift));
         if (page < 0 || page >= s.pages) {
-            pages::flag(s.status, kPgBadPage);
+            if (RECORD) pages::flag(s.status, kPgBadPage);
             return -1;
         }
         return ((page * s.Hk + g) << s.pshift) + (t & ((1 << s.pshift) - 1));
@@ -610,8 +611,15 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
             __syncwarp();
         } else if constexpr (MADE) {
             // ------------------------------------------------------- loaders
-            // Warp 0: K and the scales, warp 3: V; a tile in one or two bulk copies.
+            // Warp 0: K and the scales, warp 3: V; a tile in one or two bulk copies. Warp 3 looks at
+            // the tile's table entries too, a lane per 16 keys: those out of range are recorded where a
+            // tile is read, not where it is made (more tiles are made than rows see). An
+            // entry is asked for after a tile's copies and looked at after the next one's.
             const bool v = warp == 3;
+            int page = 0;
+            auto look = [&] {
+                if (page < 0 || page >= s.pages) pages::flag(s.status, kPgBadPage);
+            };
             const unsigned char* tiles = made.tiles + ((long long)b.seq * s.Hk + g) * made.room * made_bytes<D>() + (v ? L::stage : 0);
             for (int i = 0; i < n; ++i) {
                 const int st = i % L::nst + (v ? L::nst : 0);
@@ -624,7 +632,13 @@ pages4_chunk_kernel(const PagedAttend4 p4, const Made made) {
                         ptx::bulk_g2s(ptx::smem_u32(tile_scales + i % L::slots), src + 2 * L::stage, sizeof(TileScales), b_full + 8 * st);
                 }
                 __syncwarp();
+                if (v) {
+                    look();
+                    const int t = tile_at(i) * kTile + 16 * lane;
+                    page = lane < kTile / 16 && t < T ? __ldg(s.table + (long long)b.seq * s.tstride + (t >> s.pshift)) : 0;
+                }
             }
+            look();
             // every requested tile has landed before the CTA may go on
             for (int i = max(0, n - L::nst); i < n; ++i) {
                 bool late = false;
@@ -1447,7 +1461,7 @@ pages4_make_kernel(const PagedAttend4 p4, const Made made) {
     const int len = pages::length_of(s, seq), T = pages::held_tokens(s, len);
     if (pages::row_begin(s, seq + 1) <= pages::row_begin(s, seq)) return;  // no rows, nobody reads it
     if (!made.has(T) || tile * kTile >= T) return;
-    CodeReader<D, 2> in(p, s, g, seq, T, 1, key0, lane, sm + kStage + sizeof(TileScales) + warp * kCodes);
+    CodeReader<D, 2, false> in(p, s, g, seq, T, 1, key0, lane, sm + kStage + sizeof(TileScales) + warp * kCodes);
     in.start([&](int) { return tile; });
     in.ask(values ? p.V : p.K, 0, 0);
     cp_commit();
