@@ -599,8 +599,9 @@ int kvpool_pages_append_rotary(const kvpool_pages_t* pages, int layer, const kvp
  * operations: x is scaled by the power of two that brings its largest value
  * into [1/2, 1) (exponents clamped to +-126); squares are added in neighbouring
  * pairs; y by the stages h = 1, 2, 4, ... (x_i + x_{i+h}, x_i - x_{i+h}); u from
- * y_i * (1 / step). A vector that holds an infinity or NaN stands for NaN;
- * scales that float32 holds with few bits only (vectors below 2^-100) keep few.
+ * y_i * (1 / step); t from step / d, times the power of two taken off. A vector
+ * that holds an infinity or NaN stands for NaN; scales that float32 holds with
+ * few bits only (vectors below 2^-100) keep few.
  * ------------------------------------------------------------------------- */
 typedef struct {
     void* K;          /* uint8 [layers][pages][kv_heads][page_tokens][head_dim / 2], device, 16-byte aligned: 32-bit

@@ -59,7 +59,7 @@ def encode(x):
             h *= 2
         u = np.clip(np.floor(y * (np.float32(1) / step)) + 8, 0, 15)
         u = np.where(step > 0, u, 8)
-        t = (step * np.ldexp(np.float32(1), e).astype(np.float32))[..., 0] * np.float32(1 / d)
+        t = (step * np.float32(1 / d) * np.ldexp(np.float32(1), e).astype(np.float32))[..., 0]
         bad = ~np.isfinite(x).all(-1)
     return np.nan_to_num(u).astype(np.uint8), np.where(bad, np.float32(np.nan), t).astype(np.float32)
 

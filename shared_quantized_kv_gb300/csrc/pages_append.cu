@@ -157,7 +157,7 @@ __device__ __forceinline__ void encode(float (&x0)[8], float (&x1)[8], uint32_t&
     if (!(step > 0.0f)) w0 = w1 = 0x88888888u;
     // a vector that holds an infinity or NaN stands for NaN
     t = top >= 0x7F800000u ? CUDART_NAN_F
-                           : __fmul_rn(__fmul_rn(step, __uint_as_float((uint32_t)(127 + e) << 23)), 1.0f / (16 * L));
+                           : __fmul_rn(__fmul_rn(step, 1.0f / (16 * L)), __uint_as_float((uint32_t)(127 + e) << 23));
 }
 
 // The token row `tok`: its sequence, position and, where the table has a page
