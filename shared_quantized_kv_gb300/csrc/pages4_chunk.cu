@@ -1447,6 +1447,7 @@ cudaError_t launch(const PagedAttend4& p4, const Made& made, int max_q, int max_
 // key and head of 128, 512 of them written: 4,096 keys of 8 heads of 19 sequences in 62
 // us, 6.6 TB/s (88 with K and V made by one CTA, two of which an SM has room for).
 constexpr int kMakeThreads = 128;
+constexpr int kMadeSeqs = 65535;  // a grid's third extent: more sequences go without a workspace
 template <int D>
 __global__ void __launch_bounds__(kMakeThreads)
 pages4_make_kernel(const PagedAttend4 p4, const Made made) {
@@ -1528,6 +1529,7 @@ cudaError_t launch_kind(const PagedAttend4& p4, const Made& made, int max_q, int
 
 // Bytes of a workspace with room for max_kv tokens of every sequence.
 long long pages4_chunk_ws_bytes(const PagedSeqs& s, int head_dim, int max_kv) {
+    if (s.seqs > kMadeSeqs) return 0;
     const long long tiles = (max_kv + kTile - 1) / kTile * (long long)s.Hk * s.seqs;
     return tiles * (head_dim == 64 ? made_bytes<64>() : made_bytes<128>());
 }
@@ -1544,7 +1546,7 @@ cudaError_t launch_pages4_chunk(const PagedAttend4& p4, int head_dim, int max_q,
     if (ws) {
         const long long each = (long long)a.s.seqs * a.s.Hk * (head_dim == 64 ? made_bytes<64>() : made_bytes<128>());
         made.room = (int)std::min<long long>((long long)ws_bytes / each, (max_kv + kTile - 1) / kTile);
-        if (a.s.seqs > 65535) made.room = 0;  // (a grid's third extent)
+        if (a.s.seqs > kMadeSeqs) made.room = 0;
     }
 #define KVP_PG4_CHUNK(KK) \
     (head_dim == 64 ? launch_kind<64, KK>(p4, made, max_q, max_kv, st) : launch_kind<128, KK>(p4, made, max_q, max_kv, st))
