@@ -26,8 +26,15 @@ int check_pages4(const kvpool_pages4_t* pg, int layer, kvpool_pages_t& v) {
 }
 
 // Blocks of 8 rows, each through all its keys, are the kernel's for few rows while
-// these are few: one sequence of 16K keys, 8 KV heads: 48 us against 56 with 64
-// rows per head, 79 against 57 with 128; of 2,048 keys and 256 rows 25 against 32.
+// these are few: one sequence of 16K keys, 8 KV heads of 128: 51 us against 56 with
+// 64 rows per head, 81 against 57 with 128; of 2,048 keys 24 against 25 with 256
+// rows, 52 against 28 with 640. 32 heads of 64, 8,192 keys: 30 against 35 with 32
+// rows, 37 against 35 with 40, 41 against 35 with 64. 2 heads of 64, 8,192 keys: 21
+// against 34 with 256, 40 against 33 with 1,024. 4 heads of 128 in groups of 7,
+// 20,011 keys: 31 against 65 with 56, 74 against 61 with 280. (Both kernels go by
+// keys and rows; channels hardly move the border. The lengths do, which the rule
+// leaves out: of 4 sequences of 2,048 keys and 128 rows the other kernel would take
+// 27 us, not 41; 16 of 8,192 keys and 24 rows would take 122 here, not 167.)
 constexpr double kRowsReads = 5 << 18;
 bool few_rows(const kvp::PagedAttend& a, int max_q, int max_kv) {
     const long long rows = (long long)max_q * a.G, blocks = a.s.seqs * ((rows + 7) / 8);

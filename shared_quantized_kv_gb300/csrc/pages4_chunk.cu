@@ -33,7 +33,7 @@
 // Every wait on a barrier in memory is bounded; one that expires is recorded in
 // the status word, and the CTA runs to its end without waiting again.
 //
-// Measured on 2,048 new tokens over 16K keys, 32 query heads on 8 of 128: 442 us
+// Measured on 2,048 new tokens over 16K keys, 32 query heads on 8 of 128: 443 us
 // with a workspace, 15 of them to make it (1.16 PFLOP/s; the bf16 pages take 352), 748
 // without. The scales cost most beside the products: a version without their
 // multiplications took 344 us. What got it there, without a workspace at first: one
@@ -219,52 +219,52 @@ template <int D>
 __device__ __forceinline__ void expand_k(const unsigned char* own, unsigned char* stage, int key0, const uint32_t (&h16)[2][2],
                                          uint32_t half_sum) {
     const int lane = threadIdx.x & 31, quad = lane >> 2, qi = lane & 3;
-                constexpr int kGroups = D / 16;
+    constexpr int kGroups = D / 16;
 #pragma unroll 1
-                for (int x = 0; x < 2; ++x) {  // keys 16 x + quad and + 8
-                    uint32_t z[2][kGroups][2];  // [key][group][half of its channels]
+    for (int x = 0; x < 2; ++x) {  // keys 16 x + quad and + 8
+        uint32_t z[2][kGroups][2];  // [key][group][half of its channels]
 #pragma unroll
-                    for (int g2 = 0; g2 < kGroups / 2; ++g2) {  // two groups: four words
-                        uint4 w[2];
+        for (int g2 = 0; g2 < kGroups / 2; ++g2) {  // two groups: four words
+            uint4 w[2];
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            w[y] = *reinterpret_cast<const uint4*>(own + (16 * x + 8 * y + quad) * (D / 2) + g2 * 16);
-                        const int sh = 4 * qi;
-                        const uint32_t a0 = k_pair(w[0].x >> sh), a1 = k_pair(w[1].x >> sh);
-                        const uint32_t a2 = k_pair(w[0].y >> sh), a3 = k_pair(w[1].y >> sh);
-                        const uint32_t c0 = k_pair(w[0].z >> sh), c1 = k_pair(w[1].z >> sh);
-                        const uint32_t c2 = k_pair(w[0].w >> sh), c3 = k_pair(w[1].w >> sh);
+            for (int y = 0; y < 2; ++y)
+                w[y] = *reinterpret_cast<const uint4*>(own + (16 * x + 8 * y + quad) * (D / 2) + g2 * 16);
+            const int sh = 4 * qi;
+            const uint32_t a0 = k_pair(w[0].x >> sh), a1 = k_pair(w[1].x >> sh);
+            const uint32_t a2 = k_pair(w[0].y >> sh), a3 = k_pair(w[1].y >> sh);
+            const uint32_t c0 = k_pair(w[0].z >> sh), c1 = k_pair(w[1].z >> sh);
+            const uint32_t c2 = k_pair(w[0].w >> sh), c3 = k_pair(w[1].w >> sh);
 #pragma unroll
-                        for (int nb = 0; nb < 2; ++nb) {
-                            mma_half(z[0][2 * g2][nb], z[1][2 * g2][nb], a0, a1, a2, a3, h16[nb][0], h16[nb][1]);
-                            mma_half(z[0][2 * g2 + 1][nb], z[1][2 * g2 + 1][nb], c0, c1, c2, c3, h16[nb][0], h16[nb][1]);
+            for (int nb = 0; nb < 2; ++nb) {
+                mma_half(z[0][2 * g2][nb], z[1][2 * g2][nb], a0, a1, a2, a3, h16[nb][0], h16[nb][1]);
+                mma_half(z[0][2 * g2 + 1][nb], z[1][2 * g2 + 1][nb], c0, c1, c2, c3, h16[nb][0], h16[nb][1]);
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int h = 1; h < kGroups; h <<= 1)
+#pragma unroll
+                    for (int q = 0; q < kGroups; ++q)
+                        if (!(q & h)) {
+                            const uint32_t a = z[y][q][nb], c = z[y][q + h][nb];
+                            z[y][q][nb] = hadd2(a, c), z[y][q + h][nb] = hsub2(a, c);
                         }
-                    }
+            z[y][0][0] = hadd2(z[y][0][0], half_sum);
+            // channels 16 q + 8 nb + 2 qi and the next: 4 bytes of piece 2 q + nb
+            const int key = key0 + 16 * x + 8 * y + quad;  // (key & 7 is quad)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
+            for (int q = 0; q < kGroups; ++q)
 #pragma unroll
-                        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                            for (int h = 1; h < kGroups; h <<= 1)
-#pragma unroll
-                                for (int q = 0; q < kGroups; ++q)
-                                    if (!(q & h)) {
-                                        const uint32_t a = z[y][q][nb], c = z[y][q + h][nb];
-                                        z[y][q][nb] = hadd2(a, c), z[y][q + h][nb] = hsub2(a, c);
-                                    }
-                        z[y][0][0] = hadd2(z[y][0][0], half_sum);
-                        // channels 16 q + 8 nb + 2 qi and the next: 4 bytes of piece 2 q + nb
-                        const int key = key0 + 16 * x + 8 * y + quad;  // (key & 7 is quad)
-#pragma unroll
-                        for (int q = 0; q < kGroups; ++q)
-#pragma unroll
-                            for (int nb = 0; nb < 2; ++nb) {
-                                const int pc = 2 * q + nb;
-                                *reinterpret_cast<uint32_t*>(stage + (pc / 8) * (kTile * 128) + key * 128 +
-                                                             (((pc % 8) ^ quad) << 4) + 4 * qi) = z[y][q][nb];
-                            }
-                    }
+                for (int nb = 0; nb < 2; ++nb) {
+                    const int pc = 2 * q + nb;
+                    *reinterpret_cast<uint32_t*>(stage + (pc / 8) * (kTile * 128) + key * 128 +
+                                                 (((pc % 8) ^ quad) << 4) + 4 * qi) = z[y][q][nb];
                 }
+        }
+    }
 }
 // The same of V: u - 7.5 as they are. D / 8 lanes take a key, a word each, which becomes 16 bytes of its row.
 template <int D>

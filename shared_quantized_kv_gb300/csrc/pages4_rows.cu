@@ -12,10 +12,10 @@
 // part alone, off by 2^-11, leaves the log of the sum 1e-6 off (relative) where
 // 16K keys weigh alike, but 1e-4 where a window, a document or a peaked row leaves
 // few keys that count, at any length; the second costs 32 sequences of 32K keys
-// 7 %. Codes enter the
-// products exactly: of Q K^T as fp16 u - 8 or 16 (u - 8) (one mask and one
-// addition; the sixteenth is in that channel's H q, the other half of a step is
-// the product's first summand), of P V as bf16 u - 7.5.
+// 8 % (250 us against 230). With both the log of the sum is within 3e-7 of its size
+// in all of these. Codes enter the products exactly: of Q K^T as fp16 u - 8 or 16
+// (u - 8) (one mask and one addition; the sixteenth is in that channel's H q, the
+// other half of a step is the product's first summand), of P V as bf16 u - 7.5.
 //
 // Bound: memory, as a step reads D + 8 bytes per key and KV head, and before it the
 // instructions that make operands of codes, so the layout serves these. The keys
@@ -30,16 +30,16 @@
 // the end, those of a cluster's CTAs, which split the keys, in distributed shared
 // memory: no workspace, no second launch.
 //
-// Measured: 32 sequences of 32K keys, 64 query heads on 8 of 128: 233 us, 4.7 TB/s
+// Measured: 32 sequences of 32K keys, 64 query heads on 8 of 128: 250 us, 4.4 TB/s
 // of 6.8 (the bf16 pages, 3.8 times the bytes, take 570); without its loads the
-// kernel takes 13 us less, without what takes V's codes apart 56, without the
-// matrix instructions of Q K^T 79 (by a version of 291 us): a mixture of the
+// kernel takes 40 us less, without what takes V's codes apart 51, without the
+// matrix instructions of Q K^T 75, with one fp16 part of H q 19: a mixture of the
 // half-rate integer pipe, the matrix instructions' chains and the issue slots. 5
-// tokens of one sequence of 20,011 keys, 28 heads on 4: 25 us, of which a start of
-// 1.6 us and a cluster's merge of 3.5 are fixed. Not kept: 5 or 6 CTAs per SM with
-// two units in a ring (315, 376 us against 294), 3 with four (325), blocks of 32
-// rows (spills; 43 us against 25 on those 5 tokens), CTAs of 8 warps, shifts by
-// multiplication (326 against 301).
+// tokens of one sequence of 20,011 keys, 28 heads on 4: 26 us, of which a start of
+// 1.6 us and a cluster's merge of 3.5 are fixed. Not kept (each against the version
+// of its time): 5 or 6 CTAs per SM with two units in a ring (315, 376 us against
+// 294), 3 with four (325), blocks of 32 rows (spills; 43 us against 25 on those 5
+// tokens), CTAs of 8 warps, shifts by multiplication (326 against 301).
 #include <algorithm>
 #include <mutex>
 
@@ -622,8 +622,8 @@ cudaError_t launch_rows(const PagedAttend4& p, int max_q, int max_kv, int sm_cou
     // Keys split over a cluster, every warp with two units at least, so that the
     // fullest SM has least to do: its CTAs' units, and for every wave of CTAs a start
     // and an end that take about as long as kWave units of an SM (32 sequences of 32K
-    // keys, 8 KV heads: 270 us in 2, one wave of 512 CTAs on 152 SMs, 233 in 4; 15 of
-    // 4,096 keys: 29 us in 5, 35 in 10).
+    // keys, 8 KV heads: 292 us in 2, one wave of 512 CTAs on 152 SMs, 256 in 4; 15 of
+    // 4,096 keys: 28 us in 5, 33 in 10, though 24 in 4, which this does not tell apart).
     const long long jobs = std::max(1LL, std::min(blocks, a.s.seqs * (((long long)max_q * a.G + kRows - 1) / kRows)) * a.s.Hk);
     const long long units = std::max(1, (max_kv + kUnit - 1) / kUnit), most = std::min(kMaxSplit, max_kv / (2 * kWarps * kUnit));
     long long split = 1, best = LLONG_MAX;
@@ -647,8 +647,8 @@ cudaError_t launch_pages4_rows(const PagedAttend4& a, int head_dim, int max_q, i
                                cudaStream_t st) {
     // Blocks of 8 rows fill the GPU sooner and take less time to start; blocks of 16
     // take the codes apart half as often, which pays where there are many units of
-    // keys (32 sequences of 16K keys, 16 rows: 233 us against 297; 8 of 4,096: 32
-    // against 26).
+    // keys (32 sequences of 16K keys, 16 rows: 206 us against 251, of 4,096 66 against
+    // 77; 8 of 4,096: 32 against 25).
     const long long rows = (long long)max_q * a.a.G;
     const bool two = rows > 8 && (double)a.a.s.seqs * ((rows + 15) / 16) * a.a.s.Hk * max_kv >= (double)(1 << 20);
 #define KVP_PG4_ROWS(DD) \
